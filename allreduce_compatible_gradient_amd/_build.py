@@ -1,4 +1,5 @@
-"""Build step of libgq.so: one hipcc invocation for gfx950 (MI355X)."""
+"""Build step of libgq.so and its companions: one hipcc invocation each for
+gfx950 (MI355X)."""
 from __future__ import annotations
 
 import os
@@ -8,6 +9,9 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", "gq.hip")]
 LIB_PATH = os.path.join(PKG, "libgq.so")
+# the training operators (include/gq_train.h), a library of their own
+TRAIN_SOURCES = [os.path.join(PKG, "csrc", f) for f in ("train.hip", "weight_grad.hip")]
+TRAIN_LIB_PATH = os.path.join(PKG, "libgq_train.so")
 # measurement kernels (read and VALU-issue ceilings), a library of their own
 PROBE_SOURCES = [os.path.join(PKG, "csrc", "probe.hip")]
 PROBE_LIB_PATH = os.path.join(PKG, "libgq_probe.so")
@@ -50,10 +54,15 @@ def build_library(verbose: bool = False, sources=None, lib_path: str = LIB_PATH)
     return lib_path
 
 
+def build_train(verbose: bool = False) -> str:
+    return build_library(verbose, TRAIN_SOURCES, TRAIN_LIB_PATH)
+
+
 def build_probe(verbose: bool = False) -> str:
     return build_library(verbose, PROBE_SOURCES, PROBE_LIB_PATH)
 
 
 if __name__ == "__main__":
     print(build_library(verbose=True))
+    print(build_train(verbose=True))
     print(build_probe(verbose=True))

@@ -1,0 +1,1014 @@
+// train.hip -- layer norm, GELU and the 8-bit activation copies on MI355X
+// (gfx950): the operators of include/gq_train.h that are bound by memory.
+//
+// Every kernel reads its inputs once and writes its outputs once, eight
+// columns (one 16-byte bf16 load) per lane and step, so that four lanes hold
+// one 32-column group of the 8-bit format and one Philox call serves a
+// lane's eight roundings.
+#include "train_common.h"
+
+#include <stdarg.h>
+#include <stdio.h>
+
+namespace gqt {
+
+thread_local char g_err[512];
+
+int32_t fail(int32_t status, const char *fmt, ...)
+{
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return status;
+}
+
+int32_t ok()
+{
+    g_err[0] = 0;
+    return GQ_OK;
+}
+
+int32_t check_launch(const char *kernel)
+{
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return fail(GQ_ERR_DEVICE, "%s: %s", kernel, hipGetErrorString(e));
+    return ok();
+}
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Layer norm
+//
+// TPR threads hold one row, C chunks of eight columns each (chunk c of lane t
+// at column 8 (c TPR + t)), so the row is read once and its mean and the sum
+// of squared deviations from it (no cancellation, whatever the mean) are
+// taken in registers.  Rows beyond 16384 columns are read three times by
+// k_layer_norm_long, from the cache after the first.
+
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float *lds)
+{
+#pragma unroll
+    for (int o = 1; o < (TPR < 64 ? TPR : 64); o <<= 1)
+        v += __shfl_xor(v, o);
+    if (TPR > 64) {
+        // one slot per wave; the leading barrier frees the previous sum's slots
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0)
+            lds[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < TPR / 64; ++w)
+            v += lds[w];
+    }
+    return v;
+}
+
+__device__ __forceinline__ void load_weight8(const void *w, int32_t wdtype, int32_t col, int n,
+                                             float (&v)[8])
+{
+    if (wdtype == GQ_IN_F32)
+        load8(static_cast<const float *>(w) + col, n, v);
+    else
+        load8(static_cast<const bf16 *>(w) + col, n, v);
+}
+
+template <int TPR>
+constexpr int block_threads()
+{
+    return TPR > 256 ? TPR : 256;
+}
+
+template <typename T, int TPR, int C, bool KEEP>
+__global__ __launch_bounds__(block_threads<TPR>()) void k_layer_norm(
+    const T *__restrict__ x, int64_t rows, int32_t d, int64_t ldx, const void *__restrict__ w,
+    const void *__restrict__ b, int32_t wdtype, float eps, T *__restrict__ y,
+    float *__restrict__ mean_out, float *__restrict__ rstd_out, Act8 keep_x, Act8 keep_y)
+{
+    constexpr int kRows = block_threads<TPR>() / TPR;
+    __shared__ float lds[TPR > 64 ? TPR / 64 : 1];
+    const int t = threadIdx.x % TPR;
+    float wv[C][8], bv[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int col = 8 * (c * TPR + t);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            wv[c][k] = 1.0f;
+            bv[c][k] = 0.0f;
+        }
+        if (w && col < d)
+            load_weight8(w, wdtype, col, d - col, wv[c]);
+        if (b && col < d)
+            load_weight8(b, wdtype, col, d - col, bv[c]);
+    }
+    for (int64_t base = (int64_t)blockIdx.x * kRows; base < rows;
+         base += (int64_t)gridDim.x * kRows) {
+        const int64_t row = base + threadIdx.x / TPR;
+        if (TPR <= 64 && row >= rows)
+            break; // whole rows of lanes leave; no barrier follows for TPR <= 64
+        float v[C][8];
+        float s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = 8 * (c * TPR + t);
+            load8(x + row * ldx + (col < d ? col : 0), d - col, v[c]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                s += v[c][k];
+        }
+        const float mean = row_sum<TPR>(s, lds) / (float)d;
+        s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = 8 * (c * TPR + t);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float u = v[c][k] - mean;
+                s = fmaf(col + k < d ? u : 0.0f, u, s);
+            }
+        }
+        const float rstd = 1.0f / sqrtf(row_sum<TPR>(s, lds) / (float)d + eps);
+        if (t == 0) {
+            if (mean_out)
+                mean_out[row] = mean;
+            if (rstd_out)
+                rstd_out[row] = rstd;
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = 8 * (c * TPR + t);
+            if (KEEP && keep_x.keep != kKeepNone)
+                keep8(keep_x, row, col, v[c]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[c][k] = fmaf((v[c][k] - mean) * rstd, wv[c][k], bv[c][k]);
+            if (col < d)
+                store8(y + row * d + col, d - col, v[c]);
+            if (KEEP && keep_y.keep != kKeepNone) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (col + k >= d)
+                        v[c][k] = 0.0f;
+                keep8(keep_y, row, col, v[c]);
+            }
+        }
+    }
+}
+
+constexpr int kLongThreads = 1024;
+
+template <typename T>
+__global__ __launch_bounds__(kLongThreads) void k_layer_norm_long(
+    const T *__restrict__ x, int64_t rows, int32_t d, int64_t ldx, const void *__restrict__ w,
+    const void *__restrict__ b, int32_t wdtype, float eps, T *__restrict__ y,
+    float *__restrict__ mean_out, float *__restrict__ rstd_out, Act8 keep_x, Act8 keep_y)
+{
+    __shared__ float lds[kLongThreads / 64];
+    // columns rounded up to whole groups, so that quads stay whole
+    const int64_t cols = ((int64_t)d + 31) / 32 * 32;
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+        const T *xr = x + row * ldx;
+        float s = 0.0f;
+        for (int64_t col = 8 * threadIdx.x; col < d; col += 8 * kLongThreads) {
+            float v[8];
+            load8(xr + col, (int)(d - col), v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                s += v[k];
+        }
+        const float mean = row_sum<kLongThreads>(s, lds) / (float)d;
+        s = 0.0f;
+        for (int64_t col = 8 * threadIdx.x; col < d; col += 8 * kLongThreads) {
+            float v[8];
+            load8(xr + col, (int)(d - col), v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float u = v[k] - mean;
+                s = fmaf(col + k < d ? u : 0.0f, u, s);
+            }
+        }
+        const float rstd = 1.0f / sqrtf(row_sum<kLongThreads>(s, lds) / (float)d + eps);
+        if (threadIdx.x == 0) {
+            if (mean_out)
+                mean_out[row] = mean;
+            if (rstd_out)
+                rstd_out[row] = rstd;
+        }
+        for (int64_t col = 8 * threadIdx.x; col < cols; col += 8 * kLongThreads) {
+            float v[8], wv[8], bv[8];
+            const int n = (int)(d - col);
+            load8(xr + (n > 0 ? col : 0), n, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                wv[k] = 1.0f;
+                bv[k] = 0.0f;
+            }
+            if (w && n > 0)
+                load_weight8(w, wdtype, (int32_t)col, n, wv);
+            if (b && n > 0)
+                load_weight8(b, wdtype, (int32_t)col, n, bv);
+            if (keep_x.keep != kKeepNone)
+                keep8(keep_x, row, (int32_t)col, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = fmaf((v[k] - mean) * rstd, wv[k], bv[k]);
+            if (n > 0)
+                store8(y + row * d + col, n, v);
+            if (keep_y.keep != kKeepNone) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k >= n)
+                        v[k] = 0.0f;
+                keep8(keep_y, row, (int32_t)col, v);
+            }
+        }
+    }
+}
+
+// One row's dx from its dy (g = dy w) and xh, given the two row means.
+// The gradient kernels accumulate dw and db per thread over the rows of a
+// block in a fixed order; partial[block][2][d] is reduced by k_sum_partials.
+template <typename T, int TPR, int C, bool ACT8>
+__global__ __launch_bounds__(block_threads<TPR>()) void k_layer_norm_backward(
+    const T *__restrict__ dy, int64_t rows, int32_t d, int64_t lddy, const T *__restrict__ x,
+    int64_t ldx, Act8 x8, const float *__restrict__ mean_in, const float *__restrict__ rstd_in,
+    const void *__restrict__ w, int32_t wdtype, T *__restrict__ dx, float *__restrict__ partial)
+{
+    constexpr int kRows = block_threads<TPR>() / TPR;
+    __shared__ float lds[TPR > 64 ? TPR / 64 : 1];
+    __shared__ float sums[kRows > 1 ? kRows * TPR * C * 8 : 1];
+    const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+    float wv[C][8], aw[C][8], ab[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int col = 8 * (c * TPR + t);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            wv[c][k] = 1.0f;
+            aw[c][k] = ab[c][k] = 0.0f;
+        }
+        if (w && col < d)
+            load_weight8(w, wdtype, col, d - col, wv[c]);
+    }
+    const float inv_d = 1.0f / (float)d;
+    for (int64_t base = (int64_t)blockIdx.x * kRows; base < rows;
+         base += (int64_t)gridDim.x * kRows) {
+        const int64_t row = base + slot;
+        if (TPR <= 64 && row >= rows)
+            break;
+        const float mean = mean_in[row], rstd = rstd_in[row];
+        float g[C][8], xh[C][8];
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = 8 * (c * TPR + t);
+            const int n = d - col;
+            load8(dy + row * lddy + (n > 0 ? col : 0), n, g[c]);
+            if (ACT8) {
+                if (n > 0)
+                    restore8(x8, row, col, xh[c]);
+                else
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        xh[c][k] = 0.0f;
+            } else {
+                load8(x + row * ldx + (n > 0 ? col : 0), n, xh[c]);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                // columns past d contribute nothing, even where the
+                // statistics or the copy's padding hold a NaN
+                xh[c][k] = k < n ? (xh[c][k] - mean) * rstd : 0.0f;
+                aw[c][k] = fmaf(g[c][k], xh[c][k], aw[c][k]);
+                ab[c][k] += g[c][k];
+                g[c][k] *= wv[c][k];
+                s1 += g[c][k];
+                s2 = fmaf(g[c][k], xh[c][k], s2);
+            }
+        }
+        s1 = row_sum<TPR>(s1, lds) * inv_d;
+        s2 = row_sum<TPR>(s2, lds) * inv_d;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = 8 * (c * TPR + t);
+            if (col >= d)
+                continue;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                g[c][k] = rstd * (g[c][k] - s1 - xh[c][k] * s2);
+            store8(dx + row * d + col, d - col, g[c]);
+        }
+    }
+    if (!partial)
+        return;
+    float *out = partial + (int64_t)blockIdx.x * 2 * d;
+    if (kRows == 1) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = 8 * (c * TPR + t);
+            if (col < d) {
+                store8(out + col, d - col, aw[c]);
+                store8(out + d + col, d - col, ab[c]);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                sums[(slot * C + c) * TPR * 8 + 8 * t + k] = which ? ab[c][k] : aw[c][k];
+        __syncthreads();
+        for (int col = threadIdx.x; col < d; col += block_threads<TPR>()) {
+            float s = 0.0f;
+            for (int r = 0; r < kRows; ++r)
+                s += sums[r * C * TPR * 8 + col];
+            out[which * d + col] = s;
+        }
+    }
+}
+
+template <typename T, bool ACT8>
+__global__ __launch_bounds__(kLongThreads) void k_layer_norm_backward_long(
+    const T *__restrict__ dy, int64_t rows, int32_t d, int64_t lddy, const T *__restrict__ x,
+    int64_t ldx, Act8 x8, const float *__restrict__ mean_in, const float *__restrict__ rstd_in,
+    const void *__restrict__ w, int32_t wdtype, T *__restrict__ dx, float *__restrict__ partial)
+{
+    __shared__ float lds[kLongThreads / 64];
+    const float inv_d = 1.0f / (float)d;
+    float *out = partial ? partial + (int64_t)blockIdx.x * 2 * d : nullptr;
+    bool first = true; // the block's partial sums live in its own slice of the workspace
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, first = false) {
+        const float mean = mean_in[row], rstd = rstd_in[row];
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int pass = 0; pass < 2; ++pass) {
+            for (int64_t col = 8 * threadIdx.x; col < d; col += 8 * kLongThreads) {
+                const int n = (int)(d - col);
+                float g[8], xh[8], wv[8];
+                load8(dy + row * lddy + col, n, g);
+                if (ACT8)
+                    restore8(x8, row, (int32_t)col, xh);
+                else
+                    load8(x + row * ldx + col, n, xh);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    wv[k] = 1.0f;
+                    xh[k] = k < n ? (xh[k] - mean) * rstd : 0.0f;
+                }
+                if (w)
+                    load_weight8(w, wdtype, (int32_t)col, n, wv);
+                if (pass == 0) {
+                    if (out) {
+                        float a[8], b[8];
+                        load8(out + col, first ? 0 : n, a);
+                        load8(out + d + col, first ? 0 : n, b);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            a[k] = fmaf(g[k], xh[k], a[k]);
+                            b[k] += g[k];
+                        }
+                        store8(out + col, n, a);
+                        store8(out + d + col, n, b);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        s1 = fmaf(g[k], wv[k], s1);
+                        s2 = fmaf(g[k] * wv[k], xh[k], s2);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        g[k] = rstd * (g[k] * wv[k] - s1 - xh[k] * s2);
+                    store8(dx + row * d + col, n, g);
+                }
+            }
+            if (pass == 0) {
+                s1 = row_sum<kLongThreads>(s1, lds) * inv_d;
+                s2 = row_sum<kLongThreads>(s2, lds) * inv_d;
+            }
+        }
+    }
+}
+
+// dw and db: the blocks' partial sums added in block order, four waves a
+// quarter of the blocks each.  Column blocks along x, dw / db along y.
+__global__ __launch_bounds__(256) void k_sum_partials(const float *__restrict__ partial,
+                                                      int32_t blocks, int32_t d,
+                                                      void *__restrict__ dw,
+                                                      void *__restrict__ db, int32_t wdtype)
+{
+    __shared__ float part[4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t col = (int64_t)blockIdx.x * 64 + lane;
+    void *out = blockIdx.y ? db : dw;
+    if (!out)
+        return;
+    float s = 0.0f;
+    if (col < d) {
+        const float *p = partial + (int64_t)blockIdx.y * d + col;
+        const int lo = (int)((int64_t)blocks * wave / 4), hi = (int)((int64_t)blocks * (wave + 1) / 4);
+        for (int i = lo; i < hi; ++i)
+            s += p[(int64_t)i * 2 * d];
+    }
+    part[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && col < d) {
+        s = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+        if (wdtype == GQ_IN_F32)
+            static_cast<float *>(out)[col] = s;
+        else
+            static_cast<bf16 *>(out)[col] = (bf16)s;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Elementwise operators: one thread per 8 columns, rows padded to whole groups
+
+// Division of a 31-bit number by an invariant one: q = n m >> s.
+struct FastDiv {
+    uint32_t d, m, s;
+};
+inline FastDiv fast_div(uint32_t d)
+{
+    FastDiv f{d, 0, 31};
+    while (((uint64_t)1 << (f.s - 31)) < d)
+        ++f.s;
+    f.m = (uint32_t)((((uint64_t)1 << f.s) / d) + 1);
+    return f;
+}
+__device__ __forceinline__ uint32_t divide(uint32_t n, const FastDiv &f)
+{
+    return (uint32_t)(((uint64_t)n * f.m) >> f.s);
+}
+
+// The chunk of this thread; chunks = rows * (4 G).
+struct Chunk {
+    int64_t row;
+    int32_t col;
+};
+__device__ __forceinline__ Chunk chunk_at(uint32_t i, const FastDiv &per_row)
+{
+    const uint32_t row = divide(i, per_row);
+    return {(int64_t)row, (int32_t)((i - row * per_row.d) * 8)};
+}
+
+constexpr int kThreads = 256;
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_act8_save(const T *__restrict__ x, uint32_t chunks,
+                                                        FastDiv per_row, int32_t d, int64_t ldx,
+                                                        Act8 out)
+{
+    const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
+    if (i >= chunks)
+        return;
+    const Chunk c = chunk_at(i, per_row);
+    const int n = d - c.col;
+    float v[8];
+    load8(x + c.row * ldx + (n > 0 ? c.col : 0), n, v);
+    keep8(out, c.row, c.col, v);
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_act8_restore(Act8 in, uint32_t chunks,
+                                                           FastDiv per_row, int32_t d,
+                                                           T *__restrict__ out)
+{
+    const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
+    if (i >= chunks)
+        return;
+    const Chunk c = chunk_at(i, per_row);
+    if (c.col >= d)
+        return;
+    float v[8];
+    restore8(in, c.row, c.col, v);
+    store8(out + c.row * d + c.col, d - c.col, v);
+}
+
+// Phi(-z) e^(z^2 / 2) for z >= 0, as t p(t) with t = 1 / (1 + 0.32 z) and p of
+// degree 9 fitted (minimax, relative error 3.2e-8; 1.4e-7 evaluated in fp32)
+// to the scaled complementary error function.  1 - erf would lose the tail.
+__device__ __forceinline__ float scaled_tail(float z)
+{
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.32f, z, 1.0f));
+    float p = -0.021078171208500862f;
+    p = fmaf(p, t, 0.09540726244449615f);
+    p = fmaf(p, t, -0.1467074602842331f);
+    p = fmaf(p, t, 0.06532800942659378f);
+    p = fmaf(p, t, -0.009377559646964073f);
+    p = fmaf(p, t, 0.05865396186709404f);
+    p = fmaf(p, t, 0.0878290981054306f);
+    p = fmaf(p, t, 0.11462236195802689f);
+    p = fmaf(p, t, 0.12766094505786896f);
+    p = fmaf(p, t, 0.12766152620315552f);
+    return p * t;
+}
+
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+constexpr float kTanhC = 0.79788456080286536f; // sqrt(2 / pi)
+constexpr float kTanhA = 0.044715f;
+
+// The tanh form's logistic function s = s(2 u) and its complement 1 - s, both
+// from e^-|2u|, so that neither is the difference of near numbers.
+struct Gate {
+    float s, c;
+};
+__device__ __forceinline__ Gate tanh_gate(float h)
+{
+    const float u = kTanhC * h * fmaf(kTanhA * h, h, 1.0f);
+    const float e = expf(-2.0f * fabsf(u));
+    const float big = __builtin_amdgcn_rcpf(1.0f + e);
+    const float small = e * big;
+    return h < 0.0f ? Gate{small, big} : Gate{big, small};
+}
+
+template <int FORM>
+__device__ __forceinline__ float gelu(float h)
+{
+    if (FORM == GQT_GELU_TANH)
+        return h * tanh_gate(h).s;
+    const float tail = scaled_tail(fabsf(h)) * expf(-0.5f * h * h);
+    return h * (h < 0.0f ? tail : 1.0f - tail);
+}
+
+template <int FORM>
+__device__ __forceinline__ float gelu_slope(float h)
+{
+    if (FORM == GQT_GELU_TANH) {
+        const Gate g = tanh_gate(h);
+        // s (1 - s) is 0 in fp32 long before |h| = 64, where h u' would go
+        // on to overflow; a NaN comes through g
+        const float c = fminf(fmaxf(h, -64.0f), 64.0f);
+        const float u = kTanhC * fmaf(3.0f * kTanhA * c, c, 1.0f);
+        return fmaf(2.0f * c * u, g.s * g.c, g.s);
+    }
+    const float e = expf(-0.5f * h * h);
+    const float tail = scaled_tail(fabsf(h)) * e;
+    return fmaf(h * kInvSqrt2Pi, e, h < 0.0f ? tail : 1.0f - tail);
+}
+
+template <typename T, int FORM, bool KEEP>
+__global__ __launch_bounds__(kThreads) void k_gelu(const T *__restrict__ h, uint32_t chunks,
+                                                   FastDiv per_row, int32_t d, int64_t ldh,
+                                                   T *__restrict__ y, Act8 keep_h, Act8 keep_y)
+{
+    const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
+    if (i >= chunks)
+        return;
+    const Chunk c = chunk_at(i, per_row);
+    const int n = d - c.col;
+    float v[8];
+    load8(h + c.row * ldh + (n > 0 ? c.col : 0), n, v);
+    if (KEEP && keep_h.keep != kKeepNone)
+        keep8(keep_h, c.row, c.col, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        v[k] = gelu<FORM>(v[k]);
+    if (n > 0)
+        store8(y + c.row * d + c.col, n, v); // columns past d: gelu(0) = 0
+    if (KEEP && keep_y.keep != kKeepNone)
+        keep8(keep_y, c.row, c.col, v);
+}
+
+template <typename T, int FORM, bool ACT8>
+__global__ __launch_bounds__(kThreads) void k_gelu_backward(
+    const T *__restrict__ dy, uint32_t chunks, FastDiv per_row, int32_t d, int64_t lddy,
+    const T *__restrict__ h, int64_t ldh, Act8 h8, T *__restrict__ dh)
+{
+    const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
+    if (i >= chunks)
+        return;
+    const Chunk c = chunk_at(i, per_row);
+    const int n = d - c.col;
+    if (n <= 0)
+        return;
+    float g[8], v[8];
+    load8(dy + c.row * lddy + c.col, n, g);
+    if (ACT8)
+        restore8(h8, c.row, c.col, v);
+    else
+        load8(h + c.row * ldh + c.col, n, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        g[k] *= gelu_slope<FORM>(v[k]);
+    store8(dh + c.row * d + c.col, n, g);
+}
+
+// ---------------------------------------------------------------------------
+// Argument checks
+
+int32_t check_sizes(int32_t dtype, int64_t rows, int64_t d)
+{
+    if (!dtype_ok(dtype))
+        return fail(GQ_ERR_ARG, "dtype %d is neither GQ_IN_F32 nor GQ_IN_BF16", dtype);
+    if (rows < 0 || rows >= ((int64_t)1 << 32) || d < 1 || d > 0x7FFFFFFF - 31)
+        return fail(GQ_ERR_ARG, "rows = %lld, d = %lld out of range", (long long)rows,
+                    (long long)d);
+    if (rows > 0 && groups_of(d) >= (kMaxGroups + rows - 1) / rows)
+        return fail(GQ_ERR_UNSUPPORTED, "rows = %lld of d = %lld: 2^29 groups of 32 or more",
+                    (long long)rows, (long long)d);
+    return GQ_OK;
+}
+
+int32_t check_matrix(const char *name, const void *p, int32_t dtype, int64_t rows)
+{
+    if (!p && rows > 0)
+        return fail(GQ_ERR_NULL, "%s is NULL", name);
+    if (!aligned_to(p, elem_bytes(dtype)))
+        return fail(GQ_ERR_ALIGN, "%s is not aligned to its elements", name);
+    return GQ_OK;
+}
+
+int32_t check_ld(const char *name, int64_t ld, int64_t d)
+{
+    if (ld != 0 && ld < d)
+        return fail(GQ_ERR_ARG, "%s = %lld: 0 or at least %lld", name, (long long)ld,
+                    (long long)d);
+    if (ld > ((int64_t)1 << 40))
+        return fail(GQ_ERR_ARG, "%s = %lld out of range", name, (long long)ld);
+    return GQ_OK;
+}
+
+int32_t check_vector(const char *name, const void *p, int64_t align)
+{
+    if (!aligned_to(p, align))
+        return fail(GQ_ERR_ALIGN, "%s is not aligned to its elements", name);
+    return GQ_OK;
+}
+
+} // namespace
+
+int32_t check_act8(const char *name, const gqt_act8 *a, int64_t rows, bool written)
+{
+    if (!a)
+        return GQ_OK;
+    if ((!a->codes || !a->exps) && rows > 0)
+        return fail(GQ_ERR_NULL, "%s has no codes or no exps", name);
+    if (!aligned_to(a->codes, 16))
+        return fail(GQ_ERR_ALIGN, "the codes of %s are not 16-byte aligned", name);
+    if (written && a->rounding != GQT_ROUND_NEAREST && a->rounding != GQT_ROUND_RANDOM)
+        return fail(GQ_ERR_ARG, "%s: rounding %d", name, a->rounding);
+    return GQ_OK;
+}
+
+namespace {
+
+constexpr int kCUs = 256;
+
+// Layer norm shapes: the fewest threads per row (whole waves from 64 on)
+// whose C <= 4 chunks each hold d.
+#define GQT_BY_ROW_LENGTH(LAUNCH, LONG) \
+    do {                                \
+        if (d <= 128)                   \
+            LAUNCH(16, 1);              \
+        else if (d <= 512)              \
+            LAUNCH(64, 1);              \
+        else if (d <= 1024)             \
+            LAUNCH(64, 2);              \
+        else if (d <= 2048)             \
+            LAUNCH(256, 1);             \
+        else if (d <= 4096)             \
+            LAUNCH(256, 2);             \
+        else if (d <= 8192)             \
+            LAUNCH(256, 4);             \
+        else if (d <= 16384)            \
+            LAUNCH(512, 4);             \
+        else                            \
+            LONG();                     \
+    } while (0)
+
+// Rows that one block takes at a time.
+int64_t rows_per_block(int64_t d) { return d <= 128 ? 16 : d <= 1024 ? 4 : 1; }
+
+// Blocks of a layer norm launch: each loops over its rows with the weights
+// in registers.
+int64_t norm_blocks(int64_t rows, int64_t d)
+{
+    const int64_t all = (rows + rows_per_block(d) - 1) / rows_per_block(d);
+    const int64_t most = d > 8192 ? 2 * kCUs : 8 * kCUs;
+    return all < most ? all : most;
+}
+
+// The gradient's blocks: fewer, since each leaves 2 d partial sums.
+int64_t grad_blocks(int64_t rows, int64_t d)
+{
+    const int64_t all = (rows + rows_per_block(d) - 1) / rows_per_block(d);
+    const int64_t most = d > 8192 ? kCUs : 4 * kCUs;
+    return all < most ? all : most;
+}
+
+template <typename T>
+int32_t launch_norm(const void *x, int64_t rows, int32_t d, int64_t ldx, const void *w,
+                    const void *b, int32_t wdtype, float eps, void *y, float *mean, float *rstd,
+                    const gqt_act8 *sx, const gqt_act8 *sy, hipStream_t st)
+{
+    const Act8 kx = act8_view(sx, d), ky = act8_view(sy, d);
+    const dim3 grid((uint32_t)norm_blocks(rows, d));
+    const T *xt = (const T *)x;
+    T *yt = (T *)y;
+    const bool keep = sx || sy;
+#define GQT_LAUNCH(TPR, C)                                                                       \
+    do {                                                                                         \
+        if (keep)                                                                                \
+            k_layer_norm<T, TPR, C, true><<<grid, block_threads<TPR>(), 0, st>>>(                \
+                xt, rows, d, ldx, w, b, wdtype, eps, yt, mean, rstd, kx, ky);                    \
+        else                                                                                     \
+            k_layer_norm<T, TPR, C, false><<<grid, block_threads<TPR>(), 0, st>>>(               \
+                xt, rows, d, ldx, w, b, wdtype, eps, yt, mean, rstd, kx, ky);                    \
+    } while (0)
+#define GQT_LONG()                                                                               \
+    k_layer_norm_long<T><<<grid, kLongThreads, 0, st>>>(xt, rows, d, ldx, w, b, wdtype, eps, yt, \
+                                                        mean, rstd, kx, ky)
+    GQT_BY_ROW_LENGTH(GQT_LAUNCH, GQT_LONG);
+#undef GQT_LAUNCH
+#undef GQT_LONG
+    return check_launch("k_layer_norm");
+}
+
+template <typename T>
+int32_t launch_norm_backward(const void *dy, int64_t rows, int32_t d, int64_t lddy, const void *x,
+                             int64_t ldx, const gqt_act8 *x8, const float *mean,
+                             const float *rstd, const void *w, int32_t wdtype, void *dx,
+                             float *partial, hipStream_t st)
+{
+    const Act8 a = act8_view(x ? nullptr : x8, d);
+    const dim3 grid((uint32_t)grad_blocks(rows, d));
+    const T *dyt = (const T *)dy, *xt = (const T *)x;
+    T *dxt = (T *)dx;
+#define GQT_LAUNCH(TPR, C)                                                                       \
+    do {                                                                                         \
+        if (x)                                                                                   \
+            k_layer_norm_backward<T, TPR, C, false><<<grid, block_threads<TPR>(), 0, st>>>(      \
+                dyt, rows, d, lddy, xt, ldx, a, mean, rstd, w, wdtype, dxt, partial);            \
+        else                                                                                     \
+            k_layer_norm_backward<T, TPR, C, true><<<grid, block_threads<TPR>(), 0, st>>>(       \
+                dyt, rows, d, lddy, xt, ldx, a, mean, rstd, w, wdtype, dxt, partial);            \
+    } while (0)
+#define GQT_LONG()                                                                               \
+    do {                                                                                         \
+        if (x)                                                                                   \
+            k_layer_norm_backward_long<T, false><<<grid, kLongThreads, 0, st>>>(                 \
+                dyt, rows, d, lddy, xt, ldx, a, mean, rstd, w, wdtype, dxt, partial);            \
+        else                                                                                     \
+            k_layer_norm_backward_long<T, true><<<grid, kLongThreads, 0, st>>>(                  \
+                dyt, rows, d, lddy, xt, ldx, a, mean, rstd, w, wdtype, dxt, partial);            \
+    } while (0)
+    GQT_BY_ROW_LENGTH(GQT_LAUNCH, GQT_LONG);
+#undef GQT_LAUNCH
+#undef GQT_LONG
+    return check_launch("k_layer_norm_backward");
+}
+
+inline dim3 chunk_grid(uint32_t chunks) { return dim3((chunks + kThreads - 1) / kThreads); }
+
+} // namespace
+} // namespace gqt
+
+// ---------------------------------------------------------------------------
+// C ABI
+
+using namespace gqt;
+
+extern "C" {
+
+const char *gqt_last_error(void) { return g_err; }
+
+int64_t gqt_act8_groups(int64_t d) { return d < 1 || d > 0x7FFFFFFF - 31 ? -1 : groups_of(d); }
+
+int64_t gqt_act8_code_pitch(int64_t d)
+{
+    return d < 1 || d > 0x7FFFFFFF - 31 ? -1 : 32 * groups_of(d);
+}
+
+int32_t gqt_act8_save(const void *x, int32_t dtype, int64_t rows, int64_t d, int64_t ldx,
+                      const gqt_act8 *out, void *stream)
+{
+    GQT_TRY(check_sizes(dtype, rows, d));
+    GQT_TRY(check_matrix("x", x, dtype, rows));
+    GQT_TRY(check_ld("ldx", ldx, d));
+    if (!out)
+        return fail(GQ_ERR_NULL, "out is NULL");
+    GQT_TRY(check_act8("out", out, rows, true));
+    if (rows == 0)
+        return ok();
+    const FastDiv per_row = fast_div((uint32_t)(4 * groups_of(d)));
+    const uint32_t chunks = (uint32_t)rows * per_row.d;
+    const Act8 a = act8_view(out, d);
+    const hipStream_t st = (hipStream_t)stream;
+    if (dtype == GQ_IN_F32)
+        k_act8_save<float><<<chunk_grid(chunks), kThreads, 0, st>>>((const float *)x, chunks,
+                                                                    per_row, (int32_t)d, ldx, a);
+    else
+        k_act8_save<bf16><<<chunk_grid(chunks), kThreads, 0, st>>>((const bf16 *)x, chunks,
+                                                                   per_row, (int32_t)d, ldx, a);
+    return check_launch("k_act8_save");
+}
+
+int32_t gqt_act8_restore(const gqt_act8 *in, int64_t rows, int64_t d, int32_t dtype, void *out,
+                         void *stream)
+{
+    GQT_TRY(check_sizes(dtype, rows, d));
+    if (!in)
+        return fail(GQ_ERR_NULL, "in is NULL");
+    GQT_TRY(check_act8("in", in, rows, false));
+    GQT_TRY(check_matrix("out", out, dtype, rows));
+    if (rows == 0)
+        return ok();
+    const FastDiv per_row = fast_div((uint32_t)(4 * groups_of(d)));
+    const uint32_t chunks = (uint32_t)rows * per_row.d;
+    const Act8 a = act8_view(in, d);
+    const hipStream_t st = (hipStream_t)stream;
+    if (dtype == GQ_IN_F32)
+        k_act8_restore<float><<<chunk_grid(chunks), kThreads, 0, st>>>(a, chunks, per_row,
+                                                                       (int32_t)d, (float *)out);
+    else
+        k_act8_restore<bf16><<<chunk_grid(chunks), kThreads, 0, st>>>(a, chunks, per_row,
+                                                                      (int32_t)d, (bf16 *)out);
+    return check_launch("k_act8_restore");
+}
+
+int32_t gqt_layer_norm(const void *x, int32_t dtype, int64_t rows, int64_t d, int64_t ldx,
+                       const void *w, const void *b, int32_t wdtype, float eps, void *y,
+                       float *mean, float *rstd, const gqt_act8 *save_x, const gqt_act8 *save_y,
+                       void *stream)
+{
+    GQT_TRY(check_sizes(dtype, rows, d));
+    GQT_TRY(check_matrix("x", x, dtype, rows));
+    GQT_TRY(check_ld("ldx", ldx, d));
+    if (!dtype_ok(wdtype))
+        return fail(GQ_ERR_ARG, "wdtype %d is neither GQ_IN_F32 nor GQ_IN_BF16", wdtype);
+    if (!(eps >= 0.0f) || isinf(eps))
+        return fail(GQ_ERR_ARG, "eps must be finite and >= 0");
+    GQT_TRY(check_matrix("y", y, dtype, rows));
+    GQT_TRY(check_vector("w", w, elem_bytes(wdtype)));
+    GQT_TRY(check_vector("b", b, elem_bytes(wdtype)));
+    GQT_TRY(check_vector("mean", mean, 4));
+    GQT_TRY(check_vector("rstd", rstd, 4));
+    GQT_TRY(check_act8("save_x", save_x, rows, true));
+    GQT_TRY(check_act8("save_y", save_y, rows, true));
+    if (rows == 0)
+        return ok();
+    return dtype == GQ_IN_F32
+               ? launch_norm<float>(x, rows, (int32_t)d, ldx, w, b, wdtype, eps, y, mean, rstd,
+                                    save_x, save_y, (hipStream_t)stream)
+               : launch_norm<bf16>(x, rows, (int32_t)d, ldx, w, b, wdtype, eps, y, mean, rstd,
+                                   save_x, save_y, (hipStream_t)stream);
+}
+
+int64_t gqt_layer_norm_backward_workspace_bytes(int64_t rows, int64_t d)
+{
+    if (rows < 0 || rows >= ((int64_t)1 << 32) || d < 1 || d > 0x7FFFFFFF - 31)
+        return -1;
+    return 8 * d * grad_blocks(rows, d);
+}
+
+int32_t gqt_layer_norm_backward(const void *dy, int32_t dtype, int64_t rows, int64_t d,
+                                int64_t lddy, const void *x, int64_t ldx, const gqt_act8 *x8,
+                                const float *mean, const float *rstd, const void *w,
+                                int32_t wdtype, void *dx, void *dw, void *db, void *workspace,
+                                int64_t workspace_bytes, void *stream)
+{
+    GQT_TRY(check_sizes(dtype, rows, d));
+    GQT_TRY(check_matrix("dy", dy, dtype, rows));
+    GQT_TRY(check_ld("lddy", lddy, d));
+    if (x) {
+        GQT_TRY(check_matrix("x", x, dtype, rows));
+        GQT_TRY(check_ld("ldx", ldx, d));
+    } else if (!x8) {
+        return fail(GQ_ERR_NULL, "x and x8 are both NULL");
+    } else {
+        GQT_TRY(check_act8("x8", x8, rows, false));
+    }
+    if (!dtype_ok(wdtype))
+        return fail(GQ_ERR_ARG, "wdtype %d is neither GQ_IN_F32 nor GQ_IN_BF16", wdtype);
+    if ((!mean || !rstd) && rows > 0)
+        return fail(GQ_ERR_NULL, "mean or rstd is NULL");
+    GQT_TRY(check_vector("mean", mean, 4));
+    GQT_TRY(check_vector("rstd", rstd, 4));
+    GQT_TRY(check_matrix("dx", dx, dtype, rows));
+    GQT_TRY(check_vector("w", w, elem_bytes(wdtype)));
+    GQT_TRY(check_vector("dw", dw, elem_bytes(wdtype)));
+    GQT_TRY(check_vector("db", db, elem_bytes(wdtype)));
+    const bool sums = dw || db;
+    if (sums) {
+        const int64_t need = gqt_layer_norm_backward_workspace_bytes(rows, d);
+        if (!workspace && need > 0)
+            return fail(GQ_ERR_NULL, "workspace is NULL");
+        if (workspace_bytes < need)
+            return fail(GQ_ERR_WORKSPACE, "workspace of %lld bytes, %lld are needed",
+                        (long long)workspace_bytes, (long long)need);
+        if (!aligned_to(workspace, 16))
+            return fail(GQ_ERR_ALIGN, "workspace is not 16-byte aligned");
+    }
+    const hipStream_t st = (hipStream_t)stream;
+    float *partial = sums ? (float *)workspace : nullptr;
+    if (rows > 0)
+        GQT_TRY(dtype == GQ_IN_F32
+                    ? launch_norm_backward<float>(dy, rows, (int32_t)d, lddy, x, ldx, x8, mean,
+                                                  rstd, w, wdtype, dx, partial, st)
+                    : launch_norm_backward<bf16>(dy, rows, (int32_t)d, lddy, x, ldx, x8, mean,
+                                                 rstd, w, wdtype, dx, partial, st));
+    if (!sums)
+        return ok();
+    k_sum_partials<<<dim3((uint32_t)((d + 63) / 64), 2), 256, 0, st>>>(
+        partial, (int32_t)grad_blocks(rows, d), (int32_t)d, dw, db, wdtype);
+    return check_launch("k_sum_partials");
+}
+
+int32_t gqt_gelu(const void *h, int32_t dtype, int64_t rows, int64_t d, int64_t ldh, int32_t form,
+                 void *y, const gqt_act8 *save_h, const gqt_act8 *save_y, void *stream)
+{
+    GQT_TRY(check_sizes(dtype, rows, d));
+    GQT_TRY(check_matrix("h", h, dtype, rows));
+    GQT_TRY(check_ld("ldh", ldh, d));
+    if (form != GQT_GELU_ERF && form != GQT_GELU_TANH)
+        return fail(GQ_ERR_ARG, "form %d", form);
+    GQT_TRY(check_matrix("y", y, dtype, rows));
+    GQT_TRY(check_act8("save_h", save_h, rows, true));
+    GQT_TRY(check_act8("save_y", save_y, rows, true));
+    if (rows == 0)
+        return ok();
+    const FastDiv per_row = fast_div((uint32_t)(4 * groups_of(d)));
+    const uint32_t chunks = (uint32_t)rows * per_row.d;
+    const Act8 kh = act8_view(save_h, d), ky = act8_view(save_y, d);
+    const hipStream_t st = (hipStream_t)stream;
+#define GQT_LAUNCH(T, FORM)                                                                      \
+    do {                                                                                         \
+        if (save_h || save_y)                                                                    \
+            k_gelu<T, FORM, true><<<chunk_grid(chunks), kThreads, 0, st>>>(                      \
+                (const T *)h, chunks, per_row, (int32_t)d, ldh, (T *)y, kh, ky);                 \
+        else                                                                                     \
+            k_gelu<T, FORM, false><<<chunk_grid(chunks), kThreads, 0, st>>>(                     \
+                (const T *)h, chunks, per_row, (int32_t)d, ldh, (T *)y, kh, ky);                 \
+    } while (0)
+    if (dtype == GQ_IN_F32) {
+        if (form == GQT_GELU_ERF)
+            GQT_LAUNCH(float, GQT_GELU_ERF);
+        else
+            GQT_LAUNCH(float, GQT_GELU_TANH);
+    } else if (form == GQT_GELU_ERF) {
+        GQT_LAUNCH(bf16, GQT_GELU_ERF);
+    } else {
+        GQT_LAUNCH(bf16, GQT_GELU_TANH);
+    }
+#undef GQT_LAUNCH
+    return check_launch("k_gelu");
+}
+
+int32_t gqt_gelu_backward(const void *dy, int32_t dtype, int64_t rows, int64_t d, int64_t lddy,
+                          const void *h, int64_t ldh, const gqt_act8 *h8, int32_t form, void *dh,
+                          void *stream)
+{
+    GQT_TRY(check_sizes(dtype, rows, d));
+    GQT_TRY(check_matrix("dy", dy, dtype, rows));
+    GQT_TRY(check_ld("lddy", lddy, d));
+    if (h) {
+        GQT_TRY(check_matrix("h", h, dtype, rows));
+        GQT_TRY(check_ld("ldh", ldh, d));
+    } else if (!h8) {
+        return fail(GQ_ERR_NULL, "h and h8 are both NULL");
+    } else {
+        GQT_TRY(check_act8("h8", h8, rows, false));
+    }
+    if (form != GQT_GELU_ERF && form != GQT_GELU_TANH)
+        return fail(GQ_ERR_ARG, "form %d", form);
+    GQT_TRY(check_matrix("dh", dh, dtype, rows));
+    if (rows == 0)
+        return ok();
+    const FastDiv per_row = fast_div((uint32_t)(4 * groups_of(d)));
+    const uint32_t chunks = (uint32_t)rows * per_row.d;
+    const Act8 a = act8_view(h ? nullptr : h8, d);
+    const hipStream_t st = (hipStream_t)stream;
+#define GQT_LAUNCH(T, FORM)                                                                      \
+    do {                                                                                         \
+        if (h)                                                                                   \
+            k_gelu_backward<T, FORM, false><<<chunk_grid(chunks), kThreads, 0, st>>>(            \
+                (const T *)dy, chunks, per_row, (int32_t)d, lddy, (const T *)h, ldh, a,          \
+                (T *)dh);                                                                        \
+        else                                                                                     \
+            k_gelu_backward<T, FORM, true><<<chunk_grid(chunks), kThreads, 0, st>>>(             \
+                (const T *)dy, chunks, per_row, (int32_t)d, lddy, nullptr, 0, a, (T *)dh);       \
+    } while (0)
+    if (dtype == GQ_IN_F32) {
+        if (form == GQT_GELU_ERF)
+            GQT_LAUNCH(float, GQT_GELU_ERF);
+        else
+            GQT_LAUNCH(float, GQT_GELU_TANH);
+    } else if (form == GQT_GELU_ERF) {
+        GQT_LAUNCH(bf16, GQT_GELU_ERF);
+    } else {
+        GQT_LAUNCH(bf16, GQT_GELU_TANH);
+    }
+#undef GQT_LAUNCH
+    return check_launch("k_gelu_backward");
+}
+
+} // extern "C"

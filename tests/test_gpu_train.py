@@ -1,0 +1,676 @@
+"""The training operators on the GPU against their plain 64-bit forms
+(tests/train_plain.py, whose bounds are those of fp32 arithmetic): sizes and
+strides where the kernels change shape, non-finite values, empty inputs,
+streams, graphs, offsets beyond 32 bits, and the operators under autograd."""
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import allreduce_compatible_gradient_amd as gq  # noqa: E402
+import train_plain as plain  # noqa: E402
+from allreduce_compatible_gradient_amd import train  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+EPS = 1e-5
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    train.lib()
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def draw(rows, d, seed, dtype="f32", scale=1.0, mean=0.0):
+    """A device matrix of values `dtype` holds, and the same values in 64 bits."""
+    x = np.random.default_rng(seed).standard_normal((rows, d)) * scale + mean
+    t = torch.from_numpy(x).to(DEV).to(DT[dtype])
+    return t, host(t)
+
+
+def strided(t, how):
+    """The same values in another layout: rows further apart, off the 16-byte
+    alignment, or as they are."""
+    rows, d = t.shape
+    if how == "apart":
+        big = torch.full((rows, d + 13), float("nan"), dtype=t.dtype, device=t.device)
+        big[:, 5:5 + d] = t
+        return big[:, 5:5 + d]
+    if how == "off":
+        flat = torch.empty(rows * d + 3, dtype=t.dtype, device=t.device)
+        flat[3:] = t.reshape(-1)
+        return flat[3:].view(rows, d)
+    return t
+
+
+def within(got, want, bound, what):
+    got = host(got)
+    assert got.shape == want.shape, (what, got.shape, want.shape)
+    bad = ~(np.abs(got - want) <= bound)
+    assert not bad.any(), (what, int(bad.sum()), float((np.abs(got - want) / bound).max()),
+                           np.argwhere(bad)[:4].tolist())
+
+
+def same_copy(a, codes, exps, what=""):
+    assert np.array_equal(a.exps.cpu().numpy(), exps), what
+    assert np.array_equal(a.codes.cpu().numpy(), codes), what
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit copy
+
+@pytest.mark.parametrize("how", ["plain", "apart", "off"])
+@pytest.mark.parametrize("seed", [None, 0x1234567890ABCDEF])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,d", [(1, 1), (3, 7), (2, 31), (5, 32), (4, 33), (3, 250), (17, 64)])
+def test_save_and_restore(rows, d, dtype, seed, how):
+    t, x = draw(rows, d, rows * 100 + d, dtype)
+    codes, exps = plain.save(x, seed)
+    a = train.gqt_act8_save(strided(t, how), seed=seed)
+    same_copy(a, codes, exps)
+    for out in ("f32", "bf16"):
+        got = train.gqt_act8_restore(a, DT[out])
+        assert got.dtype == DT[out]
+        assert np.array_equal(host(got), plain.restore(codes, exps, d)), out
+
+
+def test_save_of_extreme_values():
+    """Groups of zeros, of subnormals, at and next to 127 steps, at the ends
+    of the range, and with an inf or NaN among finite values."""
+    f = np.float32
+    top, tiny = np.finfo(f).max, np.finfo(f).smallest_subnormal
+    rows = [np.zeros(32, f), np.full(32, -0.0, f), np.arange(32, dtype=f) * tiny,
+            np.linspace(-2e-38, 2e-38, 32, dtype=f), np.full(32, top), np.full(32, -top),
+            np.linspace(-1, 1, 32, dtype=f) * top]
+    for k in (-120, -1, 0, 7, 100):
+        for edge in (np.nextafter(f(127), f(0)), f(127), np.nextafter(f(127), f(999))):
+            r = np.linspace(-1, 1, 32, dtype=f) * f(2.0**k)
+            r[11] = edge * f(2.0**k)
+            rows.append(r)
+    # halves: ties of rounding to nearest
+    rows.append((np.arange(32, dtype=f) - 15.5))
+    for bad in (np.inf, -np.inf, np.nan):
+        r = np.linspace(-1, 1, 32, dtype=f)
+        r[29] = bad
+        rows.append(r)
+    x = np.stack(rows)
+    x = np.concatenate([x, x[::-1]], axis=1)  # each group beside another
+    for seed in (None, 5):
+        codes, exps = plain.save(x.astype(np.float64), seed)
+        a = train.gqt_act8_save(torch.from_numpy(x).to(DEV), seed=seed)
+        same_copy(a, codes, exps, seed)
+        got = host(train.gqt_act8_restore(a, torch.float32))
+        want = plain.restore(codes, exps, 64)
+        assert np.array_equal(got, want, equal_nan=True)
+        assert np.isfinite(got[np.isfinite(want)]).all()
+        got = host(train.gqt_act8_restore(a, torch.bfloat16))
+        assert np.array_equal(got, want, equal_nan=True)
+
+
+def test_second_draw_settles_ties():
+    """x = 1 + h 2^-16 + 2^-17 (in steps, in a group of step 1) ties the first
+    draw's half h exactly: the second draw decides, about half of the time."""
+    rows, seed = 40, 99
+    u = plain.uniforms(rows, 32, seed)
+    x = 1 + (u >> 16) * 2.0**-16 + 2.0**-17
+    x[:, 0] = 127.0  # the step is 1
+    t = torch.from_numpy(x).to(DEV).float()
+    assert np.array_equal(host(t), x)
+    codes, exps = plain.save(x, seed)
+    same_copy(train.gqt_act8_save(t, seed=seed), codes, exps)
+    up = (codes[:, 1:] == 2).mean()
+    assert 0.3 < up < 0.7
+
+
+def test_save_of_a_broadcast_row():
+    t, x = draw(1, 70, 3)
+    codes, exps = plain.save(np.tile(x, (6, 1)), 8)
+    same_copy(train.gqt_act8_save(t.expand(6, 70), seed=8), codes, exps)
+
+
+# ---------------------------------------------------------------------------
+# layer norm
+
+# both sides of every change of the kernel's shape
+LENGTHS = [1, 5, 64, 128, 129, 512, 513, 1000, 1024, 1025, 2047, 2049, 4096, 4097, 8192, 8193,
+           16384, 16385, 20001]
+
+
+@pytest.mark.parametrize("d", LENGTHS)
+@pytest.mark.parametrize("dtype,wdtype,how", [("f32", "f32", "plain"), ("bf16", "f32", "off"),
+                                              ("bf16", "bf16", "apart")])
+def test_layer_norm(d, dtype, wdtype, how):
+    rows = 37 if d <= 1025 else 3
+    t, x = draw(rows, d, d, dtype, mean=0.5)
+    w, wn = draw(1, d, d + 1, wdtype)
+    b, bn = draw(1, d, d + 2, wdtype)
+    y, mean, rstd = train.gqt_layer_norm(strided(t, how), w[0], b[0], EPS)
+    within(y, plain.layer_norm(x, wn, bn, EPS), plain.layer_norm_bound(x, wn, bn, EPS, dtype), "y")
+    em, er = plain.norm_stats(x, EPS)
+    within(mean, em[:, 0], plain.gamma(d) * np.abs(x).mean(axis=1) + plain.U, "mean")
+    dm = plain.gamma(d) * np.abs(x).mean(axis=1) + plain.U * np.abs(em[:, 0])
+    within(rstd, er[:, 0], er[:, 0] * (plain.gamma(d) + 8 * plain.U + (dm * er[:, 0])**2), "rstd")
+    y2, none, _ = train.gqt_layer_norm(strided(t, how), w[0], b[0], EPS, stats=False)
+    assert none is None and torch.equal(y, y2)
+
+
+@pytest.mark.parametrize("rows,d", [(1, 96), (1, 4096), (9, 40), (3000, 24), (1500, 640)])
+@pytest.mark.parametrize("weight,bias", [(True, False), (False, True), (False, False)])
+def test_layer_norm_without_weights(rows, d, weight, bias):
+    t, x = draw(rows, d, 1)
+    w, wn = draw(1, d, 2)
+    b, bn = draw(1, d, 3)
+    y, _, _ = train.gqt_layer_norm(t, w[0] if weight else None, b[0] if bias else None, EPS)
+    wn, bn = wn if weight else np.ones_like(wn), bn if bias else np.zeros_like(bn)
+    within(y, plain.layer_norm(x, wn, bn, EPS), plain.layer_norm_bound(x, wn, bn, EPS, "f32"), "y")
+
+
+def test_layer_norm_of_a_large_mean():
+    t, x = draw(8, 3000, 4, mean=1000.0)
+    y, _, _ = train.gqt_layer_norm(t, eps=EPS)
+    one, zero = np.ones((1, 3000)), np.zeros((1, 3000))
+    within(y, plain.layer_norm(x, one, zero, EPS),
+           plain.layer_norm_bound(x, one, zero, EPS, "f32"), "y")
+
+
+def test_layer_norm_of_constant_and_non_finite_rows():
+    """A constant row gives its bias; an inf or NaN stays in its row; a row of
+    zero variance with eps = 0 is what the formula says, not a number."""
+    t, x = draw(6, 200, 5)
+    t[1] = 3.25
+    t[2, 7] = float("inf")
+    t[4, 150] = float("nan")
+    b, bn = draw(1, 200, 6)
+    y, mean, rstd = train.gqt_layer_norm(t, None, b[0], EPS)
+    y = host(y)
+    assert np.array_equal(y[1], bn[0])
+    assert np.isnan(y[2]).any() and np.isnan(y[4]).all()
+    assert np.isfinite(y[[0, 3, 5]]).all()
+    dy, _ = draw(6, 200, 7)
+    dx, _, _ = train.gqt_layer_norm_backward(dy, t, mean, rstd)
+    assert np.isfinite(host(dx)[[0, 1, 3, 5]]).all()
+    y, _, _ = train.gqt_layer_norm(t[1:2], eps=0.0)
+    assert np.isnan(host(y)).all()
+
+
+@pytest.mark.parametrize("d", [1, 33, 96, 1000, 1030, 4100, 8200, 16400])
+@pytest.mark.parametrize("dtype,seeds", [("f32", (None, None)), ("bf16", (3, 4)),
+                                         ("bf16", (None, 2**63 + 5))])
+def test_layer_norm_saves_in_the_same_pass(d, dtype, seeds):
+    """The copies are those of the separate calls, and y does not change."""
+    rows = 5
+    t, _ = draw(rows, d, d, dtype)
+    w, _ = draw(1, d, d + 1, dtype)
+    x8, y8 = train.Act8.empty(rows, d, DEV), train.Act8.empty(rows, d, DEV)
+    y, mean, rstd = train.gqt_layer_norm(t, w[0], None, EPS)
+    z, mean2, rstd2 = train.gqt_layer_norm(t, w[0], None, EPS, save_x=x8, seed_x=seeds[0],
+                                           save_y=y8, seed_y=seeds[1])
+    assert torch.equal(y, z) and torch.equal(mean, mean2) and torch.equal(rstd, rstd2)
+    for a, v, s in ((x8, t, seeds[0]), (y8, y, seeds[1])):
+        ref = train.gqt_act8_save(v, seed=s)
+        assert torch.equal(a.codes, ref.codes) and torch.equal(a.exps, ref.exps)
+    only = train.Act8.empty(rows, d, DEV)
+    train.gqt_layer_norm(t, w[0], None, EPS, save_y=only, seed_y=seeds[1])
+    assert torch.equal(only.codes, y8.codes) and torch.equal(only.exps, y8.exps)
+
+
+@pytest.mark.parametrize("d", LENGTHS)
+@pytest.mark.parametrize("dtype,wdtype,kept", [("f32", "f32", False), ("bf16", "f32", True),
+                                               ("bf16", "bf16", False), ("f32", "f32", True)])
+def test_layer_norm_backward(d, dtype, wdtype, kept):
+    rows = 70 if d <= 1025 else 3
+    t, x = draw(rows, d, d + 10, dtype, mean=-0.3)
+    dyt, dy = draw(rows, d, d + 11, dtype)
+    w, wn = draw(1, d, d + 12, wdtype)
+    _, mean, rstd = train.gqt_layer_norm(t, w[0], None, EPS)
+    xin = strided(t, "apart")
+    if kept:
+        xin = train.gqt_act8_save(t, seed=d)
+        x = host(train.gqt_act8_restore(xin, torch.float32))
+    dx, dw, db = train.gqt_layer_norm_backward(strided(dyt, "off"), xin, mean, rstd, w[0])
+    args = dy, x, host(mean)[:, None], host(rstd)[:, None], wn
+    want = plain.layer_norm_backward(*args)
+    for g, e, bound, what in zip((dx, dw, db), want,
+                                 plain.layer_norm_backward_bounds(*args, dtype, wdtype),
+                                 ("dx", "dw", "db")):
+        within(g, e, bound, what)
+    assert dw.dtype == w.dtype and db.dtype == w.dtype
+    dx2, none, db2 = train.gqt_layer_norm_backward(dyt, xin, mean, rstd, w[0], weight_grad=False)
+    assert none is None and torch.equal(dx, dx2) and torch.equal(db, db2)
+    dx3, none, none2 = train.gqt_layer_norm_backward(dyt, xin, mean, rstd, w[0],
+                                                     weight_grad=False, bias_grad=False)
+    assert none is none2 is None and torch.equal(dx, dx3)
+
+
+@pytest.mark.parametrize("rows,d", [(1, 64), (1, 3000), (5000, 16), (40_000, 72), (2500, 1024),
+                                    (1300, 5000)])
+def test_layer_norm_backward_over_many_rows(rows, d):
+    t, x = draw(rows, d, 20)
+    dyt, dy = draw(rows, d, 21)
+    _, mean, rstd = train.gqt_layer_norm(t, eps=EPS)
+    got = train.gqt_layer_norm_backward(dyt, t, mean, rstd)
+    args = dy, x, host(mean)[:, None], host(rstd)[:, None], np.ones((1, d))
+    for g, e, bound, what in zip(got, plain.layer_norm_backward(*args),
+                                 plain.layer_norm_backward_bounds(*args, "f32", "f32"),
+                                 ("dx", "dw", "db")):
+        within(g, e, bound, what)
+    again = train.gqt_layer_norm_backward(dyt, t, mean, rstd)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+def test_layer_norm_backward_against_differences():
+    t, x = draw(7, 300, 30)
+    dyt, dy = draw(7, 300, 31)
+    w, wn = draw(1, 300, 32)
+    b, bn = draw(1, 300, 33)
+    _, mean, rstd = train.gqt_layer_norm(t, w[0], b[0], EPS)
+    dx, dw, db = (host(g) for g in train.gqt_layer_norm_backward(dyt, t, mean, rstd, w[0]))
+    rng, e = np.random.default_rng(34), 1e-6
+    for grad, i in ((dx, 0), (dw[None], 1), (db[None], 2)):
+        args = [x, wn, bn]
+        v = rng.standard_normal(args[i].shape)
+
+        def loss(s):
+            a = list(args)
+            a[i] = a[i] + s * v
+            return (dy * plain.layer_norm(*a, EPS)).sum()
+        # fp32 gradient: 2^-20 of the terms' magnitude
+        assert abs((loss(e) - loss(-e)) / (2 * e) - (grad * v).sum()) \
+            < 1e-6 * np.abs(grad * v).sum() + 1e-6
+
+
+# ---------------------------------------------------------------------------
+# GELU
+
+@pytest.mark.parametrize("form", ["none", "tanh"])
+@pytest.mark.parametrize("dtype,how", [("f32", "plain"), ("bf16", "apart"), ("f32", "off")])
+@pytest.mark.parametrize("rows,d", [(1, 1), (3, 33), (40, 256), (7, 1001)])
+def test_gelu(rows, d, dtype, form, how):
+    t, h = draw(rows, d, rows + d, dtype, scale=3.0)
+    y = train.gqt_gelu(strided(t, how), form)
+    by, bs = plain.gelu_bounds(h, form)
+    want = plain.gelu(h, form)
+    within(y, want, by + np.abs(want) * plain.HALF[dtype] * 1.01 + 2.0**-126, "y")
+    dyt, dy = draw(rows, d, rows + d + 1, dtype)
+    want = dy * plain.gelu_slope(h, form)
+    dh = train.gqt_gelu_backward(strided(dyt, how), t, form)
+    within(dh, want, np.abs(dy) * bs + np.abs(want) * (plain.HALF[dtype] * 1.01 + plain.U)
+           + 2.0**-126, "dh")
+    # from the 8-bit copy, written in the forward pass
+    h8, y8 = train.Act8.empty(rows, d, DEV), train.Act8.empty(rows, d, DEV)
+    z = train.gqt_gelu(strided(t, how), form, save_h=h8, seed_h=6, save_y=y8)
+    assert torch.equal(y, z)
+    for a, ref in ((h8, train.gqt_act8_save(t, seed=6)), (y8, train.gqt_act8_save(y))):
+        assert torch.equal(a.codes, ref.codes) and torch.equal(a.exps, ref.exps)
+    dh = train.gqt_gelu_backward(dyt, h8, form)
+    kept = train.gqt_act8_restore(h8, DT[dtype])
+    assert torch.equal(dh, train.gqt_gelu_backward(dyt, kept, form))
+
+
+@pytest.mark.parametrize("form", ["none", "tanh"])
+def test_gelu_over_its_range(form):
+    """The whole axis, the far tail and the largest values: no overflow where
+    the result has none, NaN only for NaN (and -inf, inf 0 in the formula)."""
+    h = np.concatenate([np.linspace(-14, 14, 4001), -np.logspace(-30, 38, 300),
+                        np.logspace(-30, 38, 300)]).astype(np.float32)
+    t = torch.from_numpy(h[None]).to(DEV)
+    h = h[None].astype(np.float64)
+    y = train.gqt_gelu(t, form)
+    s = train.gqt_gelu_backward(torch.ones_like(t), t, form)
+    with np.errstate(over="ignore", invalid="ignore"):
+        clip = np.clip(h, -100, 100)
+        want = np.where(np.abs(h) > 100, np.maximum(h, 0), plain.gelu(clip, form))
+        slope = np.where(np.abs(h) > 100, h > 0, plain.gelu_slope(clip, form))
+        by, bs = plain.gelu_bounds(clip, form)
+    within(y, want, np.where(np.abs(h) > 100, 0, by) + np.abs(want) * 2 * plain.U + 1e-36, "y")
+    within(s, slope, np.where(np.abs(h) > 100, 0, bs) + np.abs(slope) * plain.U + 1e-36, "slope")
+    t = torch.tensor([[float("nan"), float("inf")]], device=DEV)
+    y, s = host(train.gqt_gelu(t, form)), host(train.gqt_gelu_backward(torch.ones_like(t), t, form))
+    assert np.isnan(y[0, 0]) and np.isnan(s[0, 0]) and y[0, 1] == np.inf
+
+
+# ---------------------------------------------------------------------------
+# the weight gradient
+
+def kept_matrix(m, k, seed):
+    t, _ = draw(m, k, seed)
+    a = train.gqt_act8_save(t)
+    return a, host(train.gqt_act8_restore(a, torch.float32))
+
+
+@pytest.mark.parametrize("m,n,k", [
+    (1, 1, 1), (1, 16, 16), (2, 5, 3), (16, 128, 128), (31, 33, 65), (32, 128, 64), (33, 127, 129),
+    (64, 256, 256), (65, 130, 31), (100, 257, 300), (300, 8, 1000), (257, 1000, 8), (600, 129, 131),
+    (512, 256, 512)])
+@pytest.mark.parametrize("dtype,wdtype", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32"),
+                                          ("f32", "bf16")])
+def test_weight_grad(m, n, k, dtype, wdtype):
+    a, x = kept_matrix(m, k, m + k)
+    t, dy = draw(m, n, m + n, dtype)
+    dw, db = train.gqt_weight_grad(t, a, dtype=DT[wdtype])
+    assert dw.dtype == DT[wdtype] and db.dtype == DT[wdtype]
+    want, wantb = plain.weight_grad(dy, x)
+    bw, bb = plain.weight_grad_bounds(dy, x, wdtype)
+    within(dw, want, bw, "dw")
+    within(db, wantb, bb, "db")
+    for how in ("apart", "off"):
+        v, none = train.gqt_weight_grad(strided(t, how), a, dtype=DT[wdtype], bias=False)
+        assert none is None and torch.equal(v, dw), how
+
+
+@pytest.mark.parametrize("m,n,k,dtype", [(5000, 64, 48, "bf16"), (3001, 100, 200, "f32"),
+                                         (20_000, 17, 33, "bf16")])
+def test_weight_grad_over_many_tokens(m, n, k, dtype):
+    """The tokens are split over blocks and joined; integers of dy keep every
+    sum exact, so the result has to be."""
+    rng = np.random.default_rng(m)
+    dy = rng.integers(-3, 4, (m, n)).astype(np.float64)
+    codes = rng.integers(-9, 10, (m, 32 * -(-k // 32))).astype(np.int8)
+    exps = rng.integers(126, 129, (m, -(-k // 32))).astype(np.uint8)
+    x = plain.restore(codes, exps, k)
+    assert np.abs(dy).T.dot(np.abs(x)).max() < 2**22  # in halves: below 2^24
+    a = train.Act8(torch.from_numpy(codes).to(DEV), torch.from_numpy(exps).to(DEV), k)
+    t = torch.from_numpy(dy).to(DEV).to(DT[dtype])
+    for _ in range(2):
+        dw, db = train.gqt_weight_grad(t, a)
+        want, wantb = plain.weight_grad(dy, x)
+        assert np.array_equal(host(dw), want) and np.array_equal(host(db), wantb)
+
+
+def test_weight_grad_of_a_broadcast_row():
+    a, x = kept_matrix(50, 40, 1)
+    t, dy = draw(1, 24, 2)
+    dw, db = train.gqt_weight_grad(t.expand(50, 24), a)
+    full = np.tile(dy, (50, 1))
+    for g, e, b in zip((dw, db), plain.weight_grad(full, x),
+                       plain.weight_grad_bounds(full, x, "f32")):
+        within(g, e, b, "dw")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_weight_grad_keeps_non_finite_values_in_place(dtype):
+    """An inf in dy reaches its own row of dw alone (inf, or NaN where its
+    token's activation is 0); a NaN group its own columns, and only those."""
+    m, n, k = 40, 70, 100
+    a, x = kept_matrix(m, k, 3)
+    t, dy = draw(m, n, 4, dtype)
+    t[3, 5] = float("inf")
+    t[9, 8] = float("nan")
+    a.exps[7, 1] = 255
+    a.exps[8, 3] = 255  # the last group holds columns 96 to 99 and padding
+    dw, db = train.gqt_weight_grad(t, a)
+    dw, db = host(dw), host(db)
+    cols = np.zeros(k, bool)
+    cols[32:64] = cols[96:] = True
+    assert not np.isfinite(dw[5]).any() and np.isnan(dw[8]).all()
+    assert db[5] == np.inf and np.isnan(db[8])
+    rows = np.ones(n, bool)
+    rows[[5, 8]] = False
+    assert np.isfinite(dw[rows][:, ~cols]).all() and np.isnan(dw[rows][:, cols]).all()
+    assert np.isfinite(db[rows]).all()
+    live = x[3] != 0
+    live[cols] = False
+    assert np.array_equal(np.sign(x[3][live]) * np.inf, dw[5][live])
+
+
+def test_weight_grad_takes_fp32_whole():
+    """Every bit of an fp32 dy counts: one token, so each product of a value
+    of 24 significant bits with a power of two comes back unchanged."""
+    n, k = 50, 32
+    rng = np.random.default_rng(6)
+    dy = (rng.standard_normal((1, n)) * 10.0**rng.integers(-20, 20, (1, n))).astype(np.float32)
+    codes = np.ones((1, k), dtype=np.int8)
+    exps = np.full((1, 1), 127, dtype=np.uint8)
+    a = train.Act8(torch.from_numpy(codes).to(DEV), torch.from_numpy(exps).to(DEV), k)
+    dw, db = train.gqt_weight_grad(torch.from_numpy(dy).to(DEV), a)
+    assert np.array_equal(dw.cpu().numpy(), np.tile(dy.T, (1, k)))
+    assert np.array_equal(db.cpu().numpy(), dy[0])
+
+
+# ---------------------------------------------------------------------------
+# empty inputs, refusals, large offsets, streams, graphs
+
+def test_no_rows():
+    x = torch.empty((0, 40), device=DEV)
+    w = torch.ones(40, device=DEV)
+    a = train.gqt_act8_save(x)
+    assert train.gqt_act8_restore(a).shape == (0, 40)
+    y, mean, rstd = train.gqt_layer_norm(x, w, w)
+    assert y.shape == (0, 40) and mean.shape == (0,)
+    for kept in (x, a):
+        dx, dw, db = train.gqt_layer_norm_backward(x, kept, mean, rstd, w)
+        assert dx.shape == (0, 40) and not dw.any() and not db.any()
+        assert train.gqt_gelu_backward(x, kept).shape == (0, 40)
+    assert train.gqt_gelu(x).shape == (0, 40)
+    dw, db = train.gqt_weight_grad(torch.empty((0, 9), device=DEV), a)
+    assert dw.shape == (9, 40) and not dw.any() and not db.any()
+
+
+def test_refusals():
+    x = torch.randn(4, 64, device=DEV)
+    a = train.gqt_act8_save(x)
+    _, mean, rstd = train.gqt_layer_norm(x)
+    w = torch.ones(64, device=DEV)
+    value = [lambda: train.gqt_layer_norm(x.t()),                      # column stride
+             lambda: train.gqt_layer_norm(x[0]),                       # not a matrix
+             lambda: train.gqt_layer_norm(x, w[:63]),
+             lambda: train.gqt_layer_norm(x, w.cpu()),
+             lambda: train.gqt_layer_norm(x, torch.ones(128, device=DEV)[::2]),
+             lambda: train.gqt_layer_norm(torch.as_strided(x, (4, 8), (4, 1))),  # rows overlap
+             lambda: train.gqt_layer_norm(x, save_x=train.Act8.empty(4, 63, DEV)),
+             lambda: train.gqt_layer_norm(x, save_x=train.Act8.empty(4, 64, "cpu")),
+             lambda: train.gqt_layer_norm_backward(x, x[:3], mean, rstd),
+             lambda: train.gqt_layer_norm_backward(x, x, mean[:3], rstd),
+             lambda: train.gqt_layer_norm_backward(x, x, None, rstd),
+             lambda: train.gqt_gelu(x, "quick"),
+             lambda: train.gqt_gelu_backward(x, train.gqt_act8_save(x[:2])),
+             lambda: train.gqt_weight_grad(x[:3], a),
+             lambda: train.gqt_weight_grad(torch.randn(9000, 8, device=DEV),
+                                           train.Act8.empty(9000, 8, DEV),
+                                           workspace=torch.empty(8, device=DEV)),
+             lambda: train.layer_norm(x, bits=4)]
+    for i, call in enumerate(value):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"value {i} was taken")
+    types = [lambda: train.gqt_layer_norm(x.half()), lambda: train.gqt_layer_norm(x, w, w.bfloat16()),
+             lambda: train.gqt_act8_restore(a, torch.float16),
+             lambda: train.gqt_layer_norm_backward(x, x.bfloat16(), mean, rstd),
+             lambda: train.gqt_layer_norm_backward(x, x, mean.double(), rstd),
+             lambda: train.gqt_gelu(x, save_h=x), lambda: train.gqt_weight_grad(x, x),
+             lambda: train.gqt_act8_restore(train.Act8(a.codes, a.exps.int(), 64)),
+             lambda: train.gqt_weight_grad(x, a, dtype=torch.float64)]
+    for i, call in enumerate(types):
+        with pytest.raises(TypeError):
+            call()
+            pytest.fail(f"type {i} was taken")
+    with pytest.raises(gq.GQError) as e:
+        train.gqt_layer_norm(x, eps=-1.0)
+    assert e.value.status == 2 and "eps" in str(e.value)
+    torch.cuda.synchronize()
+
+
+def test_offsets_beyond_32_bits():
+    """2.2 G values: the last rows are computed at their own places."""
+    rows, d = 34_000, 65_536
+    x = torch.zeros((rows, d), dtype=torch.bfloat16, device=DEV)
+    tail = torch.randn(3, d, device=DEV).bfloat16()
+    x[-3:] = tail
+    a = train.gqt_act8_save(x)
+    ref = train.gqt_act8_save(tail)
+    assert torch.equal(a.codes[-3:], ref.codes) and torch.equal(a.exps[-3:], ref.exps)
+    assert not a.codes[:-3].any()
+    assert torch.equal(train.gqt_act8_restore(a)[-3:], train.gqt_act8_restore(ref))
+    assert torch.equal(train.gqt_gelu(x)[-3:], train.gqt_gelu(tail))
+    assert torch.equal(train.gqt_gelu_backward(x, a)[-3:], train.gqt_gelu_backward(tail, ref))
+    x, tail = x.view(-1, 4096), tail.view(-1, 4096)
+    y, mean, rstd = train.gqt_layer_norm(x)
+    y3, mean3, rstd3 = train.gqt_layer_norm(tail)
+    assert torch.equal(y[-48:], y3) and torch.equal(mean[-48:], mean3)
+    dx, dw, _ = train.gqt_layer_norm_backward(x, x, mean, rstd)
+    dx3, dw3, _ = train.gqt_layer_norm_backward(tail, tail, mean3, rstd3)
+    assert torch.equal(dx[-48:], dx3)
+    # the rows of zeros add nothing but the order of the others' sums
+    assert torch.allclose(dw, dw3, rtol=1e-4, atol=1e-4)
+    a = train.gqt_act8_save(x)
+    ref = train.gqt_act8_save(tail)
+    dw, db = train.gqt_weight_grad(x[:, :64], a)
+    dw3, db3 = train.gqt_weight_grad(tail[:, :64], ref)
+    assert torch.allclose(dw, dw3, rtol=1e-4, atol=1e-4)
+    assert torch.allclose(db, db3, rtol=1e-4, atol=1e-4)
+
+
+def _step(x, dy, w, seed, stream=None):
+    """Every operator once, as a block's forward and backward pass call them."""
+    m, d = x.shape
+    x8, y8 = train.Act8.empty(m, d, x.device), train.Act8.empty(m, d, x.device)
+    y, mean, rstd = train.gqt_layer_norm(x, w, w, save_x=x8, seed_x=seed, save_y=y8, stream=stream)
+    h8 = train.gqt_act8_save(y, seed=seed + 1, stream=stream)
+    g = train.gqt_gelu(y, "tanh", stream=stream)
+    dh = train.gqt_gelu_backward(dy, h8, "tanh", stream=stream)
+    dw, db = train.gqt_weight_grad(dh, y8, stream=stream)
+    dx, dnw, dnb = train.gqt_layer_norm_backward(dh, x8, mean, rstd, w, stream=stream)
+    r = train.gqt_act8_restore(x8, torch.float32, stream=stream)
+    return y, g, dh, dw, db, dx, dnw, dnb, r, h8.codes, h8.exps
+
+
+def test_other_streams():
+    x, dy = draw(700, 320, 1, "bf16")[0], draw(700, 320, 2, "bf16")[0]
+    w = draw(1, 320, 3, "bf16")[0][0]
+    want = _step(x, dy, w, 5)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        got = _step(x, dy, w, 5, stream=stream)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with torch.cuda.stream(side):
+        got = _step(x, dy, w, 5)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_graph_replays_match_eager():
+    x, dy = draw(3000, 200, 1, "bf16")[0], draw(3000, 200, 2, "bf16")[0]
+    w = draw(1, 200, 3, "bf16")[0][0]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _step(x, dy, w, 5)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = _step(x, dy, w, 5)
+    for k in range(3):
+        x.copy_(draw(3000, 200, 10 + k, "bf16")[0])
+        dy.copy_(draw(3000, 200, 20 + k, "bf16")[0])
+        graph.replay()
+        torch.cuda.synchronize()
+        want = _step(x, dy, w, 5)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), k
+
+
+# ---------------------------------------------------------------------------
+# under autograd
+
+@pytest.mark.parametrize("bits", [None, 8])
+def test_autograd_layer_norm_and_gelu(bits):
+    t, x = draw(12, 50, 1)
+    w, wn = draw(1, 50, 2)
+    b, _ = draw(1, 50, 3)
+    t = t.view(3, 4, 50).requires_grad_()
+    w, b = w[0].detach().requires_grad_(), b[0].detach().requires_grad_()
+    y = train.layer_norm(t, w, b, EPS, bits=bits, seed=9 if bits else None)
+    assert y.shape == t.shape
+    y.sum().backward()  # an expanded gradient of strides 0
+    kept = host(train.gqt_act8_restore(train.gqt_act8_save(t.detach().view(12, 50), seed=9),
+                                       torch.float32)) if bits else x
+    mean, rstd = plain.norm_stats(x, EPS)
+    dx, dw, db = plain.layer_norm_backward(np.ones((12, 50)), kept, mean, rstd, wn)
+    assert np.abs(host(t.grad).reshape(12, 50) - dx).max() < 1e-5
+    assert np.abs(host(w.grad) - dw).max() < 1e-5 and np.abs(host(b.grad) - db).max() < 1e-5
+    t.grad = None
+    for form in ("none", "tanh"):
+        y = train.gelu(t, form, bits=bits, seed=9 if bits else None)
+        (2 * y).sum().backward()
+        assert np.abs(host(t.grad).reshape(12, 50) - 2 * plain.gelu_slope(kept, form)).max() < 1e-5
+        t.grad = None
+
+
+def test_autograd_linear():
+    t, _ = draw(60, 40, 1)
+    w, wn = draw(24, 40, 2)
+    b, _ = draw(1, 24, 3)
+    t, w, b = (v.detach().requires_grad_() for v in (t, w, b[0]))
+    y = train.linear(t, w, b, seed=4)
+    assert torch.equal(y, torch.nn.functional.linear(t, w, b))
+    g, gn = draw(60, 24, 5)
+    y.backward(g)
+    kept = host(train.gqt_act8_restore(train.gqt_act8_save(t.detach(), seed=4), torch.float32))
+    dw, db = plain.weight_grad(gn, kept)
+    assert np.abs(host(w.grad) - dw).max() < 1e-4 and np.abs(host(b.grad) - db).max() < 1e-4
+    assert np.abs(host(t.grad) - gn @ wn).max() < 1e-4
+    w.grad = None
+    frozen = train.linear(t.detach(), w, None)
+    frozen.sum().backward()
+    assert w.grad is not None
+
+
+@pytest.mark.parametrize("random", [False, True])
+def test_mlp8(random):
+    """The block's output is the plain block's; its gradients are those of the
+    exact activations up to the 8-bit rounding (at most half, or with random
+    rounding one, of a step of 1/64 of its group's largest value)."""
+    torch.manual_seed(0)
+    block = train.Mlp8(96, 200, random=random, seed=3, device=DEV, dtype=torch.float32)
+    x = torch.randn(5, 80, 96, device=DEV, requires_grad=True)
+    dy = torch.randn(5, 80, 96, device=DEV)
+    y = block(x)
+    y.backward(dy)
+    got = [x.grad] + [p.grad for p in block.parameters()]
+    xr = x.detach().clone().requires_grad_()
+    ref = torch.nn.functional.layer_norm(xr, (96,), block.norm.weight, block.norm.bias, EPS)
+    ref = xr + block.down(torch.nn.functional.gelu(block.up(ref), approximate="tanh"))
+    assert torch.allclose(y, ref, rtol=1e-4, atol=1e-5)
+    block.zero_grad()
+    ref.backward(dy)
+    want = [xr.grad] + [p.grad for p in block.parameters()]
+    for g, e in zip(got, want):
+        assert float((g - e).norm() / e.norm()) < 0.03
+    with torch.no_grad():
+        assert torch.allclose(block(x), ref, rtol=1e-4, atol=1e-5)
+    assert block.passes == 1
+
+
+def test_mlp8_gradients_are_unbiased():
+    """Random rounding: the mean of the weight gradient over many passes
+    approaches that of the exact activation (it is linear in the copy)."""
+    torch.manual_seed(1)
+    block = train.Mlp8(64, 64, random=True, seed=7, device=DEV, dtype=torch.float32)
+    x, dy = torch.randn(50, 64, device=DEV), torch.randn(50, 64, device=DEV)
+    passes, total, square = 200, 0, 0
+    for _ in range(passes):
+        block.zero_grad()
+        block(x).backward(dy)
+        total = total + block.down.weight.grad.double()
+        square = square + block.down.weight.grad.double()**2
+    mean = total / passes
+    dev = ((square / passes - mean**2).clamp(min=0) / passes).sqrt()
+    with torch.no_grad():
+        g = torch.nn.functional.gelu(block.up(torch.nn.functional.layer_norm(
+            x, (64,), block.norm.weight, block.norm.bias, EPS)), approximate="tanh")
+    want = (dy.t() @ g).double()
+    z = ((mean - want).abs() / (dev + 1e-6)).cpu().numpy()
+    assert z.max() < 6.5 and (z < 3).mean() > 0.98, (z.max(), (z < 3).mean())
+    assert math.isfinite(float(dev.max()))
