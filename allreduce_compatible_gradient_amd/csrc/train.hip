@@ -398,14 +398,16 @@ __global__ __launch_bounds__(kLongThreads) void k_layer_norm_backward_long(
     }
 }
 
-// dw and db: the blocks' partial sums added in block order, four waves a
-// quarter of the blocks each.  Column blocks along x, dw / db along y.
-__global__ __launch_bounds__(256) void k_sum_partials(const float *__restrict__ partial,
-                                                      int32_t blocks, int32_t d,
-                                                      void *__restrict__ dw,
-                                                      void *__restrict__ db, int32_t wdtype)
+// dw and db: the blocks' partial sums added in block order, a sixteenth of
+// the blocks a wave, eight loads in flight (one at a time, the chain of
+// loads took 62 us for 1024 blocks whatever d).  64 columns a block along x,
+// dw / db along y.
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(64 * kSumWaves) void k_sum_partials(
+    const float *__restrict__ partial, int32_t blocks, int32_t d, void *__restrict__ dw,
+    void *__restrict__ db, int32_t wdtype)
 {
-    __shared__ float part[4][64];
+    __shared__ float part[kSumWaves][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t col = (int64_t)blockIdx.x * 64 + lane;
     void *out = blockIdx.y ? db : dw;
@@ -414,14 +416,27 @@ __global__ __launch_bounds__(256) void k_sum_partials(const float *__restrict__ 
     float s = 0.0f;
     if (col < d) {
         const float *p = partial + (int64_t)blockIdx.y * d + col;
-        const int lo = (int)((int64_t)blocks * wave / 4), hi = (int)((int64_t)blocks * (wave + 1) / 4);
-        for (int i = lo; i < hi; ++i)
+        const int lo = blocks * wave / kSumWaves, hi = blocks * (wave + 1) / kSumWaves;
+        int i = lo;
+        for (; i + 8 <= hi; i += 8) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = p[(int64_t)(i + j) * 2 * d];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                s += v[j];
+        }
+        for (; i < hi; ++i)
             s += p[(int64_t)i * 2 * d];
     }
     part[wave][lane] = s;
     __syncthreads();
     if (wave == 0 && col < d) {
-        s = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+        s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kSumWaves; ++w)
+            s += part[w][lane];
         if (wdtype == GQ_IN_F32)
             static_cast<float *>(out)[col] = s;
         else
@@ -918,7 +933,7 @@ int32_t gqt_layer_norm_backward(const void *dy, int32_t dtype, int64_t rows, int
                                                  rstd, w, wdtype, dx, partial, st));
     if (!sums)
         return ok();
-    k_sum_partials<<<dim3((uint32_t)((d + 63) / 64), 2), 256, 0, st>>>(
+    k_sum_partials<<<dim3((uint32_t)((d + 63) / 64), 2), 64 * kSumWaves, 0, st>>>(
         partial, (int32_t)grad_blocks(rows, d), (int32_t)d, dw, db, wdtype);
     return check_launch("k_sum_partials");
 }
