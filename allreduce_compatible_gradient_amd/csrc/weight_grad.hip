@@ -17,34 +17,65 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kTileN = 128, kTileK = 128; // output tile: rows of dw, columns of dw
-constexpr int kTileM = 32;                // tokens per step: the depth of one MFMA
-constexpr int kWgThreads = 256;
+constexpr int kStepM = 64;                // tokens per step: 32 for each half of the waves
+constexpr int kWgThreads = 512;
+constexpr int kAhead = 2; // steps whose loads are in flight
 // LDS rows of 128 bf16 lie 288 bytes apart: a transposed read takes 32 bytes
 // of each of 16 rows, which then fall into all banks evenly.
 constexpr int kRowBytes = 288;
-constexpr int kTileBytes = kTileM * kRowBytes;
+constexpr int kTileBytes = kStepM * kRowBytes;
 
 template <typename T>
 constexpr int parts() { return sizeof(T) == 4 ? 3 : 1; }
 
+// One thread's share of a step as loaded: rows r and r + 32, eight columns.
+template <typename T>
+struct Loaded {
+    u32x4 a[2][sizeof(T) / 2];
+    u32x2 b[2];
+    uint32_t e[2];
+};
+
+__device__ __forceinline__ void load_raw(const bf16 *p, u32x4 (&w)[1])
+{
+    w[0] = *reinterpret_cast<const u32x4_e2 *>(p);
+}
+__device__ __forceinline__ void load_raw(const float *p, u32x4 (&w)[2])
+{
+    w[0] = *reinterpret_cast<const u32x4_e4 *>(p);
+    w[1] = *reinterpret_cast<const u32x4_e4 *>(p + 4);
+}
+// the first n elements, the others 0
+__device__ __forceinline__ void load_raw_part(const bf16 *p, int n, u32x4 (&w)[1])
+{
+    const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        w[0][k] = 2 * k < n ? q[2 * k] : 0u;
+        w[0][k] |= 2 * k + 1 < n ? (uint32_t)q[2 * k + 1] << 16 : 0u;
+    }
+}
+__device__ __forceinline__ void load_raw_part(const float *p, int n, u32x4 (&w)[2])
+{
+    const uint32_t *q = reinterpret_cast<const uint32_t *>(p);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        w[k / 4][k % 4] = k < n ? q[k] : 0u;
+}
+
 // The bf16 parts of eight values of dy: themselves, or the leading 8, middle
 // 8 and last 8 significant bits of each float (truncated, so that the rest
 // is exact; an inf or NaN stays in the first part alone).
-__device__ __forceinline__ void split(const float (&v)[8], u32x4 (&part)[1])
-{
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        part[0][k] = __float_as_uint(v[2 * k]) >> 16 | (__float_as_uint(v[2 * k + 1]) & 0xFFFF0000u);
-}
+__device__ __forceinline__ void split(const u32x4 (&w)[1], u32x4 (&part)[1]) { part[0] = w[0]; }
 
-__device__ __forceinline__ void split(const float (&v)[8], u32x4 (&part)[3])
+__device__ __forceinline__ void split(const u32x4 (&w)[2], u32x4 (&part)[3])
 {
     uint32_t b[3][8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const uint32_t u = __float_as_uint(v[k]);
+        const uint32_t u = w[k / 4][k % 4];
         b[0][k] = u & 0xFFFF0000u;
-        const float r1 = (u & 0x7F800000u) == 0x7F800000u ? 0.0f : v[k] - bits_f32(b[0][k]);
+        const float r1 = (u & 0x7F800000u) == 0x7F800000u ? 0.0f : bits_f32(u) - bits_f32(b[0][k]);
         b[1][k] = __float_as_uint(r1) & 0xFFFF0000u;
         b[2][k] = __float_as_uint(r1 - bits_f32(b[1][k]));
         if ((u & 0x7FFFFFFFu) > 0x7F800000u) // a NaN whose payload lies below the cut
@@ -53,8 +84,28 @@ __device__ __forceinline__ void split(const float (&v)[8], u32x4 (&part)[3])
 #pragma unroll
     for (int p = 0; p < 3; ++p)
 #pragma unroll
+        for (int k = 0; k < 4; ++k) // the upper halves of a pair
+            part[p][k] = __builtin_amdgcn_perm(b[p][2 * k + 1], b[p][2 * k], 0x07060302u);
+}
+
+// Eight codes as bf16.  A code + 128 is an unsigned byte, which one
+// instruction makes a float; (code + 128) step - 128 step is exact.
+__device__ __forceinline__ u32x4 decode8(u32x2 codes, uint32_t e)
+{
+    const float step = step_of(e), off = -128.0f * step;
+    u32x4 r;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t u = codes[h] ^ 0x80808080u;
+        float f[4];
+#pragma unroll
         for (int k = 0; k < 4; ++k)
-            part[p][k] = b[p][2 * k] >> 16 | (b[p][2 * k + 1] & 0xFFFF0000u);
+            f[k] = fmaf((float)((u >> (8 * k)) & 0xFFu), step, off);
+        r[2 * h] = __builtin_amdgcn_perm(__float_as_uint(f[1]), __float_as_uint(f[0]), 0x07060302u);
+        r[2 * h + 1] =
+            __builtin_amdgcn_perm(__float_as_uint(f[3]), __float_as_uint(f[2]), 0x07060302u);
+    }
+    return r;
 }
 
 __device__ __forceinline__ s16x8 read_fragment(const char *tile, int col)
@@ -67,69 +118,83 @@ __device__ __forceinline__ s16x8 read_fragment(const char *tile, int col)
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// One block: the 128 x 128 tile (blockIdx.x over n, blockIdx.y over k) of
-// the tokens [z chunk, (z + 1) chunk).  out: dw itself (one split) or the
-// z-th fp32 partial.
-template <typename T, typename O>
-__global__ __launch_bounds__(kWgThreads) void k_weight_grad(
-    const T *__restrict__ dy, int64_t m, int32_t n, int64_t lddy, Act8 x, int32_t k, int64_t chunk,
-    O *__restrict__ dw, O *__restrict__ db)
+struct Tiles {
+    int32_t n, k, total; // tiles along n and k, and blocks (times the splits)
+};
+
+// One block: a 128 x 128 tile of dw over the tokens of one split.  Its two
+// halves of four waves take 32 of each step's 64 tokens, a 64 x 64 quarter
+// of the tile a wave, and are added at the end.  out: dw itself (one split)
+// or the split's fp32 partial.  EDGE: the tile reaches past n or past the
+// codes' pitch.
+template <typename T, typename O, bool EDGE>
+__device__ __forceinline__ void weight_grad_tile(const T *__restrict__ dy, int64_t m, int32_t n,
+                                                 int64_t lddy, const Act8 &x, int32_t k,
+                                                 int64_t m_begin, int64_t m_end, int n0, int k0,
+                                                 O *__restrict__ out, O *__restrict__ db,
+                                                 char *lds)
 {
     constexpr int P = parts<T>();
-    __shared__ __align__(16) char lds[(P + 1) * kTileBytes];
-    char *const lds_b = lds + P * kTileBytes;
+    constexpr int kBufBytes = (P + 1) * kTileBytes;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int n0 = blockIdx.x * kTileN, k0 = blockIdx.y * kTileK;
-    const int wn = (wave & 1) * 64, wk = (wave >> 1) * 64;
-    const int64_t m_begin = (int64_t)blockIdx.z * chunk;
-    const int64_t m_end = m_begin + chunk < m ? m_begin + chunk : m;
-    const bool with_bias = db != nullptr && blockIdx.y == 0 && wk == 0;
+    const int half = wave >> 2, wn = (wave & 1) * 64, wk = ((wave >> 1) & 1) * 64;
+    const int steps = (int)((m_end - m_begin + kStepM - 1) / kStepM);
+    const bool with_bias = db != nullptr && k0 == 0 && wk == 0;
+    const int r = t / 16, c = (t % 16) * 8;
+    const int left = EDGE ? n - n0 - c : 8;              // columns of dy from here
+    const bool coded = !EDGE || k0 + c < x.pitch;        // and whether x has any
+    const T *const dy_at = dy + (left > 0 ? n0 + c : 0);
+    const int8_t *const codes_at = x.codes + (coded ? k0 + c : 0);
+    const uint8_t *const exps_at = x.exps + (coded ? (k0 + c) >> 5 : 0);
+
+    Loaded<T> reg[kAhead];
+    const auto load = [&](Loaded<T> &l, int s) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            // past the last token, that token again with a dy of 0
+            const int64_t want = m_begin + (int64_t)s * kStepM + r + 32 * i;
+            const int64_t row = want < m_end ? want : m_end - 1;
+            if (left >= 8)
+                load_raw(dy_at + row * lddy, l.a[i]);
+            else
+                load_raw_part(dy_at + row * lddy, left, l.a[i]);
+            if (want >= m_end)
+#pragma unroll
+                for (size_t h = 0; h < sizeof(T) / 2; ++h)
+                    l.a[i][h] = u32x4{0, 0, 0, 0};
+            l.b[i] = *reinterpret_cast<const u32x2 *>(codes_at + row * x.pitch);
+            l.e[i] = exps_at[row * x.groups];
+        }
+    };
+    const auto store = [&](const Loaded<T> &l, char *buf) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            char *const at = buf + (r + 32 * i) * kRowBytes + c * 2;
+            u32x4 part[P];
+            split(l.a[i], part);
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                *reinterpret_cast<u32x4 *>(at + p * kTileBytes) = part[p];
+            *reinterpret_cast<u32x4 *>(at + P * kTileBytes) = decode8(l.b[i], l.e[i]);
+        }
+    };
 
     f32x4 acc[4][4] = {}, bias[4] = {};
     s16x8 ones;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         ones[j] = 0x3F80;
-
-    for (int64_t m0 = m_begin; m0 < m_end; m0 += kTileM) {
-        // dy: rows t / 16 and 16 more, eight columns
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = t / 16 + 16 * i, c = (t % 16) * 8;
-            float v[8];
-            const int left = m0 + r < m_end ? n - n0 - c : 0;
-            load8(dy + (left > 0 ? (m0 + r) * lddy + n0 + c : 0), left, v);
-            u32x4 part[P];
-            split(v, part);
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-                *reinterpret_cast<u32x4 *>(lds + p * kTileBytes + r * kRowBytes + c * 2) = part[p];
-        }
-        // codes: row t / 8, sixteen columns (half a group)
-        {
-            const int r = t / 8, c = (t % 8) * 16;
-            float v[2][8] = {};
-            if (m0 + r < m_end && k0 + c < x.pitch) {
-                restore8(x, m0 + r, k0 + c, v[0]);
-                restore8(x, m0 + r, k0 + c + 8, v[1]);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                u32x4 part[1];
-                split(v[h], part);
-                *reinterpret_cast<u32x4 *>(lds_b + r * kRowBytes + (c + 8 * h) * 2) = part[0];
-            }
-        }
-        __syncthreads();
+    const auto multiply = [&](const char *buf) {
+        const char *const a = buf + half * 32 * kRowBytes, *const b = a + P * kTileBytes;
         s16x8 fb[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            fb[j] = read_fragment(lds_b, wk + 16 * j);
+            fb[j] = read_fragment(b, wk + 16 * j);
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const s16x8 fa = read_fragment(lds + p * kTileBytes, wn + 16 * i);
+                const s16x8 fa = read_fragment(a + p * kTileBytes, wn + 16 * i);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -140,27 +205,93 @@ __global__ __launch_bounds__(kWgThreads) void k_weight_grad(
                         __builtin_bit_cast(bf16x8, fa), __builtin_bit_cast(bf16x8, ones), bias[i],
                         0, 0, 0);
             }
+    };
+
+    // Step s + 2 is loaded, step s multiplied, and step s + 1 (loaded a step
+    // ago) decoded into the other buffer, which the barrier of step s - 1
+    // freed.
+    const auto step = [&](int s, int i) {
+        if (s + kAhead < steps)
+            load(reg[i], s + kAhead);
+        multiply(lds + i * kBufBytes);
+        if (s + 1 < steps)
+            store(reg[1 - i], lds + (1 - i) * kBufBytes);
+        __syncthreads();
+    };
+    if (steps > 0) {
+        load(reg[0], 0);
+        if (steps > 1)
+            load(reg[1], 1);
+        store(reg[0], lds);
         __syncthreads();
     }
+    for (int s = 0; s < steps; s += 2) {
+        step(s, 0);
+        if (s + 1 < steps)
+            step(s + 1, 1);
+    }
 
+    // The halves trade: each keeps two of the four rows of MFMA tiles and
+    // gets the other half's sums of them.
+    f32x4(*const trade)[4][2][5][64] = reinterpret_cast<f32x4(*)[4][2][5][64]>(lds);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        f32x4(*const to)[64] = trade[half][wave & 3][i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            to[j][lane] = half ? acc[i][j] : acc[2 + i][j];
+        if (with_bias)
+            to[4][lane] = half ? bias[i] : bias[2 + i];
+    }
+    __syncthreads();
     // lane l holds rows 4 (l / 16) + {0..3} of column l % 16
-    O *const out = dw + (int64_t)blockIdx.z * n * k;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i) {
+        f32x4(*const from)[64] = trade[1 - half][wave & 3][i];
+        const int row0 = n0 + wn + 16 * (2 * half + i) + 4 * (lane >> 4);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = n0 + wn + 16 * i + 4 * (lane >> 4) + r;
-            if (row >= n)
-                continue;
+        for (int j = 0; j < 4; ++j) {
+            const f32x4 v = (half ? acc[2 + i][j] : acc[i][j]) + from[j][lane];
+            const int col = k0 + wk + 16 * j + (lane & 15);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int col = k0 + wk + 16 * j + (lane & 15);
-                if (col < k)
-                    out[(int64_t)row * k + col] = (O)acc[i][j][r];
-            }
-            if (with_bias && (lane & 15) == 0)
-                db[(int64_t)blockIdx.z * n + row] = (O)bias[i][r];
+            for (int e = 0; e < 4; ++e)
+                if (row0 + e < n && col < k)
+                    out[(int64_t)(row0 + e) * k + col] = (O)v[e];
         }
+        if (with_bias) {
+            const f32x4 v = (half ? bias[2 + i] : bias[i]) + from[4][lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (row0 + e < n && (lane & 15) == 0)
+                    db[row0 + e] = (O)v[e];
+        }
+    }
+}
+
+template <typename T, typename O>
+__global__ __launch_bounds__(kWgThreads) void k_weight_grad(
+    const T *__restrict__ dy, int64_t m, int32_t n, int64_t lddy, Act8 x, int32_t k, int64_t chunk,
+    Tiles tiles, O *__restrict__ dw, O *__restrict__ db)
+{
+    constexpr int kBufBytes = 2 * (parts<T>() + 1) * kTileBytes;
+    constexpr int kTradeBytes = 2 * 4 * 2 * 5 * 64 * 16; // the halves' sums
+    __shared__ __align__(16) char lds[kBufBytes > kTradeBytes ? kBufBytes : kTradeBytes];
+    // Blocks go to the 8 XCDs in turn; each XCD takes a contiguous run of
+    // tiles, k fastest, so that its L2 holds the rows of dy they share.
+    const int xcd = blockIdx.x % 8, q = tiles.total / 8, rem = tiles.total % 8;
+    const int tile = xcd * q + min(xcd, rem) + blockIdx.x / 8;
+    const int tk = tile % tiles.k, tn = tile / tiles.k % tiles.n, z = tile / tiles.k / tiles.n;
+    const int n0 = tn * kTileN, k0 = tk * kTileK;
+    const int64_t m_begin = (int64_t)z * chunk;
+    const int64_t m_end = m_begin + chunk < m ? m_begin + chunk : m;
+    O *const out = dw + (int64_t)z * n * k;
+    O *const out_b = db ? db + (int64_t)z * n : nullptr;
+    if (n0 + kTileN <= n && k0 + kTileK <= x.pitch)
+        weight_grad_tile<T, O, false>(dy, m, n, lddy, x, k, m_begin, m_end, n0, k0, out, out_b,
+                                      lds);
+    else
+        weight_grad_tile<T, O, true>(dy, m, n, lddy, x, k, m_begin, m_end, n0, k0, out, out_b,
+                                     lds);
 }
 
 // Adds `splits` partials in order: count values of dw (or db).
@@ -177,7 +308,7 @@ __global__ __launch_bounds__(256) void k_sum_splits(const float *__restrict__ pa
     out[i] = (O)s;
 }
 
-// How the tokens are split: enough blocks for two per CU, chunks of at least
+// How the tokens are split: enough blocks for every CU, chunks of at least
 // 256 tokens.
 struct Split {
     int32_t splits;
@@ -186,16 +317,16 @@ struct Split {
 Split split_of(int64_t m, int64_t n, int64_t k)
 {
     const int64_t tiles = ((n + kTileN - 1) / kTileN) * ((k + kTileK - 1) / kTileK);
-    int64_t s = 512 / tiles;
+    int64_t s = 256 / tiles;
     if (s > (m + 255) / 256)
         s = (m + 255) / 256;
     if (s < 1)
         s = 1;
     Split r;
     r.chunk = (m + s - 1) / s;
-    r.chunk = (r.chunk + kTileM - 1) / kTileM * kTileM;
-    if (r.chunk < kTileM)
-        r.chunk = kTileM;
+    r.chunk = (r.chunk + kStepM - 1) / kStepM * kStepM;
+    if (r.chunk < kStepM)
+        r.chunk = kStepM;
     r.splits = (int32_t)((m + r.chunk - 1) / r.chunk);
     if (r.splits < 1)
         r.splits = 1;
@@ -213,20 +344,22 @@ int32_t launch(const void *dy, int64_t m, int32_t n, int64_t lddy, const Act8 &x
                void *dw, void *db, int32_t wdtype, float *ws, hipStream_t st)
 {
     const Split s = split_of(m, n, k);
-    const dim3 grid((n + kTileN - 1) / kTileN, (k + kTileK - 1) / kTileK, s.splits);
+    Tiles tiles{(n + kTileN - 1) / kTileN, (k + kTileK - 1) / kTileK, 0};
+    tiles.total = tiles.n * tiles.k * s.splits; // n k < 2^40: below 2^26 tiles, split or not
+    const dim3 grid((uint32_t)tiles.total);
     const T *dyt = (const T *)dy;
     if (s.splits == 1) {
         if (wdtype == GQ_IN_F32)
-            k_weight_grad<T, float><<<grid, kWgThreads, 0, st>>>(dyt, m, n, lddy, x, k, s.chunk,
+            k_weight_grad<T, float><<<grid, kWgThreads, 0, st>>>(dyt, m, n, lddy, x, k, s.chunk, tiles,
                                                                  (float *)dw, (float *)db);
         else
-            k_weight_grad<T, bf16><<<grid, kWgThreads, 0, st>>>(dyt, m, n, lddy, x, k, s.chunk,
+            k_weight_grad<T, bf16><<<grid, kWgThreads, 0, st>>>(dyt, m, n, lddy, x, k, s.chunk, tiles,
                                                                 (bf16 *)dw, (bf16 *)db);
         return check_launch("k_weight_grad");
     }
     const int64_t count = (int64_t)n * k;
     float *const db_part = ws + s.splits * count;
-    k_weight_grad<T, float><<<grid, kWgThreads, 0, st>>>(dyt, m, n, lddy, x, k, s.chunk, ws,
+    k_weight_grad<T, float><<<grid, kWgThreads, 0, st>>>(dyt, m, n, lddy, x, k, s.chunk, tiles, ws,
                                                          db ? db_part : nullptr);
     GQT_TRY(check_launch("k_weight_grad"));
     const auto blocks = [](int64_t c) { return dim3((uint32_t)((c + 255) / 256)); };
