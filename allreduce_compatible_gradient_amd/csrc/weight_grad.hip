@@ -19,7 +19,6 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 constexpr int kTileN = 128, kTileK = 128; // output tile: rows of dw, columns of dw
 constexpr int kStepM = 64;                // tokens per step: 32 for each half of the waves
 constexpr int kWgThreads = 512;
-constexpr int kAhead = 2; // steps whose loads are in flight
 // LDS rows of 128 bf16 lie 288 bytes apart: a transposed read takes 32 bytes
 // of each of 16 rows, which then fall into all banks evenly.
 constexpr int kRowBytes = 288;
@@ -125,57 +124,83 @@ struct Tiles {
 // One block: a 128 x 128 tile of dw over the tokens of one split.  Its two
 // halves of four waves take 32 of each step's 64 tokens, a 64 x 64 quarter
 // of the tile a wave, and are added at the end.  out: dw itself (one split)
-// or the split's fp32 partial.  EDGE: the tile reaches past n or past the
-// codes' pitch.
-template <typename T, typename O, bool EDGE>
-__device__ __forceinline__ void weight_grad_tile(const T *__restrict__ dy, int64_t m, int32_t n,
-                                                 int64_t lddy, const Act8 &x, int32_t k,
-                                                 int64_t m_begin, int64_t m_end, int n0, int k0,
+// or the split's fp32 partial.  BIAS: the tile also sums dy's rows, as a
+// product with ones.
+//
+// Columns of the tile past n or past the codes' pitch may hold anything:
+// they reach only values of dw that are not stored.  So every lane loads
+// eight columns that exist, and the lane whose eight would end past n loads
+// the row's last eight and places them one by one.
+template <typename T, typename O, bool BIAS>
+__device__ __forceinline__ void weight_grad_tile(const T *__restrict__ dy, int32_t n, int64_t lddy,
+                                                 const Act8 &x, int32_t k, int64_t m_begin,
+                                                 int64_t m_end, int n0, int k0,
                                                  O *__restrict__ out, O *__restrict__ db,
                                                  char *lds)
 {
     constexpr int P = parts<T>();
     constexpr int kBufBytes = (P + 1) * kTileBytes;
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int t = threadIdx.x, lane = t & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int half = wave >> 2, wn = (wave & 1) * 64, wk = ((wave >> 1) & 1) * 64;
-    const int steps = (int)((m_end - m_begin + kStepM - 1) / kStepM);
-    const bool with_bias = db != nullptr && k0 == 0 && wk == 0;
     const int r = t / 16, c = (t % 16) * 8;
-    const int left = EDGE ? n - n0 - c : 8;              // columns of dy from here
-    const bool coded = !EDGE || k0 + c < x.pitch;        // and whether x has any
-    const T *const dy_at = dy + (left > 0 ? n0 + c : 0);
-    const int8_t *const codes_at = x.codes + (coded ? k0 + c : 0);
-    const uint8_t *const exps_at = x.exps + (coded ? (k0 + c) >> 5 : 0);
+    const int left = n - n0 - c;
+    const bool odd = left > 0 && left < 8; // eight columns from n - 8, from column `from` of the tile
+    const int from = n - 8 - n0;
+    const int dy_col = n < 8 ? 0 : odd ? n - 8 : left > 0 ? n0 + c : 0;
+    const int code_col = k0 + c < x.pitch ? k0 + c : 0;
 
-    Loaded<T> reg[kAhead];
-    const auto load = [&](Loaded<T> &l, int s) {
+    const auto load_dy = [&](Loaded<T> &l, int i, int64_t row) {
+        const T *const p = dy + row * lddy + dy_col;
+        if (n >= 8)
+            load_raw(p, l.a[i]);
+        else
+            load_raw_part(p, n, l.a[i]);
+    };
+    const auto load_codes = [&](Loaded<T> &l, int i, int64_t row) {
+        l.b[i] = *reinterpret_cast<const u32x2 *>(x.codes + row * x.pitch + code_col);
+        l.e[i] = x.exps[row * x.groups + (code_col >> 5)];
+    };
+    const auto load = [&](Loaded<T> &l, int64_t m0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            // past the last token, that token again with a dy of 0
-            const int64_t want = m_begin + (int64_t)s * kStepM + r + 32 * i;
-            const int64_t row = want < m_end ? want : m_end - 1;
-            if (left >= 8)
-                load_raw(dy_at + row * lddy, l.a[i]);
-            else
-                load_raw_part(dy_at + row * lddy, left, l.a[i]);
+            load_dy(l, i, m0 + r + 32 * i);
+            load_codes(l, i, m0 + r + 32 * i);
+        }
+    };
+    // the last step: past the last token, that token again with a dy of 0
+    const auto load_tail = [&](Loaded<T> &l, int64_t m0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int64_t want = m0 + r + 32 * i, row = want < m_end ? want : m_end - 1;
+            load_dy(l, i, row);
+            load_codes(l, i, row);
             if (want >= m_end)
 #pragma unroll
                 for (size_t h = 0; h < sizeof(T) / 2; ++h)
                     l.a[i][h] = u32x4{0, 0, 0, 0};
-            l.b[i] = *reinterpret_cast<const u32x2 *>(codes_at + row * x.pitch);
-            l.e[i] = exps_at[row * x.groups];
         }
     };
     const auto store = [&](const Loaded<T> &l, char *buf) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            char *const at = buf + (r + 32 * i) * kRowBytes + c * 2;
+            char *const at = buf + (r + 32 * i) * kRowBytes;
             u32x4 part[P];
             split(l.a[i], part);
+            if (odd && n >= 8) {
 #pragma unroll
-            for (int p = 0; p < P; ++p)
-                *reinterpret_cast<u32x4 *>(at + p * kTileBytes) = part[p];
-            *reinterpret_cast<u32x4 *>(at + P * kTileBytes) = decode8(l.b[i], l.e[i]);
+                for (int p = 0; p < P; ++p)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (from + e >= 0)
+                            *reinterpret_cast<uint16_t *>(at + p * kTileBytes + (from + e) * 2) =
+                                (uint16_t)(part[p][e / 2] >> (16 * (e % 2)));
+            } else {
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+                    *reinterpret_cast<u32x4 *>(at + p * kTileBytes + c * 2) = part[p];
+            }
+            *reinterpret_cast<u32x4 *>(at + P * kTileBytes + c * 2) = decode8(l.b[i], l.e[i]);
         }
     };
 
@@ -191,37 +216,43 @@ __device__ __forceinline__ void weight_grad_tile(const T *__restrict__ dy, int64
         for (int j = 0; j < 4; ++j)
             fb[j] = read_fragment(b, wk + 16 * j);
 #pragma unroll
-        for (int p = 0; p < P; ++p)
+        for (int p = 0; p < P; ++p) {
+            s16x8 fa[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                fa[i] = read_fragment(a + p * kTileBytes, wn + 16 * i);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const s16x8 fa = read_fragment(a + p * kTileBytes, wn + 16 * i);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        __builtin_bit_cast(bf16x8, fa), __builtin_bit_cast(bf16x8, fb[j]),
+                        __builtin_bit_cast(bf16x8, fa[i]), __builtin_bit_cast(bf16x8, fb[j]),
                         acc[i][j], 0, 0, 0);
-                if (with_bias)
+                if (BIAS)
                     bias[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        __builtin_bit_cast(bf16x8, fa), __builtin_bit_cast(bf16x8, ones), bias[i],
-                        0, 0, 0);
+                        __builtin_bit_cast(bf16x8, fa[i]), __builtin_bit_cast(bf16x8, ones),
+                        bias[i], 0, 0, 0);
             }
+        }
     };
 
     // Step s + 2 is loaded, step s multiplied, and step s + 1 (loaded a step
     // ago) decoded into the other buffer, which the barrier of step s - 1
-    // freed.
+    // freed.  Tokens that do not fill a step come last, on their own.
+    const int steps = (int)((m_end - m_begin) / kStepM);
+    Loaded<T> reg[2];
     const auto step = [&](int s, int i) {
-        if (s + kAhead < steps)
-            load(reg[i], s + kAhead);
+        if (s + 2 < steps)
+            load(reg[i], m_begin + (int64_t)(s + 2) * kStepM);
         multiply(lds + i * kBufBytes);
         if (s + 1 < steps)
             store(reg[1 - i], lds + (1 - i) * kBufBytes);
         __syncthreads();
     };
     if (steps > 0) {
-        load(reg[0], 0);
+        load(reg[0], m_begin);
         if (steps > 1)
-            load(reg[1], 1);
+            load(reg[1], m_begin + kStepM);
         store(reg[0], lds);
         __syncthreads();
     }
@@ -229,6 +260,13 @@ __device__ __forceinline__ void weight_grad_tile(const T *__restrict__ dy, int64
         step(s, 0);
         if (s + 1 < steps)
             step(s + 1, 1);
+    }
+    if (m_begin + (int64_t)steps * kStepM < m_end) {
+        load_tail(reg[0], m_begin + (int64_t)steps * kStepM);
+        store(reg[0], lds);
+        __syncthreads();
+        multiply(lds);
+        __syncthreads();
     }
 
     // The halves trade: each keeps two of the four rows of MFMA tiles and
@@ -240,7 +278,7 @@ __device__ __forceinline__ void weight_grad_tile(const T *__restrict__ dy, int64
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             to[j][lane] = half ? acc[i][j] : acc[2 + i][j];
-        if (with_bias)
+        if (BIAS)
             to[4][lane] = half ? bias[i] : bias[2 + i];
     }
     __syncthreads();
@@ -258,7 +296,7 @@ __device__ __forceinline__ void weight_grad_tile(const T *__restrict__ dy, int64
                 if (row0 + e < n && col < k)
                     out[(int64_t)(row0 + e) * k + col] = (O)v[e];
         }
-        if (with_bias) {
+        if (BIAS && wk == 0) {
             const f32x4 v = (half ? bias[2 + i] : bias[i]) + from[4][lane];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -286,12 +324,10 @@ __global__ __launch_bounds__(kWgThreads) void k_weight_grad(
     const int64_t m_end = m_begin + chunk < m ? m_begin + chunk : m;
     O *const out = dw + (int64_t)z * n * k;
     O *const out_b = db ? db + (int64_t)z * n : nullptr;
-    if (n0 + kTileN <= n && k0 + kTileK <= x.pitch)
-        weight_grad_tile<T, O, false>(dy, m, n, lddy, x, k, m_begin, m_end, n0, k0, out, out_b,
-                                      lds);
+    if (out_b && tk == 0)
+        weight_grad_tile<T, O, true>(dy, n, lddy, x, k, m_begin, m_end, n0, k0, out, out_b, lds);
     else
-        weight_grad_tile<T, O, true>(dy, m, n, lddy, x, k, m_begin, m_end, n0, k0, out, out_b,
-                                     lds);
+        weight_grad_tile<T, O, false>(dy, n, lddy, x, k, m_begin, m_end, n0, k0, out, out_b, lds);
 }
 
 // Adds `splits` partials in order: count values of dw (or db).
