@@ -1,372 +1,550 @@
 // weight_grad.hip -- dw = dy^T x and db of a linear layer on MI355X (gfx950),
 // with x in the 8-bit format of include/gq_train.h.
 //
-// Both operands are stored with the reduced axis (the tokens) outermost, so
-// a wave's MFMA fragments, eight consecutive tokens of one column, are
-// transposed reads of row-major LDS tiles (ds_read_b64_tr_b16).  A code times
-// its group's power of two is exact in bf16, so the codes become bf16 on
-// their way into LDS and one bf16 MFMA per tile serves a bf16 dy; an fp32 dy
-// is the exact sum of three bf16 parts and takes three.  All sums are fp32.
+// Both operands are stored with the summed axis (the tokens) outermost, and
+// an MFMA fragment is eight tokens of one column.  No transposing through
+// LDS is needed for that: a lane that loads eight columns of eight tokens
+// holds, column by column, eight fragments' parts, and which of the 16 rows
+// or columns of an MFMA stands for which column of the matrix is free.  So
+// lane i of a row of 16 takes columns 8 i to 8 i + 7; fragment c is column
+// 8 i + c, put together by four byte permutes of pairs of tokens (dy), or by
+// the permutes that narrow the decoded codes to bf16 (x).  A code times its
+// group's power of two is exact in bf16; an fp32 dy is the exact sum of three
+// bf16 parts and takes three MFMAs.  All sums are fp32.
 #include "train_common.h"
 
 namespace gqt {
 namespace {
 
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+constexpr int kTile = 128;  // output tile: 128 rows and 128 columns of dw
+constexpr int kWaves = 4;   // one per SIMD: a wave's sums take half its registers
+constexpr int kWaveM = 32;  // tokens of a wave in a step: the depth of one MFMA
+constexpr int kStepM = kWaves * kWaveM;
+constexpr int kThreads = 64 * kWaves;
 
-constexpr int kTileN = 128, kTileK = 128; // output tile: rows of dw, columns of dw
-constexpr int kStepM = 64;                // tokens per step: 32 for each half of the waves
-constexpr int kWgThreads = 512;
-// LDS rows of 128 bf16 lie 288 bytes apart: a transposed read takes 32 bytes
-// of each of 16 rows, which then fall into all banks evenly.
-constexpr int kRowBytes = 288;
-constexpr int kTileBytes = kStepM * kRowBytes;
+#define GQT_INLINE __attribute__((always_inline))
+
+typedef uint32_t u32_e1 __attribute__((aligned(1)));
 
 template <typename T>
 constexpr int parts() { return sizeof(T) == 4 ? 3 : 1; }
 
-// One thread's share of a step as loaded: rows r and r + 32, eight columns.
+// Eight tokens of eight columns of dy as loaded: token j in a[j].
 template <typename T>
-struct Loaded {
-    u32x4 a[2][sizeof(T) / 2];
-    u32x2 b[2];
-    uint32_t e[2];
+struct RawDy {
+    u32x4 a[8][sizeof(T) / 2];
+};
+// and of x: codes, and a word whose top byte is the group's exponent
+struct RawX {
+    u32x2 b[8];
+    uint32_t e[8];
 };
 
-__device__ __forceinline__ void load_raw(const bf16 *p, u32x4 (&w)[1])
+__device__ __forceinline__ u32x4 load16(const bf16 *p)
 {
-    w[0] = *reinterpret_cast<const u32x4_e2 *>(p);
+    return *reinterpret_cast<const u32x4_e2 *>(p);
 }
-__device__ __forceinline__ void load_raw(const float *p, u32x4 (&w)[2])
+__device__ __forceinline__ u32x4 load16(const float *p)
 {
-    w[0] = *reinterpret_cast<const u32x4_e4 *>(p);
-    w[1] = *reinterpret_cast<const u32x4_e4 *>(p + 4);
+    return *reinterpret_cast<const u32x4_e4 *>(p);
 }
-// the first n elements, the others 0
-__device__ __forceinline__ void load_raw_part(const bf16 *p, int n, u32x4 (&w)[1])
+// the upper halves of a pair of words
+__device__ __forceinline__ uint32_t upper_halves(uint32_t lo, uint32_t hi)
 {
-    const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        w[0][k] = 2 * k < n ? q[2 * k] : 0u;
-        w[0][k] |= 2 * k + 1 < n ? (uint32_t)q[2 * k + 1] << 16 : 0u;
-    }
-}
-__device__ __forceinline__ void load_raw_part(const float *p, int n, u32x4 (&w)[2])
-{
-    const uint32_t *q = reinterpret_cast<const uint32_t *>(p);
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        w[k / 4][k % 4] = k < n ? q[k] : 0u;
+    return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
 }
 
-// The bf16 parts of eight values of dy: themselves, or the leading 8, middle
-// 8 and last 8 significant bits of each float (truncated, so that the rest
-// is exact; an inf or NaN stays in the first part alone).
-__device__ __forceinline__ void split(const u32x4 (&w)[1], u32x4 (&part)[1]) { part[0] = w[0]; }
+__device__ __forceinline__ bf16x8 as_fragment(u32x4 w) { return __builtin_bit_cast(bf16x8, w); }
 
-__device__ __forceinline__ void split(const u32x4 (&w)[2], u32x4 (&part)[3])
+// Fragment c of dy in its bf16 parts.
+__device__ __forceinline__ void dy_fragment(const RawDy<bf16> &l, int c, u32x4 (&part)[1])
+{
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+        part[0][h] = __builtin_amdgcn_perm(l.a[2 * h + 1][0][c / 2], l.a[2 * h][0][c / 2],
+                                           c % 2 ? 0x07060302u : 0x05040100u);
+}
+
+// A float's leading 8, middle 8 and last 8 significant bits: truncated, so
+// that each rest is exact; an inf or NaN (made quiet, which keeps it one)
+// stays in the first part alone.
+__device__ __forceinline__ void dy_fragment(const RawDy<float> &l, int c, u32x4 (&part)[3])
 {
     uint32_t b[3][8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const uint32_t u = w[k / 4][k % 4];
-        b[0][k] = u & 0xFFFF0000u;
-        const float r1 = (u & 0x7F800000u) == 0x7F800000u ? 0.0f : bits_f32(u) - bits_f32(b[0][k]);
-        b[1][k] = __float_as_uint(r1) & 0xFFFF0000u;
-        b[2][k] = __float_as_uint(r1 - bits_f32(b[1][k]));
-        if ((u & 0x7FFFFFFFu) > 0x7F800000u) // a NaN whose payload lies below the cut
-            b[0][k] = 0x7FC00000u;
+    for (int j = 0; j < 8; ++j) {
+        const float v = __builtin_canonicalizef(bits_f32(l.a[j][c / 4][c % 4]));
+        b[0][j] = __float_as_uint(v);
+        const float rest = v - bits_f32(b[0][j] & 0xFFFF0000u);
+        const float r1 = __builtin_isfinite(v) ? rest : 0.0f;
+        b[1][j] = __float_as_uint(r1);
+        b[2][j] = __float_as_uint(r1 - bits_f32(b[1][j] & 0xFFFF0000u));
     }
 #pragma unroll
     for (int p = 0; p < 3; ++p)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) // the upper halves of a pair
-            part[p][k] = __builtin_amdgcn_perm(b[p][2 * k + 1], b[p][2 * k], 0x07060302u);
+        for (int h = 0; h < 4; ++h)
+            part[p][h] = upper_halves(b[p][2 * h], b[p][2 * h + 1]);
 }
 
-// Eight codes as bf16.  A code + 128 is an unsigned byte, which one
-// instruction makes a float; (code + 128) step - 128 step is exact.
-__device__ __forceinline__ u32x4 decode8(u32x2 codes, uint32_t e)
+// Adds the eight tokens of each column to its sum.
+__device__ __forceinline__ void add_tokens(const RawDy<bf16> &l, float (&sum)[8])
 {
-    const float step = step_of(e), off = -128.0f * step;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            sum[2 * c] += bits_f32(l.a[j][0][c] << 16);
+            sum[2 * c + 1] += bits_f32(l.a[j][0][c] & 0xFFFF0000u);
+        }
+}
+__device__ __forceinline__ void add_tokens(const RawDy<float> &l, float (&sum)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            sum[c] += bits_f32(l.a[j][c / 4][c % 4]);
+}
+
+// The eight tokens' codes and scales: code + 128 is an unsigned byte, which one
+// instruction makes a float, and (code + 128) step - 128 step is exact.  The
+// exponent byte 255 gives an infinite step, and inf - inf is the NaN it stands
+// for.
+struct Biased {
+    u32x2 b[8]; // codes + 128
+    float step[8], off[8];
+};
+__device__ __forceinline__ Biased biased(const RawX &l)
+{
+    Biased s;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        // in assembly, so that the compiler does not flip each byte by itself
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            asm("v_xor_b32 %0, %1, %2" : "=v"(s.b[j][h]) : "s"(0x80808080u), "v"(l.b[j][h]));
+        s.step[j] = bits_f32((l.e[j] >> 1) & 0x7F800000u);
+        s.off[j] = -128.0f * s.step[j];
+    }
+    return s;
+}
+
+// Fragment c of x.
+__device__ __forceinline__ u32x4 x_fragment(const Biased &s, int c)
+{
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t u = s.b[j][c / 4];
+        f[j] = fmaf((float)((u >> (8 * (c % 4))) & 0xFFu), s.step[j], s.off[j]);
+    }
     u32x4 r;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t u = codes[h] ^ 0x80808080u;
-        float f[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            f[k] = fmaf((float)((u >> (8 * k)) & 0xFFu), step, off);
-        r[2 * h] = __builtin_amdgcn_perm(__float_as_uint(f[1]), __float_as_uint(f[0]), 0x07060302u);
-        r[2 * h + 1] =
-            __builtin_amdgcn_perm(__float_as_uint(f[3]), __float_as_uint(f[2]), 0x07060302u);
-    }
+    for (int h = 0; h < 4; ++h)
+        r[h] = upper_halves(__float_as_uint(f[2 * h]), __float_as_uint(f[2 * h + 1]));
     return r;
 }
 
-__device__ __forceinline__ s16x8 read_fragment(const char *tile, int col)
+__device__ __forceinline__ void decode(const RawX &l, u32x4 (&f)[8])
 {
-    // lane l reads columns col + l % 16, tokens 4 (l / 16) + {0..3} and 16 more
-    const int lane = threadIdx.x & 63;
-    const char *p = tile + (lane >> 2) * kRowBytes + (col + (lane & 3) * 4) * 2;
-    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 16 * kRowBytes));
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    const Biased l8 = biased(l);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        f[c] = x_fragment(l8, c);
+}
+
+// Asks the scheduler for MFMAS times one MFMA and VALU vector instructions,
+// and keeps what follows behind them: left alone it brings all the decoding
+// forward and runs out of registers.
+template <int MFMAS, int VALU>
+__device__ __forceinline__ void interleave()
+{
+#pragma unroll
+    for (int i = 0; i < MFMAS; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 struct Tiles {
     int32_t n, k, total; // tiles along n and k, and blocks (times the splits)
 };
 
-// One block: a 128 x 128 tile of dw over the tokens of one split.  Its two
-// halves of four waves take 32 of each step's 64 tokens, a 64 x 64 quarter
-// of the tile a wave, and are added at the end.  out: dw itself (one split)
-// or the split's fp32 partial.  BIAS: the tile also sums dy's rows, as a
-// product with ones.
+// One block: a 128 x 128 tile of dw over the tokens of one split, each wave
+// the whole tile over 32 of a step's 128 tokens; the waves' sums are added
+// at the end.  out: dw itself (one split) or the split's fp32 partial.
 //
-// Columns of the tile past n or past the codes' pitch may hold anything:
-// they reach only values of dw that are not stored.  So every lane loads
-// eight columns that exist, and the lane whose eight would end past n loads
-// the row's last eight and places them one by one.
-template <typename T, typename O, bool BIAS>
-__device__ __forceinline__ void weight_grad_tile(const T *__restrict__ dy, int32_t n, int64_t lddy,
-                                                 const Act8 &x, int32_t k, int64_t m_begin,
-                                                 int64_t m_end, int n0, int k0,
-                                                 O *__restrict__ out, O *__restrict__ db,
-                                                 char *lds)
-{
-    constexpr int P = parts<T>();
-    constexpr int kBufBytes = (P + 1) * kTileBytes;
-    const int t = threadIdx.x, lane = t & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int half = wave >> 2, wn = (wave & 1) * 64, wk = ((wave >> 1) & 1) * 64;
-    const int r = t / 16, c = (t % 16) * 8;
-    const int left = n - n0 - c;
-    const bool odd = left > 0 && left < 8; // eight columns from n - 8, from column `from` of the tile
-    const int from = n - 8 - n0;
-    const int dy_col = n < 8 ? 0 : odd ? n - 8 : left > 0 ? n0 + c : 0;
-    const int code_col = k0 + c < x.pitch ? k0 + c : 0;
-
-    const auto load_dy = [&](Loaded<T> &l, int i, int64_t row) {
-        const T *const p = dy + row * lddy + dy_col;
-        if (n >= 8)
-            load_raw(p, l.a[i]);
-        else
-            load_raw_part(p, n, l.a[i]);
-    };
-    const auto load_codes = [&](Loaded<T> &l, int i, int64_t row) {
-        l.b[i] = *reinterpret_cast<const u32x2 *>(x.codes + row * x.pitch + code_col);
-        l.e[i] = x.exps[row * x.groups + (code_col >> 5)];
-    };
-    const auto load = [&](Loaded<T> &l, int64_t m0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            load_dy(l, i, m0 + r + 32 * i);
-            load_codes(l, i, m0 + r + 32 * i);
-        }
-    };
-    // the last step: past the last token, that token again with a dy of 0
-    const auto load_tail = [&](Loaded<T> &l, int64_t m0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int64_t want = m0 + r + 32 * i, row = want < m_end ? want : m_end - 1;
-            load_dy(l, i, row);
-            load_codes(l, i, row);
-            if (want >= m_end)
-#pragma unroll
-                for (size_t h = 0; h < sizeof(T) / 2; ++h)
-                    l.a[i][h] = u32x4{0, 0, 0, 0};
-        }
-    };
-    const auto store = [&](const Loaded<T> &l, char *buf) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            char *const at = buf + (r + 32 * i) * kRowBytes;
-            u32x4 part[P];
-            split(l.a[i], part);
-            if (odd && n >= 8) {
-#pragma unroll
-                for (int p = 0; p < P; ++p)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (from + e >= 0)
-                            *reinterpret_cast<uint16_t *>(at + p * kTileBytes + (from + e) * 2) =
-                                (uint16_t)(part[p][e / 2] >> (16 * (e % 2)));
-            } else {
-#pragma unroll
-                for (int p = 0; p < P; ++p)
-                    *reinterpret_cast<u32x4 *>(at + p * kTileBytes + c * 2) = part[p];
-            }
-            *reinterpret_cast<u32x4 *>(at + P * kTileBytes + c * 2) = decode8(l.b[i], l.e[i]);
-        }
-    };
-
-    f32x4 acc[4][4] = {}, bias[4] = {};
-    s16x8 ones;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        ones[j] = 0x3F80;
-    const auto multiply = [&](const char *buf) {
-        const char *const a = buf + half * 32 * kRowBytes, *const b = a + P * kTileBytes;
-        s16x8 fb[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            fb[j] = read_fragment(b, wk + 16 * j);
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            s16x8 fa[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                fa[i] = read_fragment(a + p * kTileBytes, wn + 16 * i);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        __builtin_bit_cast(bf16x8, fa[i]), __builtin_bit_cast(bf16x8, fb[j]),
-                        acc[i][j], 0, 0, 0);
-                if (BIAS)
-                    bias[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        __builtin_bit_cast(bf16x8, fa[i]), __builtin_bit_cast(bf16x8, ones),
-                        bias[i], 0, 0, 0);
-            }
-        }
-    };
-
-    // Step s + 2 is loaded, step s multiplied, and step s + 1 (loaded a step
-    // ago) decoded into the other buffer, which the barrier of step s - 1
-    // freed.  Tokens that do not fill a step come last, on their own.
-    const int steps = (int)((m_end - m_begin) / kStepM);
-    Loaded<T> reg[2];
-    const auto step = [&](int s, int i) {
-        if (s + 2 < steps)
-            load(reg[i], m_begin + (int64_t)(s + 2) * kStepM);
-        multiply(lds + i * kBufBytes);
-        if (s + 1 < steps)
-            store(reg[1 - i], lds + (1 - i) * kBufBytes);
-        __syncthreads();
-    };
-    if (steps > 0) {
-        load(reg[0], m_begin);
-        if (steps > 1)
-            load(reg[1], m_begin + kStepM);
-        store(reg[0], lds);
-        __syncthreads();
-    }
-    for (int s = 0; s < steps; s += 2) {
-        step(s, 0);
-        if (s + 1 < steps)
-            step(s + 1, 1);
-    }
-    if (m_begin + (int64_t)steps * kStepM < m_end) {
-        load_tail(reg[0], m_begin + (int64_t)steps * kStepM);
-        store(reg[0], lds);
-        __syncthreads();
-        multiply(lds);
-        __syncthreads();
-    }
-
-    // The halves trade: each keeps two of the four rows of MFMA tiles and
-    // gets the other half's sums of them.
-    f32x4(*const trade)[4][2][5][64] = reinterpret_cast<f32x4(*)[4][2][5][64]>(lds);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        f32x4(*const to)[64] = trade[half][wave & 3][i];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            to[j][lane] = half ? acc[i][j] : acc[2 + i][j];
-        if (BIAS)
-            to[4][lane] = half ? bias[i] : bias[2 + i];
-    }
-    __syncthreads();
-    // lane l holds rows 4 (l / 16) + {0..3} of column l % 16
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        f32x4(*const from)[64] = trade[1 - half][wave & 3][i];
-        const int row0 = n0 + wn + 16 * (2 * half + i) + 4 * (lane >> 4);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const f32x4 v = (half ? acc[2 + i][j] : acc[i][j]) + from[j][lane];
-            const int col = k0 + wk + 16 * j + (lane & 15);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (row0 + e < n && col < k)
-                    out[(int64_t)(row0 + e) * k + col] = (O)v[e];
-        }
-        if (BIAS && wk == 0) {
-            const f32x4 v = (half ? bias[2 + i] : bias[i]) + from[4][lane];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (row0 + e < n && (lane & 15) == 0)
-                    db[row0 + e] = (O)v[e];
-        }
-    }
-}
-
+// Rows of the tile past n, and columns past the codes' pitch, are not
+// stored, so what they hold is free: every lane loads eight columns that
+// exist.  The lane whose eight would end past n (n >= 8) takes the last eight
+// of the row, and so computes some rows that its neighbour stores.
+//
+// db: the tiles.k tiles that share a tile's columns of dy take turns at
+// adding up its steps, so that none is slower than the others; each leaves a
+// partial.
 template <typename T, typename O>
-__global__ __launch_bounds__(kWgThreads) void k_weight_grad(
+__global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
     const T *__restrict__ dy, int64_t m, int32_t n, int64_t lddy, Act8 x, int32_t k, int64_t chunk,
-    Tiles tiles, O *__restrict__ dw, O *__restrict__ db)
+    Tiles tiles, O *__restrict__ dw, float *__restrict__ db_part)
 {
-    constexpr int kBufBytes = 2 * (parts<T>() + 1) * kTileBytes;
-    constexpr int kTradeBytes = 2 * 4 * 2 * 5 * 64 * 16; // the halves' sums
-    __shared__ __align__(16) char lds[kBufBytes > kTradeBytes ? kBufBytes : kTradeBytes];
+    constexpr int P = parts<T>(), kLoads = sizeof(T) / 2; // 16-byte loads of eight columns
+    __shared__ __align__(16) float lds[kTile * kTile / 2 * kWaves];
     // Blocks go to the 8 XCDs in turn; each XCD takes a contiguous run of
     // tiles, k fastest, so that its L2 holds the rows of dy they share.
     const int xcd = blockIdx.x % 8, q = tiles.total / 8, rem = tiles.total % 8;
     const int tile = xcd * q + min(xcd, rem) + blockIdx.x / 8;
     const int tk = tile % tiles.k, tn = tile / tiles.k % tiles.n, z = tile / tiles.k / tiles.n;
-    const int n0 = tn * kTileN, k0 = tk * kTileK;
+    const int n0 = tn * kTile, k0 = tk * kTile;
     const int64_t m_begin = (int64_t)z * chunk;
     const int64_t m_end = m_begin + chunk < m ? m_begin + chunk : m;
-    O *const out = dw + (int64_t)z * n * k;
-    O *const out_b = db ? db + (int64_t)z * n : nullptr;
-    if (out_b && tk == 0)
-        weight_grad_tile<T, O, true>(dy, n, lddy, x, k, m_begin, m_end, n0, k0, out, out_b, lds);
-    else
-        weight_grad_tile<T, O, false>(dy, n, lddy, x, k, m_begin, m_end, n0, k0, out, out_b, lds);
+
+    const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // the first of the eight rows of dw (columns of dy) of MFMA row r
+    const auto first_row = [&](int r) { return min(n0 + 8 * r, n - 8); };
+    const int dy_col = first_row(i);
+    const int x_col = k0 + 8 * i < x.pitch ? k0 + 8 * i : 0;
+    // A load's address is a step's base and a lane's 32-bit offset to token j.
+    // The offsets are made opaque at each use, or their widening to 64 bits
+    // leaves the loop and every load adds two 64-bit numbers.
+    uint32_t dy_at[8], b_at[8], e_at[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        dy_at[j] = (uint32_t)(((4 * j + g) * lddy + dy_col) * sizeof(T));
+        b_at[j] = (uint32_t)((4 * j + g) * x.pitch + x_col);
+        e_at[j] = (uint32_t)((4 * j + g) * x.groups + (x_col >> 5));
+    }
+    // Part h of dy's token j: its eight columns, or the first or last four.
+    const auto load_dy = [&](RawDy<T> &l, int j, int h, int64_t m0) GQT_INLINE {
+        asm volatile("" : "+v"(dy_at[j]));
+        const char *p = reinterpret_cast<const char *>(dy + (m0 + kWaveM * wave) * lddy) + 16 * h;
+        l.a[j][h] = load16(reinterpret_cast<const T *>(p + dy_at[j]));
+    };
+    const auto load_x = [&](RawX &l, int j, int64_t m0) GQT_INLINE {
+        asm volatile("" : "+v"(b_at[j]), "+v"(e_at[j]));
+        const int64_t row = m0 + kWaveM * wave;
+        l.b[j] = *reinterpret_cast<const u32x2 *>(x.codes + row * x.pitch + b_at[j]);
+        // the word that ends with the exponent: three bytes lie before it,
+        // but for the first of the first step, which is not loaded here
+        l.e[j] = *reinterpret_cast<const u32_e1 *>(x.exps + row * x.groups - 3 + e_at[j]);
+    };
+
+    f32x4 acc[8][8] = {};
+    float sum[8] = {};
+    // rows c of dw by columns b of it
+    const auto mfma = [&](u32x4 fy, u32x4 fx, int c, int b) GQT_INLINE {
+        acc[c][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_fragment(fy), as_fragment(fx),
+                                                            acc[c][b], 0, 0, 0);
+    };
+
+    // While step s is multiplied, dy of step s + 1 and x of step s + 2 are
+    // loaded; past the last step the last one is loaded again.  Rows further
+    // apart than a lane's offset reaches and tokens that do not fill a step
+    // come last, one step at a time.
+    const int steps = lddy < ((int64_t)1 << 24) ? (int)((m_end - m_begin) / kStepM) : 0;
+    const auto start = [&](int s) { return m_begin + (int64_t)min(s, steps - 1) * kStepM; };
+    int next_sum = db_part ? tk : -1; // the step whose tokens this tile adds up next
+    RawDy<T> ry;
+    RawX rx;
+    if (steps > 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+#pragma unroll
+            for (int h = 0; h < kLoads; ++h)
+                load_dy(ry, j, h, m_begin);
+            if (j > 0) {
+                load_x(rx, j, m_begin);
+            } else {
+                const int64_t row = m_begin + kWaveM * wave;
+                const uint32_t back = min(e_at[0], 3u);
+                rx.b[0] = *reinterpret_cast<const u32x2 *>(x.codes + row * x.pitch + b_at[0]);
+                rx.e[0] = *reinterpret_cast<const u32_e1 *>(x.exps + row * x.groups +
+                                                            (e_at[0] - back));
+                rx.e[0] <<= 8 * (3 - back);
+            }
+        }
+        if constexpr (P == 1) {
+            // x outside: its fragment b + 1 is decoded while fragment b meets
+            // the eight of dy, which stay in registers.
+            Biased x8 = biased(rx);
+            u32x4 fx = x_fragment(x8, 0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                load_x(rx, j, start(1));
+            for (int s = 0; s < steps; ++s) {
+                if (s == next_sum) {
+                    add_tokens(ry, sum);
+                    next_sum += tiles.k;
+                }
+                const int64_t at_dy = start(s + 1), at_x = start(s + 2);
+                u32x4 fy[8][1];
+#pragma unroll
+                for (int b = 0; b < 8; ++b) {
+                    if (b == 7)
+                        x8 = biased(rx);
+                    const u32x4 fx_next = x_fragment(x8, (b + 1) % 8);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        if (b == 0)
+                            dy_fragment(ry, c, fy[c]);
+                        mfma(fy[c][0], fx, c, b);
+                    }
+                    fx = fx_next;
+                    interleave<8, 3>();
+                    if (b == 0)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            load_dy(ry, j, 0, at_dy);
+                    if (b == 7)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            load_x(rx, j, at_x);
+                }
+            }
+        } else {
+            // dy outside, four columns at a time, which leaves its registers
+            // to the next step's; x of the next step is decoded meanwhile.
+            u32x4 fx[8], fx_next[8];
+            decode(rx, fx);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                load_x(rx, j, start(1));
+            for (int s = 0; s < steps; ++s) {
+                if (s == next_sum) {
+                    add_tokens(ry, sum);
+                    next_sum += tiles.k;
+                }
+                const int64_t at_dy = start(s + 1), at_x = start(s + 2);
+                const Biased x8 = biased(rx);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    u32x4 part[P];
+                    dy_fragment(ry, c, part);
+                    fx_next[c] = x_fragment(x8, c);
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+#pragma unroll
+                        for (int b = 0; b < 8; ++b)
+                            mfma(part[p], fx[b], c, b);
+                    interleave<8 * P, 4>();
+                    load_x(rx, c, at_x);
+                    if (c % 4 == 3)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            load_dy(ry, j, c / 4, at_dy);
+                }
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    fx[c] = fx_next[c];
+            }
+        }
+    }
+    // Any tokens: those past the end read as the last one with a dy of 0.
+    for (int64_t m0 = m_begin + (int64_t)steps * kStepM; m0 < m_end; m0 += kStepM) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t want = m0 + kWaveM * wave + 4 * j + g;
+            const int64_t row = want < m_end ? want : m_end - 1;
+#pragma unroll
+            for (int h = 0; h < kLoads; ++h) {
+                ry.a[j][h] = load16(dy + row * lddy + dy_col + 8 / kLoads * h);
+                if (want >= m_end)
+                    ry.a[j][h] = u32x4{0, 0, 0, 0};
+            }
+            rx.b[j] = *reinterpret_cast<const u32x2 *>(x.codes + row * x.pitch + x_col);
+            rx.e[j] = (uint32_t)x.exps[row * x.groups + (x_col >> 5)] << 24;
+        }
+        if (db_part && tk == 0)
+            add_tokens(ry, sum);
+        u32x4 fx[8];
+        decode(rx, fx);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            u32x4 part[P];
+            dy_fragment(ry, c, part);
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+                    mfma(part[p], fx[b], c, b);
+        }
+    }
+
+    // acc[c][b] of lane (i, g): row first_row(4 g + e) + c, column 8 i + b.
+    // Half of the c at a time, each wave leaves its sums in LDS and adds up
+    // those of all four waves for one c.
+    f32x4(*const part)[4][4][2][64] = reinterpret_cast<f32x4(*)[4][4][2][64]>(lds);
+    const int col = k0 + 8 * i;
+    O *const out = dw + ((int64_t)z * n) * k + col;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    f32x4 v;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        v[w] = acc[4 * h + c][4 * b + w][e];
+                    part[wave][c][e][b][lane] = v;
+                }
+        __syncthreads();
+#pragma unroll 1
+        for (int e = 0; e < 4; ++e) {
+            float v[8];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                f32x4 t = part[0][wave][e][b][lane];
+#pragma unroll
+                for (int w = 1; w < kWaves; ++w)
+                    t += part[w][wave][e][b][lane];
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    v[4 * b + w] = t[w];
+            }
+            // rows before 8 r belong to the neighbour
+            const int r = 4 * g + e, row = first_row(r) + 4 * h + wave;
+            if (row >= n0 + 8 * r && row < n && col < k)
+                store8(out + (int64_t)row * k, k - col, v);
+        }
+    }
+    if (db_part) {
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            float v = sum[c];
+            v += __shfl_xor(v, 16);
+            v += __shfl_xor(v, 32);
+            if (g == 0)
+                lds[(wave * 16 + i) * 8 + c] = v;
+        }
+        __syncthreads();
+        if (threadIdx.x < kTile) {
+            const int t = threadIdx.x, row = first_row(t / 8) + t % 8;
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w)
+                v += lds[w * kTile + t];
+            if (row >= n0 + t / 8 * 8 && row < n)
+                db_part[((int64_t)z * tiles.k + tk) * n + row] = v;
+        }
+    }
 }
 
-// Adds `splits` partials in order: count values of dw (or db).
-template <typename O>
-__global__ __launch_bounds__(256) void k_sum_splits(const float *__restrict__ part, int32_t splits,
-                                                    int64_t count, O *__restrict__ out)
+// n < 8: too few rows of dw for a tile.  A block's 16 lanes take 128 columns
+// of x, its 16 rows of threads every 16th token, and one product a value is
+// an ordinary fused multiply-add.  out and db_part as above, db by block 0.
+template <typename T>
+__global__ __launch_bounds__(256) void k_weight_grad_narrow(
+    const T *__restrict__ dy, int64_t m, int32_t n, int64_t lddy, Act8 x, int32_t k, int64_t chunk,
+    float *__restrict__ part, float *__restrict__ db_part)
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= count)
+    __shared__ float lds[16][16][9];
+    const int i = threadIdx.x % 16, t = threadIdx.x / 16;
+    const int col = blockIdx.x * kTile + 8 * i;
+    const int64_t z = blockIdx.y, m_begin = z * chunk;
+    const int64_t m_end = m_begin + chunk < m ? m_begin + chunk : m;
+    float acc[7][8] = {}, sum[7] = {};
+    for (int64_t row = m_begin + t; row < m_end; row += 16) {
+        float v[8];
+        if (col < k)
+            restore8(x, row, col, v);
+        else
+#pragma unroll
+            for (int b = 0; b < 8; ++b)
+                v[b] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 7; ++c) {
+            const float g = c < n ? (float)dy[row * lddy + c] : 0.0f;
+            sum[c] += g;
+#pragma unroll
+            for (int b = 0; b < 8; ++b)
+                acc[c][b] = fmaf(g, v[b], acc[c][b]);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 7; ++c) {
+        __syncthreads();
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+            lds[t][i][b] = acc[c][b];
+        lds[t][i][8] = sum[c];
+        __syncthreads();
+        if (c >= n)
+            continue;
+        for (int at = threadIdx.x; at < 16 * 9; at += 256) {
+            const int b = at % 9, column = blockIdx.x * kTile + 8 * (at / 9) + b;
+            float v = 0.0f;
+            for (int w = 0; w < 16; ++w)
+                v += lds[w][at / 9][b];
+            if (b < 8 && column < k)
+                part[(z * n + c) * k + column] = v;
+            if (at == 8 && blockIdx.x == 0 && db_part)
+                db_part[z * n + c] = v;
+        }
+    }
+}
+
+// Adds partials in order: `splits` of count values for dw (unless it is
+// whole already), and `parts` of n for db, whose blocks come after dw's.
+template <typename O>
+__global__ __launch_bounds__(256) void k_sum_parts(const float *__restrict__ dw_part,
+                                                   int32_t splits, int64_t count,
+                                                   O *__restrict__ dw, uint32_t dw_blocks,
+                                                   const float *__restrict__ db_part,
+                                                   int32_t db_parts, int32_t n,
+                                                   O *__restrict__ db)
+{
+    const bool second = blockIdx.x >= dw_blocks;
+    const float *const part = second ? db_part : dw_part;
+    const int64_t size = second ? n : count;
+    const int32_t terms = second ? db_parts : splits;
+    const int64_t i = (int64_t)(blockIdx.x - (second ? dw_blocks : 0)) * 256 + threadIdx.x;
+    if (i >= size)
         return;
     float s = 0.0f;
-    for (int z = 0; z < splits; ++z)
-        s += part[z * count + i];
-    out[i] = (O)s;
+#pragma unroll 4
+    for (int z = 0; z < terms; ++z)
+        s += part[z * size + i];
+    (second ? db : dw)[i] = (O)s;
 }
 
-// How the tokens are split: enough blocks for every CU, chunks of at least
-// 256 tokens.
-struct Split {
+// How the work is cut: tiles, and how often the tokens are split.
+struct Plan {
+    Tiles tiles;
     int32_t splits;
     int64_t chunk;
+    int64_t dw_part, db_part, bytes; // partials: values of dw's, of db's, and the workspace
+    int32_t db_parts;
 };
-Split split_of(int64_t m, int64_t n, int64_t k)
+
+// Enough blocks for every CU, chunks of at least 256 tokens.
+Plan plan_of(int64_t m, int64_t n, int64_t k)
 {
-    const int64_t tiles = ((n + kTileN - 1) / kTileN) * ((k + kTileK - 1) / kTileK);
+    Plan p{};
+    if (m == 0) // no partials: sums of nothing
+        return p;
+    p.tiles = {(int32_t)((n + kTile - 1) / kTile), (int32_t)((k + kTile - 1) / kTile), 0};
+    const int64_t tiles = (int64_t)p.tiles.n * p.tiles.k;
     int64_t s = 256 / tiles;
     if (s > (m + 255) / 256)
         s = (m + 255) / 256;
     if (s < 1)
         s = 1;
-    Split r;
-    r.chunk = (m + s - 1) / s;
-    r.chunk = (r.chunk + kStepM - 1) / kStepM * kStepM;
-    if (r.chunk < kStepM)
-        r.chunk = kStepM;
-    r.splits = (int32_t)((m + r.chunk - 1) / r.chunk);
-    if (r.splits < 1)
-        r.splits = 1;
-    return r;
+    p.chunk = (m + s - 1) / s;
+    p.chunk = (p.chunk + kStepM - 1) / kStepM * kStepM;
+    p.splits = (int32_t)((m + p.chunk - 1) / p.chunk);
+    p.tiles.total = (int32_t)(tiles * p.splits); // n k < 2^40: below 2^27
+    p.db_parts = n < 8 ? p.splits : p.splits * p.tiles.k;
+    p.dw_part = p.splits > 1 || n < 8 ? p.splits * n * k : 0;
+    p.db_part = p.db_parts * n;
+    p.bytes = 4 * (p.dw_part + p.db_part);
+    return p;
 }
 
 bool sizes_ok(int64_t m, int64_t n, int64_t k)
@@ -375,40 +553,36 @@ bool sizes_ok(int64_t m, int64_t n, int64_t k)
            k <= 0x7FFFFFFF - 255 && k < (((int64_t)1 << 40) + n - 1) / n;
 }
 
-template <typename T>
+template <typename T, typename O>
 int32_t launch(const void *dy, int64_t m, int32_t n, int64_t lddy, const Act8 &x, int32_t k,
-               void *dw, void *db, int32_t wdtype, float *ws, hipStream_t st)
+               void *dw, void *db, float *ws, hipStream_t st)
 {
-    const Split s = split_of(m, n, k);
-    Tiles tiles{(n + kTileN - 1) / kTileN, (k + kTileK - 1) / kTileK, 0};
-    tiles.total = tiles.n * tiles.k * s.splits; // n k < 2^40: below 2^26 tiles, split or not
-    const dim3 grid((uint32_t)tiles.total);
-    const T *dyt = (const T *)dy;
-    if (s.splits == 1) {
-        if (wdtype == GQ_IN_F32)
-            k_weight_grad<T, float><<<grid, kWgThreads, 0, st>>>(dyt, m, n, lddy, x, k, s.chunk, tiles,
-                                                                 (float *)dw, (float *)db);
-        else
-            k_weight_grad<T, bf16><<<grid, kWgThreads, 0, st>>>(dyt, m, n, lddy, x, k, s.chunk, tiles,
-                                                                (bf16 *)dw, (bf16 *)db);
-        return check_launch("k_weight_grad");
+    const Plan p = plan_of(m, n, k);
+    float *const db_part = db ? ws + p.dw_part : nullptr;
+    const T *const dyt = (const T *)dy;
+    if (m == 0) {
+        // nothing to launch before the sums
+    } else if (n < 8) {
+        k_weight_grad_narrow<T><<<dim3(p.tiles.k, p.splits), 256, 0, st>>>(
+            dyt, m, n, lddy, x, k, p.chunk, ws, db_part);
+        GQT_TRY(check_launch("k_weight_grad_narrow"));
+    } else if (p.dw_part) {
+        k_weight_grad<T, float><<<dim3(p.tiles.total), kThreads, 0, st>>>(
+            dyt, m, n, lddy, x, k, p.chunk, p.tiles, ws, db_part);
+        GQT_TRY(check_launch("k_weight_grad"));
+    } else {
+        k_weight_grad<T, O><<<dim3(p.tiles.total), kThreads, 0, st>>>(
+            dyt, m, n, lddy, x, k, p.chunk, p.tiles, (O *)dw, db_part);
+        GQT_TRY(check_launch("k_weight_grad"));
     }
     const int64_t count = (int64_t)n * k;
-    float *const db_part = ws + s.splits * count;
-    k_weight_grad<T, float><<<grid, kWgThreads, 0, st>>>(dyt, m, n, lddy, x, k, s.chunk, tiles, ws,
-                                                         db ? db_part : nullptr);
-    GQT_TRY(check_launch("k_weight_grad"));
-    const auto blocks = [](int64_t c) { return dim3((uint32_t)((c + 255) / 256)); };
-    if (wdtype == GQ_IN_F32) {
-        k_sum_splits<float><<<blocks(count), 256, 0, st>>>(ws, s.splits, count, (float *)dw);
-        if (db)
-            k_sum_splits<float><<<blocks(n), 256, 0, st>>>(db_part, s.splits, n, (float *)db);
-    } else {
-        k_sum_splits<bf16><<<blocks(count), 256, 0, st>>>(ws, s.splits, count, (bf16 *)dw);
-        if (db)
-            k_sum_splits<bf16><<<blocks(n), 256, 0, st>>>(db_part, s.splits, n, (bf16 *)db);
-    }
-    return check_launch("k_sum_splits");
+    const int64_t dw_blocks = p.dw_part || m == 0 ? (count + 255) / 256 : 0;
+    const int64_t db_blocks = db ? (n + 255) / 256 : 0;
+    if (dw_blocks + db_blocks == 0)
+        return ok();
+    k_sum_parts<O><<<dim3((uint32_t)(dw_blocks + db_blocks)), 256, 0, st>>>(
+        ws, p.splits, count, (O *)dw, (uint32_t)dw_blocks, db_part, p.db_parts, n, (O *)db);
+    return check_launch("k_sum_parts");
 }
 
 } // namespace
@@ -422,8 +596,7 @@ int64_t gqt_weight_grad_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t
 {
     if (!sizes_ok(m, n, k) || !dtype_ok(dtype))
         return -1;
-    const Split s = split_of(m, n, k);
-    return s.splits > 1 ? 4 * s.splits * (n * k + n) : 0;
+    return plan_of(m, n, k).bytes;
 }
 
 int32_t gqt_weight_grad(const void *dy, int32_t dtype, int64_t m, int64_t n, int64_t lddy,
@@ -458,11 +631,15 @@ int32_t gqt_weight_grad(const void *dy, int32_t dtype, int64_t m, int64_t n, int
     if (!aligned_to(workspace, 16))
         return fail(GQ_ERR_ALIGN, "workspace is not 16-byte aligned");
     const Act8 x = act8_view(x8, k);
-    return dtype == GQ_IN_F32
-               ? launch<float>(dy, m, (int32_t)n, lddy, x, (int32_t)k, dw, db, wdtype,
-                               (float *)workspace, (hipStream_t)stream)
-               : launch<bf16>(dy, m, (int32_t)n, lddy, x, (int32_t)k, dw, db, wdtype,
-                              (float *)workspace, (hipStream_t)stream);
+    float *const ws = (float *)workspace;
+    const hipStream_t st = (hipStream_t)stream;
+    if (dtype == GQ_IN_F32)
+        return wdtype == GQ_IN_F32
+                   ? launch<float, float>(dy, m, (int32_t)n, lddy, x, (int32_t)k, dw, db, ws, st)
+                   : launch<float, bf16>(dy, m, (int32_t)n, lddy, x, (int32_t)k, dw, db, ws, st);
+    return wdtype == GQ_IN_F32
+               ? launch<bf16, float>(dy, m, (int32_t)n, lddy, x, (int32_t)k, dw, db, ws, st)
+               : launch<bf16, bf16>(dy, m, (int32_t)n, lddy, x, (int32_t)k, dw, db, ws, st);
 }
 
 } // extern "C"
