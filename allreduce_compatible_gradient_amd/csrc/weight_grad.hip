@@ -34,10 +34,12 @@ template <typename T>
 struct RawDy {
     u32x4 a[8][sizeof(T) / 2];
 };
-// and of x: codes, and a word whose top byte is the group's exponent
+// and of x: codes, and for one of the tokens (lane i of 16: token i % 8) the
+// exponents of the tile's four groups.  One load a lane: byte loads of each
+// token's own exponent took longer than all the others together.
 struct RawX {
     u32x2 b[8];
-    uint32_t e[8];
+    uint32_t e;
 };
 
 __device__ __forceinline__ u32x4 load16(const bf16 *p)
@@ -107,37 +109,67 @@ __device__ __forceinline__ void add_tokens(const RawDy<float> &l, float (&sum)[8
             sum[c] += bits_f32(l.a[j][c / 4][c % 4]);
 }
 
-// The eight tokens' codes and scales: code + 128 is an unsigned byte, which one
-// instruction makes a float, and (code + 128) step - 128 step is exact.  The
-// exponent byte 255 gives an infinite step, and inf - inf is the NaN it stands
-// for.
-struct Biased {
-    u32x2 b[8]; // codes + 128
-    float step[8], off[8];
+// The eight tokens' scales.  `up` moves the lane's own group's exponent to
+// the top byte.  255 makes an infinity, which inf 0 + inf turns into the NaN
+// it stands for.
+struct Steps {
+    float of[8];
 };
-__device__ __forceinline__ Biased biased(const RawX &l)
+__device__ __forceinline__ Steps steps_of(const RawX &l, uint32_t up)
 {
-    Biased s;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        // in assembly, so that the compiler does not flip each byte by itself
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            asm("v_xor_b32 %0, %1, %2" : "=v"(s.b[j][h]) : "s"(0x80808080u), "v"(l.b[j][h]));
-        s.step[j] = bits_f32((l.e[j] >> 1) & 0x7F800000u);
-        s.off[j] = -128.0f * s.step[j];
-    }
+    Steps s;
+#define GQT_TOKEN(J) /* from lane J of each 16 */                                              \
+    do {                                                                                       \
+        const uint32_t e = (uint32_t)__builtin_amdgcn_mov_dpp((int)l.e, 0x150 + J, 0xF, 0xF,   \
+                                                              true);                           \
+        const float step = bits_f32(((e << up) >> 1) & 0x7F800000u);                           \
+        s.of[J] = fmaf(step, 0.0f, step);                                                      \
+    } while (0)
+    GQT_TOKEN(0);
+    GQT_TOKEN(1);
+    GQT_TOKEN(2);
+    GQT_TOKEN(3);
+    GQT_TOKEN(4);
+    GQT_TOKEN(5);
+    GQT_TOKEN(6);
+    GQT_TOKEN(7);
+#undef GQT_TOKEN
     return s;
 }
 
-// Fragment c of x.
-__device__ __forceinline__ u32x4 x_fragment(const Biased &s, int c)
+// Byte B of w as a signed number, in one instruction (the compiler takes
+// two); one wait state ahead of it, so that no forwarding hazard has to be
+// known for it.
+template <int B>
+__device__ __forceinline__ float code_f32(uint32_t w)
+{
+    float f;
+    if (B == 0)
+        asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0"
+            : "=v"(f) : "v"(w));
+    else if (B == 1)
+        asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1"
+            : "=v"(f) : "v"(w));
+    else if (B == 2)
+        asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2"
+            : "=v"(f) : "v"(w));
+    else
+        asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3"
+            : "=v"(f) : "v"(w));
+    return f;
+}
+
+// Fragment c of x: its code times its step, exact in bf16.
+__device__ __forceinline__ u32x4 x_fragment(const RawX &l, const Steps &s, int c)
 {
     float f[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const uint32_t u = s.b[j][c / 4];
-        f[j] = fmaf((float)((u >> (8 * (c % 4))) & 0xFFu), s.step[j], s.off[j]);
+        const uint32_t w = l.b[j][c / 4];
+        f[j] = s.of[j] * (c % 4 == 0   ? code_f32<0>(w)
+                          : c % 4 == 1 ? code_f32<1>(w)
+                          : c % 4 == 2 ? code_f32<2>(w)
+                                       : code_f32<3>(w));
     }
     u32x4 r;
 #pragma unroll
@@ -146,12 +178,12 @@ __device__ __forceinline__ u32x4 x_fragment(const Biased &s, int c)
     return r;
 }
 
-__device__ __forceinline__ void decode(const RawX &l, u32x4 (&f)[8])
+__device__ __forceinline__ void decode(const RawX &l, uint32_t up, u32x4 (&f)[8])
 {
-    const Biased l8 = biased(l);
+    const Steps s = steps_of(l, up);
 #pragma unroll
     for (int c = 0; c < 8; ++c)
-        f[c] = x_fragment(l8, c);
+        f[c] = x_fragment(l, s, c);
 }
 
 // Asks the scheduler for MFMAS times one MFMA and VALU vector instructions,
@@ -209,26 +241,38 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
     // A load's address is a step's base and a lane's 32-bit offset to token j.
     // The offsets are made opaque at each use, or their widening to 64 bits
     // leaves the loop and every load adds two 64-bit numbers.
-    uint32_t dy_at[8], b_at[8], e_at[8];
+    uint32_t dy_at[8], b_at[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         dy_at[j] = (uint32_t)(((4 * j + g) * lddy + dy_col) * sizeof(T));
         b_at[j] = (uint32_t)((4 * j + g) * x.pitch + x_col);
-        e_at[j] = (uint32_t)((4 * j + g) * x.groups + (x_col >> 5));
     }
+    // The word of four exponents ends with the row at the latest (with fewer
+    // than four groups it begins in the row before).
+    const int e_col = min(k0 >> 5, x.groups - 4), e_token = 4 * (i % 8) + g;
+    const uint32_t up = 24 - 8 * ((x_col >> 5) - e_col);
+    int32_t e_at = e_token * x.groups + e_col;
+    // Where the next step's tokens of this wave lie; the last step's again
+    // past the end.
+    const int64_t row0 = m_begin + kWaveM * wave;
+    const char *dy_p = reinterpret_cast<const char *>(dy + row0 * lddy);
+    const int8_t *codes_p = x.codes + row0 * x.pitch;
+    const uint8_t *exps_p = x.exps + row0 * x.groups;
+    const int64_t dy_step = kStepM * lddy * (int64_t)sizeof(T), codes_step = kStepM * x.pitch,
+                  exps_step = (int64_t)kStepM * x.groups;
     // Part h of dy's token j: its eight columns, or the first or last four.
-    const auto load_dy = [&](RawDy<T> &l, int j, int h, int64_t m0) GQT_INLINE {
+    const auto load_dy = [&](RawDy<T> &l, int j, int h) GQT_INLINE {
         asm volatile("" : "+v"(dy_at[j]));
-        const char *p = reinterpret_cast<const char *>(dy + (m0 + kWaveM * wave) * lddy) + 16 * h;
-        l.a[j][h] = load16(reinterpret_cast<const T *>(p + dy_at[j]));
+        l.a[j][h] = load16(reinterpret_cast<const T *>(dy_p + 16 * h + dy_at[j]));
     };
-    const auto load_x = [&](RawX &l, int j, int64_t m0) GQT_INLINE {
-        asm volatile("" : "+v"(b_at[j]), "+v"(e_at[j]));
-        const int64_t row = m0 + kWaveM * wave;
-        l.b[j] = *reinterpret_cast<const u32x2 *>(x.codes + row * x.pitch + b_at[j]);
-        // the word that ends with the exponent: three bytes lie before it,
-        // but for the first of the first step, which is not loaded here
-        l.e[j] = *reinterpret_cast<const u32_e1 *>(x.exps + row * x.groups - 3 + e_at[j]);
+    const auto load_codes = [&](RawX &l, int j) GQT_INLINE {
+        asm volatile("" : "+v"(b_at[j]));
+        l.b[j] = *reinterpret_cast<const u32x2 *>(codes_p + b_at[j]);
+    };
+    // A single step's tokens, which may have no row before them, are loaded
+    // again for nothing.
+    const auto load_exps = [&](RawX &l) GQT_INLINE {
+        l.e = *reinterpret_cast<const u32_e1 *>(exps_p + e_at);
     };
 
     f32x4 acc[8][8] = {};
@@ -244,47 +288,61 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
     // apart than a lane's offset reaches and tokens that do not fill a step
     // come last, one step at a time.
     const int steps = lddy < ((int64_t)1 << 24) ? (int)((m_end - m_begin) / kStepM) : 0;
-    const auto start = [&](int s) { return m_begin + (int64_t)min(s, steps - 1) * kStepM; };
     int next_sum = db_part ? tk : -1; // the step whose tokens this tile adds up next
     RawDy<T> ry;
-    RawX rx;
+    RawX rx0, rx1;
     if (steps > 0) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
 #pragma unroll
             for (int h = 0; h < kLoads; ++h)
-                load_dy(ry, j, h, m_begin);
-            if (j > 0) {
-                load_x(rx, j, m_begin);
-            } else {
-                const int64_t row = m_begin + kWaveM * wave;
-                const uint32_t back = min(e_at[0], 3u);
-                rx.b[0] = *reinterpret_cast<const u32x2 *>(x.codes + row * x.pitch + b_at[0]);
-                rx.e[0] = *reinterpret_cast<const u32_e1 *>(x.exps + row * x.groups +
-                                                            (e_at[0] - back));
-                rx.e[0] <<= 8 * (3 - back);
-            }
+                load_dy(ry, j, h);
+            load_codes(rx0, j);
         }
+        const int64_t first = row0 * x.groups + e_at, at = max(first, (int64_t)0);
+        rx0.e = *reinterpret_cast<const u32_e1 *>(x.exps + at) << (8 * (at - first));
+        if (steps == 1)
+            e_at = max(e_at, 0);
+        const auto advance_x = [&](bool more) GQT_INLINE {
+            codes_p += more ? codes_step : 0;
+            exps_p += more ? exps_step : 0;
+        };
+        advance_x(steps > 1);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            load_codes(rx1, j);
+        load_exps(rx1);
+        // before step s is multiplied
+        const auto enter = [&](int s) GQT_INLINE {
+            if (s == next_sum) {
+                add_tokens(ry, sum);
+                next_sum += tiles.k;
+            }
+            dy_p += s + 1 < steps ? dy_step : 0;
+            advance_x(s + 2 < steps);
+        };
         if constexpr (P == 1) {
             // x outside: its fragment b + 1 is decoded while fragment b meets
             // the eight of dy, which stay in registers.
-            Biased x8 = biased(rx);
-            u32x4 fx = x_fragment(x8, 0);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                load_x(rx, j, start(1));
+            // (Two buffers of x in turn would save the copy, but a loop of two
+            // steps has the compiler move the sums between registers.  The copy
+            // is in assembly so that it stays where it is.)
+            Steps st = steps_of(rx0, up);
+            u32x4 fx = x_fragment(rx0, st, 0);
             for (int s = 0; s < steps; ++s) {
-                if (s == next_sum) {
-                    add_tokens(ry, sum);
-                    next_sum += tiles.k;
-                }
-                const int64_t at_dy = start(s + 1), at_x = start(s + 2);
+                enter(s);
                 u32x4 fy[8][1];
 #pragma unroll
                 for (int b = 0; b < 8; ++b) {
-                    if (b == 7)
-                        x8 = biased(rx);
-                    const u32x4 fx_next = x_fragment(x8, (b + 1) % 8);
+                    if (b == 7) {
+                        st = steps_of(rx1, up);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                asm("v_mov_b32 %0, %1" : "=v"(rx0.b[j][h]) : "v"(rx1.b[j][h]));
+                    }
+                    const u32x4 fx_next = x_fragment(rx0, st, (b + 1) % 8);
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         if (b == 0)
@@ -296,45 +354,43 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
                     if (b == 0)
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            load_dy(ry, j, 0, at_dy);
-                    if (b == 7)
+                            load_dy(ry, j, 0);
+                    if (b == 7) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            load_x(rx, j, at_x);
+                            load_codes(rx1, j);
+                        load_exps(rx1);
+                    }
                 }
             }
         } else {
             // dy outside, four columns at a time, which leaves its registers
             // to the next step's; x of the next step is decoded meanwhile.
             u32x4 fx[8], fx_next[8];
-            decode(rx, fx);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                load_x(rx, j, start(1));
+            decode(rx0, up, fx);
             for (int s = 0; s < steps; ++s) {
-                if (s == next_sum) {
-                    add_tokens(ry, sum);
-                    next_sum += tiles.k;
-                }
-                const int64_t at_dy = start(s + 1), at_x = start(s + 2);
-                const Biased x8 = biased(rx);
+                enter(s);
+                const Steps st = steps_of(rx1, up);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     u32x4 part[P];
                     dy_fragment(ry, c, part);
-                    fx_next[c] = x_fragment(x8, c);
+                    fx_next[c] = x_fragment(rx1, st, c);
 #pragma unroll
                     for (int p = 0; p < P; ++p)
 #pragma unroll
                         for (int b = 0; b < 8; ++b)
                             mfma(part[p], fx[b], c, b);
                     interleave<8 * P, 4>();
-                    load_x(rx, c, at_x);
                     if (c % 4 == 3)
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            load_dy(ry, j, c / 4, at_dy);
+                            load_dy(ry, j, c / 4);
                 }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    load_codes(rx1, j);
+                load_exps(rx1);
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
                     fx[c] = fx_next[c];
@@ -353,13 +409,21 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
                 if (want >= m_end)
                     ry.a[j][h] = u32x4{0, 0, 0, 0};
             }
-            rx.b[j] = *reinterpret_cast<const u32x2 *>(x.codes + row * x.pitch + x_col);
-            rx.e[j] = (uint32_t)x.exps[row * x.groups + (x_col >> 5)] << 24;
+            rx0.b[j] = *reinterpret_cast<const u32x2 *>(x.codes + row * x.pitch + x_col);
+        }
+        {
+            const int64_t want = m0 + kWaveM * wave + e_token;
+            const int64_t row = want < m_end ? want : m_end - 1;
+            rx0.e = 0;
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                if (e_col + p >= 0)
+                    rx0.e |= (uint32_t)x.exps[row * x.groups + e_col + p] << (8 * p);
         }
         if (db_part && tk == 0)
             add_tokens(ry, sum);
         u32x4 fx[8];
-        decode(rx, fx);
+        decode(rx0, up, fx);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             u32x4 part[P];
@@ -523,23 +587,34 @@ struct Plan {
     int32_t db_parts;
 };
 
-// Enough blocks for every CU, chunks of at least 256 tokens.
-Plan plan_of(int64_t m, int64_t n, int64_t k)
+// The split with the least estimated time.  A CU holds one block, so blocks
+// run in rounds of 256; a round takes 8 us and 1.0 us a step (3.1 us for
+// fp32), and partials are written and read again at 4 TB/s with 3 us for
+// their launch (all measured).  Without the rounds in the estimate, 4096 x
+// 1056 (288 tiles) took two rounds of all tokens, 276 us where 4096 x 1024
+// took 146.
+Plan plan_of(int64_t m, int64_t n, int64_t k, int32_t dtype)
 {
     Plan p{};
     if (m == 0) // no partials: sums of nothing
         return p;
     p.tiles = {(int32_t)((n + kTile - 1) / kTile), (int32_t)((k + kTile - 1) / kTile), 0};
-    const int64_t tiles = (int64_t)p.tiles.n * p.tiles.k;
-    int64_t s = 256 / tiles;
-    if (s > (m + 255) / 256)
-        s = (m + 255) / 256;
-    if (s < 1)
-        s = 1;
-    p.chunk = (m + s - 1) / s;
-    p.chunk = (p.chunk + kStepM - 1) / kStepM * kStepM;
-    p.splits = (int32_t)((m + p.chunk - 1) / p.chunk);
-    p.tiles.total = (int32_t)(tiles * p.splits); // n k < 2^40: below 2^27
+    const int64_t tiles = (int64_t)p.tiles.n * p.tiles.k, steps = (m + kStepM - 1) / kStepM;
+    const double step_us = dtype == GQ_IN_F32 ? 3.1 : 1.0;
+    double best = 0.0;
+    for (int64_t s = 1; s <= 256 && s <= steps; ++s) {
+        const int64_t chunk = (steps + s - 1) / s, splits = (steps + chunk - 1) / chunk;
+        const double rounds = (double)((tiles * splits + 255) / 256);
+        double us = rounds * (8.0 + step_us * (double)chunk);
+        if (splits > 1)
+            us += 3.0 + (double)splits * (double)n * (double)k * 8.0 / 4e6;
+        if (s == 1 || us < best) {
+            best = us;
+            p.splits = (int32_t)splits;
+            p.chunk = chunk * kStepM;
+        }
+    }
+    p.tiles.total = (int32_t)(tiles * p.splits); // n k < 2^40: below 2^27 tiles, or few splits
     p.db_parts = n < 8 ? p.splits : p.splits * p.tiles.k;
     p.dw_part = p.splits > 1 || n < 8 ? p.splits * n * k : 0;
     p.db_part = p.db_parts * n;
@@ -557,7 +632,7 @@ template <typename T, typename O>
 int32_t launch(const void *dy, int64_t m, int32_t n, int64_t lddy, const Act8 &x, int32_t k,
                void *dw, void *db, float *ws, hipStream_t st)
 {
-    const Plan p = plan_of(m, n, k);
+    const Plan p = plan_of(m, n, k, sizeof(T) == 4 ? GQ_IN_F32 : GQ_IN_BF16);
     float *const db_part = db ? ws + p.dw_part : nullptr;
     const T *const dyt = (const T *)dy;
     if (m == 0) {
@@ -596,7 +671,7 @@ int64_t gqt_weight_grad_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t
 {
     if (!sizes_ok(m, n, k) || !dtype_ok(dtype))
         return -1;
-    return plan_of(m, n, k).bytes;
+    return plan_of(m, n, k, dtype).bytes;
 }
 
 int32_t gqt_weight_grad(const void *dy, int32_t dtype, int64_t m, int64_t n, int64_t lddy,
