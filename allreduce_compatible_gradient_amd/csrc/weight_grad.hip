@@ -19,7 +19,6 @@ namespace {
 constexpr int kTile = 128;  // output tile: 128 rows and 128 columns of dw
 constexpr int kWaves = 4;   // one per SIMD: a wave's sums take half its registers
 constexpr int kWaveM = 32;  // tokens of a wave in a step: the depth of one MFMA
-constexpr int kStepM = kWaves * kWaveM;
 constexpr int kThreads = 64 * kWaves;
 
 #define GQT_INLINE __attribute__((always_inline))
@@ -68,17 +67,17 @@ __device__ __forceinline__ void dy_fragment(const RawDy<bf16> &l, int c, u32x4 (
 }
 
 // A float's leading 8, middle 8 and last 8 significant bits: truncated, so
-// that each rest is exact; an inf or NaN (made quiet, which keeps it one)
-// stays in the first part alone.
+// that each rest is exact.  An inf stays in the first part alone; a NaN's
+// rest is one too.
 __device__ __forceinline__ void dy_fragment(const RawDy<float> &l, int c, u32x4 (&part)[3])
 {
     uint32_t b[3][8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float v = __builtin_canonicalizef(bits_f32(l.a[j][c / 4][c % 4]));
+        const float v = bits_f32(l.a[j][c / 4][c % 4]);
         b[0][j] = __float_as_uint(v);
         const float rest = v - bits_f32(b[0][j] & 0xFFFF0000u);
-        const float r1 = __builtin_isfinite(v) ? rest : 0.0f;
+        const float r1 = __builtin_isinf(v) ? 0.0f : rest;
         b[1][j] = __float_as_uint(r1);
         b[2][j] = __float_as_uint(r1 - bits_f32(b[1][j] & 0xFFFF0000u));
     }
@@ -200,40 +199,48 @@ __device__ __forceinline__ void interleave()
     __builtin_amdgcn_sched_barrier(0);
 }
 
+constexpr int step_tokens(bool shared) { return shared ? kWaves * kWaveM : kWaveM; }
+
 struct Tiles {
     int32_t n, k, total; // tiles along n and k, and blocks (times the splits)
 };
 
-// One block: a 128 x 128 tile of dw over the tokens of one split, each wave
-// the whole tile over 32 of a step's 128 tokens; the waves' sums are added
-// at the end.  out: dw itself (one split) or the split's fp32 partial.
+// A wave holds a 128 x 128 tile of dw.  Either (SHARED) the four waves of a
+// block have one tile, each takes 32 of a step's 128 tokens, and their sums
+// are added at the end; or they have the four tiles of a 256 x 256 square and
+// the same 32 tokens, which asks half as much of the L2 and ends without a
+// word between them, but leaves fewer blocks.  out: dw itself (one split of
+// the tokens) or the split's fp32 partial.
 //
 // Rows of the tile past n, and columns past the codes' pitch, are not
 // stored, so what they hold is free: every lane loads eight columns that
 // exist.  The lane whose eight would end past n (n >= 8) takes the last eight
 // of the row, and so computes some rows that its neighbour stores.
 //
-// db: the tiles.k tiles that share a tile's columns of dy take turns at
-// adding up its steps, so that none is slower than the others; each leaves a
-// partial.
-template <typename T, typename O>
+// db: the tiles that share a tile's columns of dy take turns at adding up
+// its steps, so that none is slower than the others; each leaves a partial.
+template <typename T, typename O, bool SHARED>
 __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
     const T *__restrict__ dy, int64_t m, int32_t n, int64_t lddy, Act8 x, int32_t k, int64_t chunk,
     Tiles tiles, O *__restrict__ dw, float *__restrict__ db_part)
 {
     constexpr int P = parts<T>(), kLoads = sizeof(T) / 2; // 16-byte loads of eight columns
-    __shared__ __align__(16) float lds[kTile * kTile / 2 * kWaves];
+    constexpr int kStepM = step_tokens(SHARED), kSide = SHARED ? 1 : 2;
+    __shared__ __align__(16) float lds[SHARED ? kTile * kTile / 2 * kWaves : 1];
     // Blocks go to the 8 XCDs in turn; each XCD takes a contiguous run of
     // tiles, k fastest, so that its L2 holds the rows of dy they share.
     const int xcd = blockIdx.x % 8, q = tiles.total / 8, rem = tiles.total % 8;
     const int tile = xcd * q + min(xcd, rem) + blockIdx.x / 8;
-    const int tk = tile % tiles.k, tn = tile / tiles.k % tiles.n, z = tile / tiles.k / tiles.n;
+    const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tk = tile % tiles.k * kSide + (SHARED ? 0 : wave % 2);
+    const int tn = tile / tiles.k % tiles.n * kSide + (SHARED ? 0 : wave / 2);
+    const int z = tile / tiles.k / tiles.n;
     const int n0 = tn * kTile, k0 = tk * kTile;
     const int64_t m_begin = (int64_t)z * chunk;
     const int64_t m_end = m_begin + chunk < m ? m_begin + chunk : m;
+    const int wave_m = SHARED ? kWaveM * wave : 0; // the wave's tokens in a step
 
-    const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // the first of the eight rows of dw (columns of dy) of MFMA row r
     const auto first_row = [&](int r) { return min(n0 + 8 * r, n - 8); };
     const int dy_col = first_row(i);
@@ -244,8 +251,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
     uint32_t dy_at[8], b_at[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        dy_at[j] = (uint32_t)(((4 * j + g) * lddy + dy_col) * sizeof(T));
-        b_at[j] = (uint32_t)((4 * j + g) * x.pitch + x_col);
+        dy_at[j] = ((4 * j + g) * (uint32_t)lddy + dy_col) * (uint32_t)sizeof(T);
+        b_at[j] = (4 * j + g) * (uint32_t)x.pitch + x_col;
     }
     // The word of four exponents ends with the row at the latest (with fewer
     // than four groups it begins in the row before).
@@ -254,7 +261,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
     int32_t e_at = e_token * x.groups + e_col;
     // Where the next step's tokens of this wave lie; the last step's again
     // past the end.
-    const int64_t row0 = m_begin + kWaveM * wave;
+    const int64_t row0 = m_begin + wave_m;
     const char *dy_p = reinterpret_cast<const char *>(dy + row0 * lddy);
     const int8_t *codes_p = x.codes + row0 * x.pitch;
     const uint8_t *exps_p = x.exps + row0 * x.groups;
@@ -316,7 +323,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
         const auto enter = [&](int s) GQT_INLINE {
             if (s == next_sum) {
                 add_tokens(ry, sum);
-                next_sum += tiles.k;
+                next_sum += tiles.k * kSide;
             }
             dy_p += s + 1 < steps ? dy_step : 0;
             advance_x(s + 2 < steps);
@@ -364,25 +371,31 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
                 }
             }
         } else {
-            // dy outside, four columns at a time, which leaves its registers
-            // to the next step's; x of the next step is decoded meanwhile.
-            u32x4 fx[8], fx_next[8];
+            // dy outside: the parts of its fragment c + 1 are made while
+            // fragment c is multiplied, and so is x of the next step.  Four
+            // columns of dy done with leave their registers to the next
+            // step's.
+            u32x4 fx[8], fx_next[8], part[P];
             decode(rx0, up, fx);
+            dy_fragment(ry, 0, part);
             for (int s = 0; s < steps; ++s) {
                 enter(s);
                 const Steps st = steps_of(rx1, up);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    u32x4 part[P];
-                    dy_fragment(ry, c, part);
+                    u32x4 part_next[P];
+                    dy_fragment(ry, (c + 1) % 8, part_next);
                     fx_next[c] = x_fragment(rx1, st, c);
 #pragma unroll
                     for (int p = 0; p < P; ++p)
 #pragma unroll
                         for (int b = 0; b < 8; ++b)
                             mfma(part[p], fx[b], c, b);
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+                        part[p] = part_next[p];
                     interleave<8 * P, 4>();
-                    if (c % 4 == 3)
+                    if (c % 4 == 2)
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             load_dy(ry, j, c / 4);
@@ -401,7 +414,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
     for (int64_t m0 = m_begin + (int64_t)steps * kStepM; m0 < m_end; m0 += kStepM) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int64_t want = m0 + kWaveM * wave + 4 * j + g;
+            const int64_t want = m0 + wave_m + 4 * j + g;
             const int64_t row = want < m_end ? want : m_end - 1;
 #pragma unroll
             for (int h = 0; h < kLoads; ++h) {
@@ -412,7 +425,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
             rx0.b[j] = *reinterpret_cast<const u32x2 *>(x.codes + row * x.pitch + x_col);
         }
         {
-            const int64_t want = m0 + kWaveM * wave + e_token;
+            const int64_t want = m0 + wave_m + e_token;
             const int64_t row = want < m_end ? want : m_end - 1;
             rx0.e = 0;
 #pragma unroll
@@ -437,65 +450,92 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
     }
 
     // acc[c][b] of lane (i, g): row first_row(4 g + e) + c, column 8 i + b.
-    // Half of the c at a time, each wave leaves its sums in LDS and adds up
-    // those of all four waves for one c.
-    f32x4(*const part)[4][4][2][64] = reinterpret_cast<f32x4(*)[4][4][2][64]>(lds);
+    // Rows before 8 r belong to the neighbour.
     const int col = k0 + 8 * i;
     O *const out = dw + ((int64_t)z * n) * k + col;
+    const auto put = [&](int e, int c, float (&v)[8]) GQT_INLINE {
+        const int r = 4 * g + e, row = first_row(r) + c;
+        if (row >= n0 + 8 * r && row < n && col < k)
+            store8(out + (int64_t)row * k, k - col, v);
+    };
+    if constexpr (SHARED) {
+        // Half of the c at a time, each wave leaves its sums in LDS and adds
+        // up those of all four waves for one c.
+        f32x4(*const part)[4][4][2][64] = reinterpret_cast<f32x4(*)[4][4][2][64]>(lds);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        __syncthreads();
+        for (int h = 0; h < 2; ++h) {
+            __syncthreads();
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        f32x4 v;
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+                            v[w] = acc[4 * h + c][4 * b + w][e];
+                        part[wave][c][e][b][lane] = v;
+                    }
+            __syncthreads();
+#pragma unroll 1
+            for (int e = 0; e < 4; ++e) {
+                float v[8];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    f32x4 v;
+                    f32x4 t = part[0][wave][e][b][lane];
+#pragma unroll
+                    for (int w = 1; w < kWaves; ++w)
+                        t += part[w][wave][e][b][lane];
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
-                        v[w] = acc[4 * h + c][4 * b + w][e];
-                    part[wave][c][e][b][lane] = v;
+                        v[4 * b + w] = t[w];
                 }
-        __syncthreads();
-#pragma unroll 1
-        for (int e = 0; e < 4; ++e) {
-            float v[8];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                f32x4 t = part[0][wave][e][b][lane];
-#pragma unroll
-                for (int w = 1; w < kWaves; ++w)
-                    t += part[w][wave][e][b][lane];
-#pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    v[4 * b + w] = t[w];
+                put(e, 4 * h + wave, v);
             }
-            // rows before 8 r belong to the neighbour
-            const int r = 4 * g + e, row = first_row(r) + 4 * h + wave;
-            if (row >= n0 + 8 * r && row < n && col < k)
-                store8(out + (int64_t)row * k, k - col, v);
         }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                float v[8];
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+                    v[b] = acc[c][b][e];
+                put(e, c, v);
+            }
     }
     if (db_part) {
-        __syncthreads();
+        float *const db_out = db_part + ((int64_t)z * tiles.k * kSide + tk) * n;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-            float v = sum[c];
-            v += __shfl_xor(v, 16);
-            v += __shfl_xor(v, 32);
-            if (g == 0)
-                lds[(wave * 16 + i) * 8 + c] = v;
+            sum[c] += __shfl_xor(sum[c], 16);
+            sum[c] += __shfl_xor(sum[c], 32);
         }
-        __syncthreads();
-        if (threadIdx.x < kTile) {
-            const int t = threadIdx.x, row = first_row(t / 8) + t % 8;
-            float v = 0.0f;
+        if constexpr (SHARED) {
+            __syncthreads();
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w)
-                v += lds[w * kTile + t];
-            if (row >= n0 + t / 8 * 8 && row < n)
-                db_part[((int64_t)z * tiles.k + tk) * n + row] = v;
+            for (int c = 0; c < 8; ++c)
+                if (g == 0)
+                    lds[(wave * 16 + i) * 8 + c] = sum[c];
+            __syncthreads();
+            if (threadIdx.x < kTile) {
+                const int t = threadIdx.x, row = first_row(t / 8) + t % 8;
+                float v = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w)
+                    v += lds[w * kTile + t];
+                if (row >= n0 + t / 8 * 8 && row < n)
+                    db_out[row] = v;
+            }
+        } else if (g == 0) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const int row = dy_col + c;
+                if (row >= n0 + 8 * i && row < n)
+                    db_out[row] = sum[c];
+            }
         }
     }
 }
@@ -580,6 +620,7 @@ __global__ __launch_bounds__(256) void k_sum_parts(const float *__restrict__ dw_
 
 // How the work is cut: tiles, and how often the tokens are split.
 struct Plan {
+    bool shared;
     Tiles tiles;
     int32_t splits;
     int64_t chunk;
@@ -587,35 +628,42 @@ struct Plan {
     int32_t db_parts;
 };
 
-// The split with the least estimated time.  A CU holds one block, so blocks
-// run in rounds of 256; a round takes 8 us and 1.0 us a step (3.1 us for
-// fp32), and partials are written and read again at 4 TB/s with 3 us for
-// their launch (all measured).  Without the rounds in the estimate, 4096 x
-// 1056 (288 tiles) took two rounds of all tokens, 276 us where 4096 x 1024
-// took 146.
+// The cut with the least estimated time.  A CU holds one block, so blocks
+// run in rounds of 256; a round takes a fixed time and that of its steps, and
+// partials are written and read again at 4 TB/s with 3 us for their launch
+// (all measured).  Without the rounds in the estimate, 4096 x 1056 (288
+// tiles) took two rounds of all tokens, 276 us where 4096 x 1024 took 146.
 Plan plan_of(int64_t m, int64_t n, int64_t k, int32_t dtype)
 {
     Plan p{};
     if (m == 0) // no partials: sums of nothing
         return p;
-    p.tiles = {(int32_t)((n + kTile - 1) / kTile), (int32_t)((k + kTile - 1) / kTile), 0};
-    const int64_t tiles = (int64_t)p.tiles.n * p.tiles.k, steps = (m + kStepM - 1) / kStepM;
-    const double step_us = dtype == GQ_IN_F32 ? 3.1 : 1.0;
     double best = 0.0;
-    for (int64_t s = 1; s <= 256 && s <= steps; ++s) {
-        const int64_t chunk = (steps + s - 1) / s, splits = (steps + chunk - 1) / chunk;
-        const double rounds = (double)((tiles * splits + 255) / 256);
-        double us = rounds * (8.0 + step_us * (double)chunk);
-        if (splits > 1)
-            us += 3.0 + (double)splits * (double)n * (double)k * 8.0 / 4e6;
-        if (s == 1 || us < best) {
-            best = us;
-            p.splits = (int32_t)splits;
-            p.chunk = chunk * kStepM;
+    for (int shared = 0; shared < 2; ++shared) {
+        const int64_t side = shared ? kTile : 2 * kTile, tokens = step_tokens(shared);
+        const int64_t tn = (n + side - 1) / side, tk = (k + side - 1) / side;
+        const int64_t steps = (m + tokens - 1) / tokens;
+        const double round_us = shared ? 8.0 : 17.0;
+        const double step_us = dtype == GQ_IN_F32 ? 2.8 : 1.0;
+        if (n < 8 && !shared)
+            continue;
+        for (int64_t s = 1; s <= 256 && s <= steps; ++s) {
+            const int64_t chunk = (steps + s - 1) / s, splits = (steps + chunk - 1) / chunk;
+            const double rounds = (double)((tn * tk * splits + 255) / 256);
+            double us = rounds * (round_us + step_us * (double)chunk);
+            if (splits > 1)
+                us += 3.0 + (double)splits * (double)n * (double)k * 8.0 / 4e6;
+            if (p.splits == 0 || us < best) {
+                best = us;
+                p.shared = shared;
+                p.splits = (int32_t)splits;
+                p.chunk = chunk * tokens;
+                // n k < 2^40: below 2^27 tiles, or few splits
+                p.tiles = {(int32_t)tn, (int32_t)tk, (int32_t)(tn * tk * splits)};
+            }
         }
     }
-    p.tiles.total = (int32_t)(tiles * p.splits); // n k < 2^40: below 2^27 tiles, or few splits
-    p.db_parts = n < 8 ? p.splits : p.splits * p.tiles.k;
+    p.db_parts = n < 8 ? p.splits : p.splits * p.tiles.k * (p.shared ? 1 : 2);
     p.dw_part = p.splits > 1 || n < 8 ? p.splits * n * k : 0;
     p.db_part = p.db_parts * n;
     p.bytes = 4 * (p.dw_part + p.db_part);
@@ -641,13 +689,20 @@ int32_t launch(const void *dy, int64_t m, int32_t n, int64_t lddy, const Act8 &x
         k_weight_grad_narrow<T><<<dim3(p.tiles.k, p.splits), 256, 0, st>>>(
             dyt, m, n, lddy, x, k, p.chunk, ws, db_part);
         GQT_TRY(check_launch("k_weight_grad_narrow"));
-    } else if (p.dw_part) {
-        k_weight_grad<T, float><<<dim3(p.tiles.total), kThreads, 0, st>>>(
-            dyt, m, n, lddy, x, k, p.chunk, p.tiles, ws, db_part);
-        GQT_TRY(check_launch("k_weight_grad"));
     } else {
-        k_weight_grad<T, O><<<dim3(p.tiles.total), kThreads, 0, st>>>(
-            dyt, m, n, lddy, x, k, p.chunk, p.tiles, (O *)dw, db_part);
+        const dim3 grid(p.tiles.total);
+        if (p.dw_part && p.shared)
+            k_weight_grad<T, float, true><<<grid, kThreads, 0, st>>>(dyt, m, n, lddy, x, k, p.chunk,
+                                                                     p.tiles, ws, db_part);
+        else if (p.dw_part)
+            k_weight_grad<T, float, false><<<grid, kThreads, 0, st>>>(
+                dyt, m, n, lddy, x, k, p.chunk, p.tiles, ws, db_part);
+        else if (p.shared)
+            k_weight_grad<T, O, true><<<grid, kThreads, 0, st>>>(dyt, m, n, lddy, x, k, p.chunk,
+                                                                 p.tiles, (O *)dw, db_part);
+        else
+            k_weight_grad<T, O, false><<<grid, kThreads, 0, st>>>(dyt, m, n, lddy, x, k, p.chunk,
+                                                                  p.tiles, (O *)dw, db_part);
         GQT_TRY(check_launch("k_weight_grad"));
     }
     const int64_t count = (int64_t)n * k;

@@ -367,6 +367,20 @@ def test_weight_grad(m, n, k, dtype, wdtype):
         assert none is None and torch.equal(v, dw), how
 
 
+@pytest.mark.parametrize("m,n,k", [(128, 16, 8), (129, 24, 96), (130, 300, 70), (255, 9, 31),
+                                   (150, 4097, 4000), (200, 8, 4200), (96, 4400, 3900)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_weight_grad_in_one_step_and_on_large_tiles(m, n, k, dtype):
+    """A single step of tokens whose rows hold fewer than four groups (the
+    word of exponents would begin before the first), and outputs large enough
+    for squares of four tiles, ragged on both sides."""
+    a, x = kept_matrix(m, k, m + k)
+    t, dy = draw(m, n, m + n, dtype)
+    dw, db = train.gqt_weight_grad(t, a)
+    for g, e, b in zip((dw, db), plain.weight_grad(dy, x), plain.weight_grad_bounds(dy, x, "f32")):
+        within(g, e, b, (m, n, k))
+
+
 @pytest.mark.parametrize("m,n,k,dtype", [(5000, 64, 48, "bf16"), (3001, 100, 200, "f32"),
                                          (20_000, 17, 33, "bf16")])
 def test_weight_grad_over_many_tokens(m, n, k, dtype):
