@@ -45,8 +45,9 @@ namespace {
 // TPR threads hold one row, C chunks of eight columns each (chunk c of lane t
 // at column 8 (c TPR + t)), so the row is read once and its mean and the sum
 // of squared deviations from it (no cancellation, whatever the mean) are
-// taken in registers.  Rows beyond 16384 columns are read three times by
-// k_layer_norm_long, from the cache after the first.
+// taken in registers.  Rows beyond 16384 columns are
+// read three times by k_layer_norm_long, from the cache after the first.  The
+// shape goes by d alone, so that keeping a copy does not change y.
 
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float *lds)
@@ -68,19 +69,35 @@ __device__ __forceinline__ float row_sum(float v, float *lds)
     return v;
 }
 
-__device__ __forceinline__ void load_weight8(const void *w, int32_t wdtype, int32_t col, int n,
-                                             float (&v)[8])
+// Eight columns of a weight or bias; `other` without one.
+__device__ __forceinline__ void load_weight8(const void *w, int32_t wdtype, int32_t col, int32_t d,
+                                             float other, float (&v)[8])
 {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        v[k] = other;
+    if (!w || col >= d)
+        return;
     if (wdtype == GQ_IN_F32)
-        load8(static_cast<const float *>(w) + col, n, v);
+        load8(static_cast<const float *>(w), col, d, v);
     else
-        load8(static_cast<const bf16 *>(w) + col, n, v);
+        load8(static_cast<const bf16 *>(w), col, d, v);
 }
 
 template <int TPR>
 constexpr int block_threads()
 {
     return TPR > 256 ? TPR : 256;
+}
+
+// Which of the block's rows this thread works on; of a whole wave the same,
+// which leaves what depends on the row alone (two of the random numbers'
+// products) to the scalar unit.
+template <int TPR>
+__device__ __forceinline__ int row_slot()
+{
+    const int slot = threadIdx.x / TPR;
+    return TPR >= 64 ? __builtin_amdgcn_readfirstlane(slot) : slot;
 }
 
 template <typename T, int TPR, int C, bool KEEP>
@@ -95,33 +112,35 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_layer_norm(
     float wv[C][8], bv[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int col = 8 * (c * TPR + t);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            wv[c][k] = 1.0f;
-            bv[c][k] = 0.0f;
-        }
-        if (w && col < d)
-            load_weight8(w, wdtype, col, d - col, wv[c]);
-        if (b && col < d)
-            load_weight8(b, wdtype, col, d - col, bv[c]);
+        load_weight8(w, wdtype, 8 * (c * TPR + t), d, 1.0f, wv[c]);
+        load_weight8(b, wdtype, 8 * (c * TPR + t), d, 0.0f, bv[c]);
     }
-    for (int64_t base = (int64_t)blockIdx.x * kRows; base < rows;
-         base += (int64_t)gridDim.x * kRows) {
-        const int64_t row = base + threadIdx.x / TPR;
-        if (TPR <= 64 && row >= rows)
-            break; // whole rows of lanes leave; no barrier follows for TPR <= 64
+    const float inv_d = 1.0f / (float)d;
+    const int64_t stride = (int64_t)gridDim.x * kRows;
+    int64_t row = (int64_t)blockIdx.x * kRows + row_slot<TPR>();
+    if (row >= rows)
+        return; // whole rows of lanes leave, and only where no barrier follows (kRows > 1)
+    Raw8<T> ahead[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        load_ahead(x + row * ldx, 8 * (c * TPR + t), d, ahead[c]);
+    for (; row < rows; row += stride) {
         float v[C][8];
         float s = 0.0f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int col = 8 * (c * TPR + t);
-            load8(x + row * ldx + (col < d ? col : 0), d - col, v[c]);
+            settle(x + row * ldx, 8 * (c * TPR + t), d, ahead[c]);
+            unpack(ahead[c], v[c]);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 s += v[c][k];
         }
-        const float mean = row_sum<TPR>(s, lds) / (float)d;
+        // the next row is loaded while this one is worked on
+        if (row + stride < rows)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                load_ahead(x + (row + stride) * ldx, 8 * (c * TPR + t), d, ahead[c]);
+        const float mean = row_sum<TPR>(s, lds) * inv_d;
         s = 0.0f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -132,7 +151,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_layer_norm(
                 s = fmaf(col + k < d ? u : 0.0f, u, s);
             }
         }
-        const float rstd = 1.0f / sqrtf(row_sum<TPR>(s, lds) / (float)d + eps);
+        const float rstd = 1.0f / sqrtf(row_sum<TPR>(s, lds) * inv_d + eps);
         if (t == 0) {
             if (mean_out)
                 mean_out[row] = mean;
@@ -176,7 +195,7 @@ __global__ __launch_bounds__(kLongThreads) void k_layer_norm_long(
         float s = 0.0f;
         for (int64_t col = 8 * threadIdx.x; col < d; col += 8 * kLongThreads) {
             float v[8];
-            load8(xr + col, (int)(d - col), v);
+            load8(xr, (int32_t)col, d, v);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 s += v[k];
@@ -185,7 +204,7 @@ __global__ __launch_bounds__(kLongThreads) void k_layer_norm_long(
         s = 0.0f;
         for (int64_t col = 8 * threadIdx.x; col < d; col += 8 * kLongThreads) {
             float v[8];
-            load8(xr + col, (int)(d - col), v);
+            load8(xr, (int32_t)col, d, v);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const float u = v[k] - mean;
@@ -202,16 +221,9 @@ __global__ __launch_bounds__(kLongThreads) void k_layer_norm_long(
         for (int64_t col = 8 * threadIdx.x; col < cols; col += 8 * kLongThreads) {
             float v[8], wv[8], bv[8];
             const int n = (int)(d - col);
-            load8(xr + (n > 0 ? col : 0), n, v);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                wv[k] = 1.0f;
-                bv[k] = 0.0f;
-            }
-            if (w && n > 0)
-                load_weight8(w, wdtype, (int32_t)col, n, wv);
-            if (b && n > 0)
-                load_weight8(b, wdtype, (int32_t)col, n, bv);
+            load8(xr, (int32_t)col, d, v);
+            load_weight8(w, wdtype, (int32_t)col, d, 1.0f, wv);
+            load_weight8(b, wdtype, (int32_t)col, d, 0.0f, bv);
             if (keep_x.keep != kKeepNone)
                 keep8(keep_x, row, (int32_t)col, v);
 #pragma unroll
@@ -240,50 +252,69 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_layer_norm_backward(
     const void *__restrict__ w, int32_t wdtype, T *__restrict__ dx, float *__restrict__ partial)
 {
     constexpr int kRows = block_threads<TPR>() / TPR;
+    // With one chunk a thread the registers allow the next row's loads to run
+    // ahead; with more, other waves cover them.
+    constexpr bool kAhead = C == 1;
     __shared__ float lds[TPR > 64 ? TPR / 64 : 1];
     __shared__ float sums[kRows > 1 ? kRows * TPR * C * 8 : 1];
-    const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+    const int t = threadIdx.x % TPR, slot = row_slot<TPR>();
     float wv[C][8], aw[C][8], ab[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int col = 8 * (c * TPR + t);
+        load_weight8(w, wdtype, 8 * (c * TPR + t), d, 1.0f, wv[c]);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            wv[c][k] = 1.0f;
+        for (int k = 0; k < 8; ++k)
             aw[c][k] = ab[c][k] = 0.0f;
-        }
-        if (w && col < d)
-            load_weight8(w, wdtype, col, d - col, wv[c]);
     }
     const float inv_d = 1.0f / (float)d;
-    for (int64_t base = (int64_t)blockIdx.x * kRows; base < rows;
-         base += (int64_t)gridDim.x * kRows) {
-        const int64_t row = base + slot;
-        if (TPR <= 64 && row >= rows)
-            break;
-        const float mean = mean_in[row], rstd = rstd_in[row];
-        float g[C][8], xh[C][8];
-        float s1 = 0.0f, s2 = 0.0f;
+    const int64_t stride = (int64_t)gridDim.x * kRows;
+    int64_t row = (int64_t)blockIdx.x * kRows + slot;
+    Raw8<T> raw_g[C], raw_x[C];
+    RawAct8 raw_x8[C];
+    float mean = 0.0f, rstd = 0.0f;
+    const auto load = [&](int64_t r) {
+        mean = mean_in[r];
+        rstd = rstd_in[r];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int col = 8 * (c * TPR + t);
-            const int n = d - col;
-            load8(dy + row * lddy + (n > 0 ? col : 0), n, g[c]);
-            if (ACT8) {
-                if (n > 0)
-                    restore8(x8, row, col, xh[c]);
-                else
+            load_ahead(dy + r * lddy, col, d, raw_g[c]);
+            if (ACT8)
+                load_act8(x8, r, col < d ? col : 0, raw_x8[c]);
+            else
+                load_ahead(x + r * ldx, col, d, raw_x[c]);
+        }
+    };
+    if (kAhead && row < rows)
+        load(row);
+    for (; row < rows; row += stride) {
+        if (!kAhead)
+            load(row);
+        float g[C][8], xh[C][8];
+        float s1 = 0.0f, s2 = 0.0f;
+        const float r_rstd = rstd, r_mean = mean;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        xh[c][k] = 0.0f;
+        for (int c = 0; c < C; ++c) {
+            const int col = 8 * (c * TPR + t);
+            settle(dy + row * lddy, col, d, raw_g[c]);
+            unpack(raw_g[c], g[c]);
+            if (ACT8) {
+                unpack_act8(raw_x8[c], xh[c]);
             } else {
-                load8(x + row * ldx + (n > 0 ? col : 0), n, xh[c]);
+                settle(x + row * ldx, col, d, raw_x[c]);
+                unpack(raw_x[c], xh[c]);
             }
+        }
+        if (kAhead && row + stride < rows)
+            load(row + stride);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int n = d - 8 * (c * TPR + t);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 // columns past d contribute nothing, even where the
                 // statistics or the copy's padding hold a NaN
-                xh[c][k] = k < n ? (xh[c][k] - mean) * rstd : 0.0f;
+                xh[c][k] = k < n ? (xh[c][k] - r_mean) * r_rstd : 0.0f;
                 aw[c][k] = fmaf(g[c][k], xh[c][k], aw[c][k]);
                 ab[c][k] += g[c][k];
                 g[c][k] *= wv[c][k];
@@ -300,7 +331,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_layer_norm_backward(
                 continue;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                g[c][k] = rstd * (g[c][k] - s1 - xh[c][k] * s2);
+                g[c][k] = r_rstd * (g[c][k] - s1 - xh[c][k] * s2);
             store8(dx + row * d + col, d - col, g[c]);
         }
     }
@@ -336,57 +367,43 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_layer_norm_backward(
     }
 }
 
+// Rows too long for registers: dx alone, from two readings of the row.
 template <typename T, bool ACT8>
 __global__ __launch_bounds__(kLongThreads) void k_layer_norm_backward_long(
     const T *__restrict__ dy, int64_t rows, int32_t d, int64_t lddy, const T *__restrict__ x,
     int64_t ldx, Act8 x8, const float *__restrict__ mean_in, const float *__restrict__ rstd_in,
-    const void *__restrict__ w, int32_t wdtype, T *__restrict__ dx, float *__restrict__ partial)
+    const void *__restrict__ w, int32_t wdtype, T *__restrict__ dx)
 {
     __shared__ float lds[kLongThreads / 64];
     const float inv_d = 1.0f / (float)d;
-    float *out = partial ? partial + (int64_t)blockIdx.x * 2 * d : nullptr;
-    bool first = true; // the block's partial sums live in its own slice of the workspace
-    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, first = false) {
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         const float mean = mean_in[row], rstd = rstd_in[row];
         float s1 = 0.0f, s2 = 0.0f;
         for (int pass = 0; pass < 2; ++pass) {
             for (int64_t col = 8 * threadIdx.x; col < d; col += 8 * kLongThreads) {
                 const int n = (int)(d - col);
                 float g[8], xh[8], wv[8];
-                load8(dy + row * lddy + col, n, g);
+                load8(dy + row * lddy, (int32_t)col, d, g);
                 if (ACT8)
                     restore8(x8, row, (int32_t)col, xh);
                 else
-                    load8(x + row * ldx + col, n, xh);
+                    load8(x + row * ldx, (int32_t)col, d, xh);
+                load_weight8(w, wdtype, (int32_t)col, d, 1.0f, wv);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    wv[k] = 1.0f;
                     xh[k] = k < n ? (xh[k] - mean) * rstd : 0.0f;
+                    g[k] *= wv[k];
                 }
-                if (w)
-                    load_weight8(w, wdtype, (int32_t)col, n, wv);
                 if (pass == 0) {
-                    if (out) {
-                        float a[8], b[8];
-                        load8(out + col, first ? 0 : n, a);
-                        load8(out + d + col, first ? 0 : n, b);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            a[k] = fmaf(g[k], xh[k], a[k]);
-                            b[k] += g[k];
-                        }
-                        store8(out + col, n, a);
-                        store8(out + d + col, n, b);
-                    }
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        s1 = fmaf(g[k], wv[k], s1);
-                        s2 = fmaf(g[k] * wv[k], xh[k], s2);
+                        s1 += g[k];
+                        s2 = fmaf(g[k], xh[k], s2);
                     }
                 } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        g[k] = rstd * (g[k] * wv[k] - s1 - xh[k] * s2);
+                        g[k] = rstd * (g[k] - s1 - xh[k] * s2);
                     store8(dx + row * d + col, n, g);
                 }
             }
@@ -396,6 +413,39 @@ __global__ __launch_bounds__(kLongThreads) void k_layer_norm_backward_long(
             }
         }
     }
+}
+
+// and their partial sums for dw and db, 2048 columns a block along x, the rows
+// dealt out along y (adding them up in memory row by row took 265 us at 5461 x
+// 12288, a second reading of dy and x half of that).
+template <typename T, bool ACT8>
+__global__ __launch_bounds__(256) void k_norm_column_sums(
+    const T *__restrict__ dy, int64_t rows, int32_t d, int64_t lddy, const T *__restrict__ x,
+    int64_t ldx, Act8 x8, const float *__restrict__ mean_in, const float *__restrict__ rstd_in,
+    float *__restrict__ partial)
+{
+    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (at >= d)
+        return;
+    const int32_t col = (int32_t)at;
+    float aw[8] = {}, ab[8] = {};
+    for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+        const float mean = mean_in[row], rstd = rstd_in[row];
+        float g[8], xh[8];
+        load8(dy + row * lddy, col, d, g);
+        if (ACT8)
+            restore8(x8, row, col, xh);
+        else
+            load8(x + row * ldx, col, d, xh);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            aw[k] = fmaf(g[k], (xh[k] - mean) * rstd, aw[k]);
+            ab[k] += g[k];
+        }
+    }
+    float *const out = partial + (int64_t)blockIdx.y * 2 * d + col;
+    store8(out, d - col, aw);
+    store8(out + d, d - col, ab);
 }
 
 // dw and db: the blocks' partial sums added in block order, a sixteenth of
@@ -486,9 +536,8 @@ __global__ __launch_bounds__(kThreads) void k_act8_save(const T *__restrict__ x,
     if (i >= chunks)
         return;
     const Chunk c = chunk_at(i, per_row);
-    const int n = d - c.col;
     float v[8];
-    load8(x + c.row * ldx + (n > 0 ? c.col : 0), n, v);
+    load8(x + c.row * ldx, c.col, d, v);
     keep8(out, c.row, c.col, v);
 }
 
@@ -581,7 +630,7 @@ __global__ __launch_bounds__(kThreads) void k_gelu(const T *__restrict__ h, uint
     const Chunk c = chunk_at(i, per_row);
     const int n = d - c.col;
     float v[8];
-    load8(h + c.row * ldh + (n > 0 ? c.col : 0), n, v);
+    load8(h + c.row * ldh, c.col, d, v);
     if (KEEP && keep_h.keep != kKeepNone)
         keep8(keep_h, c.row, c.col, v);
 #pragma unroll
@@ -606,11 +655,11 @@ __global__ __launch_bounds__(kThreads) void k_gelu_backward(
     if (n <= 0)
         return;
     float g[8], v[8];
-    load8(dy + c.row * lddy + c.col, n, g);
+    load8(dy + c.row * lddy, c.col, d, g);
     if (ACT8)
         restore8(h8, c.row, c.col, v);
     else
-        load8(h + c.row * ldh + c.col, n, v);
+        load8(h + c.row * ldh, c.col, d, v);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         g[k] *= gelu_slope<FORM>(v[k]);
@@ -678,45 +727,70 @@ namespace {
 
 constexpr int kCUs = 256;
 
-// Layer norm shapes: the fewest threads per row (whole waves from 64 on)
-// whose C <= 4 chunks each hold d.
+// Layer norm shapes: threads per row (whole waves from 64 on) and chunks a
+// thread, so that few lanes are idle (at half of them d = 256 and 5120 ran at
+// 3.4 and 2.7 TB/s) and the gradient's sums do not spill.
 #define GQT_BY_ROW_LENGTH(LAUNCH, LONG) \
     do {                                \
-        if (d <= 128)                   \
+        if (d <= 32)                    \
+            LAUNCH(4, 1);               \
+        else if (d <= 64)               \
+            LAUNCH(8, 1);               \
+        else if (d <= 128)              \
             LAUNCH(16, 1);              \
+        else if (d <= 256)              \
+            LAUNCH(32, 1);              \
         else if (d <= 512)              \
             LAUNCH(64, 1);              \
         else if (d <= 1024)             \
             LAUNCH(64, 2);              \
+        else if (d <= 1536)             \
+            LAUNCH(64, 3);              \
         else if (d <= 2048)             \
             LAUNCH(256, 1);             \
         else if (d <= 4096)             \
             LAUNCH(256, 2);             \
-        else if (d <= 8192)             \
-            LAUNCH(256, 4);             \
-        else if (d <= 16384)            \
-            LAUNCH(512, 4);             \
+        else if (d <= 6144)             \
+            LAUNCH(256, 3);             \
         else                            \
             LONG();                     \
     } while (0)
 
 // Rows that one block takes at a time.
-int64_t rows_per_block(int64_t d) { return d <= 128 ? 16 : d <= 1024 ? 4 : 1; }
+int64_t rows_per_block(int64_t d)
+{
+    return d <= 32 ? 64 : d <= 64 ? 32 : d <= 128 ? 16 : d <= 256 ? 8 : d <= 1536 ? 4 : 1;
+}
 
-// Blocks of a layer norm launch: each loops over its rows with the weights
-// in registers.
+// Blocks of a layer norm launch: four turns each with the weights in
+// registers where that leaves 8 blocks a CU, so that late blocks even out.
 int64_t norm_blocks(int64_t rows, int64_t d)
 {
     const int64_t all = (rows + rows_per_block(d) - 1) / rows_per_block(d);
-    const int64_t most = d > 8192 ? 2 * kCUs : 8 * kCUs;
-    return all < most ? all : most;
+    const int64_t least = 8 * kCUs;
+    const int64_t want = all / 4 > least ? all / 4 : least;
+    return all < want ? all : want;
 }
 
-// The gradient's blocks: fewer, since each leaves 2 d partial sums.
+constexpr int64_t kMostGradColumns = 8192; // beyond, dw and db have a kernel of their own
+
+// Blocks that leave 2 d partial sums each.  As many as their registers let a
+// CU hold at once: a part of a round more costs a round (16384 x 4096 takes
+// 131 us with 3 blocks a CU, 146 with 4).
 int64_t grad_blocks(int64_t rows, int64_t d)
 {
     const int64_t all = (rows + rows_per_block(d) - 1) / rows_per_block(d);
-    const int64_t most = d > 8192 ? kCUs : 4 * kCUs;
+    int64_t most;
+    if (d > kMostGradColumns) // that many rows of blocks of 2048 columns
+        most = (4 * kCUs * 2048 + d - 1) / d;
+    else if (d > 6144)
+        most = kCUs;
+    else if ((d > 1024 && d <= 1536) || d > 4096) // three chunks
+        most = 2 * kCUs;
+    else if ((d > 512 && d <= 1024) || d > 2048) // two
+        most = 3 * kCUs;
+    else
+        most = 4 * kCUs;
     return all < most ? all : most;
 }
 
@@ -730,20 +804,32 @@ int32_t launch_norm(const void *x, int64_t rows, int32_t d, int64_t ldx, const v
     const T *xt = (const T *)x;
     T *yt = (T *)y;
     const bool keep = sx || sy;
-#define GQT_LAUNCH(TPR, C)                                                                       \
-    do {                                                                                         \
-        if (keep)                                                                                \
-            k_layer_norm<T, TPR, C, true><<<grid, block_threads<TPR>(), 0, st>>>(                \
-                xt, rows, d, ldx, w, b, wdtype, eps, yt, mean, rstd, kx, ky);                    \
-        else                                                                                     \
-            k_layer_norm<T, TPR, C, false><<<grid, block_threads<TPR>(), 0, st>>>(               \
-                xt, rows, d, ldx, w, b, wdtype, eps, yt, mean, rstd, kx, ky);                    \
+#define GQT_KERNEL(TPR, C, KEEP)                                                                 \
+    k_layer_norm<T, TPR, C, KEEP><<<grid, block_threads<TPR>(), 0, st>>>(                \
+        xt, rows, d, ldx, w, b, wdtype, eps, yt, mean, rstd, kx, ky)
+#define GQT_LAUNCH(TPR, C)               \
+    do {                                 \
+        if (keep)                        \
+            GQT_KERNEL(TPR, C, true);    \
+        else                             \
+            GQT_KERNEL(TPR, C, false);   \
     } while (0)
 #define GQT_LONG()                                                                               \
     k_layer_norm_long<T><<<grid, kLongThreads, 0, st>>>(xt, rows, d, ldx, w, b, wdtype, eps, yt, \
                                                         mean, rstd, kx, ky)
-    GQT_BY_ROW_LENGTH(GQT_LAUNCH, GQT_LONG);
+#define GQT_LONGER()            \
+    do {                        \
+        if (d <= 8192)          \
+            GQT_LAUNCH(512, 2); \
+        else if (d <= 16384)    \
+            GQT_LAUNCH(512, 4); \
+        else                    \
+            GQT_LONG();         \
+    } while (0)
+    GQT_BY_ROW_LENGTH(GQT_LAUNCH, GQT_LONGER);
+#undef GQT_LONGER
 #undef GQT_LAUNCH
+#undef GQT_KERNEL
 #undef GQT_LONG
     return check_launch("k_layer_norm");
 }
@@ -755,30 +841,45 @@ int32_t launch_norm_backward(const void *dy, int64_t rows, int32_t d, int64_t ld
                              float *partial, hipStream_t st)
 {
     const Act8 a = act8_view(x ? nullptr : x8, d);
-    const dim3 grid((uint32_t)grad_blocks(rows, d));
+    const int64_t blocks = grad_blocks(rows, d);
+    const dim3 grid((uint32_t)blocks);
     const T *dyt = (const T *)dy, *xt = (const T *)x;
     T *dxt = (T *)dx;
-#define GQT_LAUNCH(TPR, C)                                                                       \
-    do {                                                                                         \
-        if (x)                                                                                   \
-            k_layer_norm_backward<T, TPR, C, false><<<grid, block_threads<TPR>(), 0, st>>>(      \
-                dyt, rows, d, lddy, xt, ldx, a, mean, rstd, w, wdtype, dxt, partial);            \
-        else                                                                                     \
-            k_layer_norm_backward<T, TPR, C, true><<<grid, block_threads<TPR>(), 0, st>>>(       \
-                dyt, rows, d, lddy, xt, ldx, a, mean, rstd, w, wdtype, dxt, partial);            \
+#define GQT_KERNEL(TPR, C, ACT8)                                                                 \
+    k_layer_norm_backward<T, TPR, C, ACT8><<<grid, block_threads<TPR>(), 0, st>>>(       \
+        dyt, rows, d, lddy, xt, ldx, a, mean, rstd, w, wdtype, dxt, partial)
+#define GQT_LAUNCH(TPR, C)               \
+    do {                                 \
+        if (x)                           \
+            GQT_KERNEL(TPR, C, false);   \
+        else                             \
+            GQT_KERNEL(TPR, C, true);    \
     } while (0)
-#define GQT_LONG()                                                                               \
-    do {                                                                                         \
-        if (x)                                                                                   \
-            k_layer_norm_backward_long<T, false><<<grid, kLongThreads, 0, st>>>(                 \
-                dyt, rows, d, lddy, xt, ldx, a, mean, rstd, w, wdtype, dxt, partial);            \
-        else                                                                                     \
-            k_layer_norm_backward_long<T, true><<<grid, kLongThreads, 0, st>>>(                  \
-                dyt, rows, d, lddy, xt, ldx, a, mean, rstd, w, wdtype, dxt, partial);            \
-    } while (0)
-    GQT_BY_ROW_LENGTH(GQT_LAUNCH, GQT_LONG);
+    if (d > kMostGradColumns) {
+        const dim3 all((uint32_t)(rows < 2 * kCUs ? rows : 2 * kCUs));
+        if (x)
+            k_layer_norm_backward_long<T, false><<<all, kLongThreads, 0, st>>>(
+                dyt, rows, d, lddy, xt, ldx, a, mean, rstd, w, wdtype, dxt);
+        else
+            k_layer_norm_backward_long<T, true><<<all, kLongThreads, 0, st>>>(
+                dyt, rows, d, lddy, xt, ldx, a, mean, rstd, w, wdtype, dxt);
+        GQT_TRY(check_launch("k_layer_norm_backward_long"));
+        if (!partial)
+            return ok();
+        const dim3 parts((uint32_t)((d + 2047) / 2048), (uint32_t)blocks);
+        if (x)
+            k_norm_column_sums<T, false><<<parts, 256, 0, st>>>(dyt, rows, d, lddy, xt, ldx, a, mean,
+                                                                rstd, partial);
+        else
+            k_norm_column_sums<T, true><<<parts, 256, 0, st>>>(dyt, rows, d, lddy, xt, ldx, a, mean,
+                                                               rstd, partial);
+        return check_launch("k_norm_column_sums");
+    }
+#define GQT_LONGER() GQT_LAUNCH(512, 2)
+    GQT_BY_ROW_LENGTH(GQT_LAUNCH, GQT_LONGER);
+#undef GQT_LONGER
 #undef GQT_LAUNCH
-#undef GQT_LONG
+#undef GQT_KERNEL
     return check_launch("k_layer_norm_backward");
 }
 

@@ -57,38 +57,91 @@ typedef u32x4 u32x4_e4 __attribute__((aligned(4)));
 
 __device__ __forceinline__ float bits_f32(uint32_t u) { return __uint_as_float(u); }
 
-// Eight consecutive elements at p as floats; those from n on read as 0.
-__device__ __forceinline__ void load8(const bf16 *p, int n, float (&v)[8])
+// Eight consecutive elements as loaded, and as floats.
+template <typename T>
+struct Raw8 {
+    u32x4 w[sizeof(T) / 2];
+};
+__device__ __forceinline__ void load_words(const bf16 *p, Raw8<bf16> &r)
 {
-    if (n >= 8) {
-        const u32x4 w = *reinterpret_cast<const u32x4_e2 *>(p);
+    r.w[0] = *reinterpret_cast<const u32x4_e2 *>(p);
+}
+__device__ __forceinline__ void load_words(const float *p, Raw8<float> &r)
+{
+    r.w[0] = *reinterpret_cast<const u32x4_e4 *>(p);
+    r.w[1] = *reinterpret_cast<const u32x4_e4 *>(p + 4);
+}
+__device__ __forceinline__ void unpack(const Raw8<bf16> &r, float (&v)[8])
+{
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[2 * k] = bits_f32(w[k] << 16);
-            v[2 * k + 1] = bits_f32(w[k] & 0xFFFF0000u);
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            v[k] = k < n ? (float)p[k] : 0.0f;
+    for (int k = 0; k < 4; ++k) {
+        v[2 * k] = bits_f32(r.w[0][k] << 16);
+        v[2 * k + 1] = bits_f32(r.w[0][k] & 0xFFFF0000u);
     }
 }
-
-__device__ __forceinline__ void load8(const float *p, int n, float (&v)[8])
+__device__ __forceinline__ void unpack(const Raw8<float> &r, float (&v)[8])
 {
-    if (n >= 8) {
-        const u32x4 a = *reinterpret_cast<const u32x4_e4 *>(p);
-        const u32x4 b = *reinterpret_cast<const u32x4_e4 *>(p + 4);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[k] = bits_f32(a[k]);
-            v[4 + k] = bits_f32(b[k]);
+    for (int k = 0; k < 8; ++k)
+        v[k] = bits_f32(r.w[k / 4][k % 4]);
+}
+
+// One element towards the front, 0 behind.
+__device__ __forceinline__ void shift_one(Raw8<bf16> &r)
+{
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        r.w[0][k] = __builtin_amdgcn_alignbit(r.w[0][k + 1], r.w[0][k], 16);
+    r.w[0][3] >>= 16;
+}
+__device__ __forceinline__ void shift_one(Raw8<float> &r)
+{
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+        r.w[k / 4][k % 4] = r.w[(k + 1) / 4][(k + 1) % 4];
+    r.w[1][3] = 0;
+}
+__device__ __forceinline__ uint32_t bits_of(const bf16 *p) { return *(const uint16_t *)p; }
+__device__ __forceinline__ uint32_t bits_of(const float *p) { return __float_as_uint(*p); }
+
+// The eight columns from col on of a row of d, in two halves, so that a loop
+// can load a row ahead: one unconditional load, which for the columns next
+// to the row's end takes its last eight; then those moved into place, with 0
+// past the end.
+template <typename T>
+__device__ __forceinline__ void load_ahead(const T *row, int32_t col, int32_t d, Raw8<T> &r)
+{
+    if (d >= 8) // uniform
+        load_words(row + min(col, d - 8), r);
+}
+template <typename T>
+__device__ __forceinline__ void settle(const T *row, int32_t col, int32_t d, Raw8<T> &r)
+{
+    constexpr int kPer = 4 / sizeof(T); // elements a word
+    if (col + 8 <= d)
+        return;
+    if (d < 8) {
+#pragma unroll
+        for (int k = 0; k < 8 / kPer; ++k) {
+            uint32_t w = 0;
+#pragma unroll
+            for (int h = 0; h < kPer; ++h)
+                if (col + kPer * k + h < d)
+                    w |= bits_of(row + col + kPer * k + h) << (16 * h);
+            r.w[k / 4][k % 4] = w;
         }
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            v[k] = k < n ? p[k] : 0.0f;
+        return;
     }
+    for (int at = max(d - col, 0); at < 8; ++at)
+        shift_one(r);
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T *row, int32_t col, int32_t d, float (&v)[8])
+{
+    Raw8<T> r;
+    load_ahead(row, col, d, r);
+    settle(row, col, d, r);
+    unpack(r, v);
 }
 
 // Rounds v to T in place (the value that a later reader of the output sees)
@@ -186,6 +239,31 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t m)
     return max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, true)); // lane ^ 2
 }
 
+// perm: byte s of the result is byte sel[s] of (hi, lo), lo's being 0 to 3;
+// 9 and 11 give lo's and hi's sign (the top bit of byte 3) eight times.
+__device__ __forceinline__ uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel)
+{
+    return __builtin_amdgcn_perm(hi, lo, sel);
+}
+
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pk_max_u16(uint32_t a, uint32_t b)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                  __builtin_bit_cast(u16x2, b)));
+}
+__device__ __forceinline__ uint32_t pk_min_u16(uint32_t a, uint32_t b)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(u16x2, a),
+                                                                  __builtin_bit_cast(u16x2, b)));
+}
+__device__ __forceinline__ uint32_t pk_sub_u16(uint32_t a, uint32_t b)
+{
+    return __builtin_bit_cast(uint32_t,
+                              (u16x2)(__builtin_bit_cast(u16x2, a) - __builtin_bit_cast(u16x2, b)));
+}
+
 // Writes the codes of the eight values at (row, col), col a multiple of 8;
 // the four lanes of a quad hold one group's four parts, all of them active,
 // and columns past d hold 0.  Scaling by a power of two is exact, so the
@@ -203,48 +281,64 @@ __device__ __forceinline__ void keep8(const Act8 &a, int64_t row, int32_t col, c
     // fraction bits are 0x7E0000
     const bool finite = m < 0x7F800000u;
     const uint32_t e = finite ? max((m + 0x1FFFFu) >> 23, 7u) - 6u : 255u;
-    const float inv = bits_f32((254u - (finite ? e : 127u)) << 23);
-    const int top = e == 249u ? 63 : 127;
-    int q[8];
+    const bool highest = e == 249u; // where 64 2^E has no float
+    u32x2 w;
     if (a.keep == kKeepNearest) {
+        // Adding 1.5 2^23 rounds the scaled value to an integer (ties to
+        // even) and leaves it in the low byte.
+        const float inv = bits_f32((254u - e) << 23);
+        uint32_t q[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            q[k] = min(max((int)rintf(finite ? v[k] * inv : 0.0f), -top), top);
+        for (int k = 0; k < 8; ++k) {
+            float f = fmaf(v[k], inv, 0x1.8p23f);
+            if (highest)
+                f = fminf(fmaxf(f, 0x1.8p23f - 63.0f), 0x1.8p23f + 63.0f);
+            q[k] = __float_as_uint(f);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            w[h] = perm(perm(q[4 * h + 3], q[4 * h + 2], 0x0C0C0400u),
+                        perm(q[4 * h + 1], q[4 * h], 0x0C0C0400u), 0x05040100u);
     } else {
         // S = floor(t 2^16) + (0xFFFF - h) for the high half h of u carries
         // into bit 16 exactly when h is below the high half of frac 2^32; a
         // tie leaves 16 ones and takes the low half, from the second draw.
         const uint32_t blk = (uint32_t)col >> 3, r0 = (uint32_t)row;
+        const int scale = 127 - (int)e; // t = |x| 2^scale
         const uint4 A = philox10(make_uint4(blk, 0u, r0, 0u), a.k0, a.k1);
-        uint32_t S[8];
-        bool tie = false;
+        const uint4 N = make_uint4(~A.x, ~A.y, ~A.z, ~A.w);
+        uint32_t S[8], most = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float t = finite ? fabsf(v[k]) * inv : 0.0f;
-            S[k] = (uint32_t)(t * 0x1p16f) + (0xFFFFu - half16(A, k));
-            tie |= (S[k] & 0xFFFFu) == 0xFFFFu;
-        }
-        if (tie) {
+        for (int k = 0; k < 8; ++k)
+            S[k] = (uint32_t)ldexpf(fabsf(v[k]), scale + 16) + half16(N, k);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            most = pk_max_u16(most, perm(S[2 * k + 1], S[2 * k], 0x05040100u));
+        if ((most >> 16) == 0xFFFFu || (most & 0xFFFFu) == 0xFFFFu) {
             const uint4 B = philox10(make_uint4(blk, 0u, r0, 1u), a.k0, a.k1);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float t = finite ? fabsf(v[k]) * inv : 0.0f;
+                const float t = ldexpf(fabsf(v[k]), scale);
                 const uint32_t F = (uint32_t)((t - floorf(t)) * 0x1p32f);
                 if ((S[k] & 0xFFFFu) == 0xFFFFu && half16(B, k) < (F & 0xFFFFu))
                     S[k] += 1u;
             }
         }
+        // magnitudes in pairs of 16 bits, negated by xor and subtraction
+        const uint32_t top = highest ? 63u * 0x10001u : 127u * 0x10001u;
+        uint32_t q[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int mag = min((int)(S[k] >> 16), top);
-            q[k] = __float_as_uint(v[k]) >> 31 ? -mag : mag;
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t mag = pk_min_u16(perm(S[2 * k + 1], S[2 * k], 0x07060302u), top);
+            const uint32_t sign =
+                perm(__float_as_uint(v[2 * k + 1]), __float_as_uint(v[2 * k]), 0x0B0B0909u);
+            q[k] = pk_sub_u16(mag ^ sign, sign);
         }
+        w[0] = perm(q[1], q[0], 0x06040200u);
+        w[1] = perm(q[3], q[2], 0x06040200u);
     }
-    u32x2 w;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-        w[h] = (uint32_t)(q[4 * h] & 0xFF) | (uint32_t)(q[4 * h + 1] & 0xFF) << 8 |
-               (uint32_t)(q[4 * h + 2] & 0xFF) << 16 | (uint32_t)q[4 * h + 3] << 24;
+    if (!finite)
+        w = u32x2{0, 0};
     *reinterpret_cast<u32x2 *>(a.codes + row * a.pitch + col) = w;
     if ((col & 24) == 0)
         a.exps[row * a.groups + (col >> 5)] = (uint8_t)e;
@@ -256,14 +350,29 @@ __device__ __forceinline__ float step_of(uint32_t e)
     return bits_f32(e == 255u ? 0x7FC00000u : e << 23);
 }
 
-// The eight values at (row, col), col a multiple of 8 and below the pitch.
-__device__ __forceinline__ void restore8(const Act8 &a, int64_t row, int32_t col, float (&v)[8])
+// The eight values at (row, col), col a multiple of 8 and below the pitch, as
+// loaded and as floats.
+struct RawAct8 {
+    u32x2 w;
+    uint32_t e;
+};
+__device__ __forceinline__ void load_act8(const Act8 &a, int64_t row, int32_t col, RawAct8 &r)
 {
-    const u32x2 w = *reinterpret_cast<const u32x2 *>(a.codes + row * a.pitch + col);
-    const float step = step_of(a.exps[row * a.groups + (col >> 5)]);
+    r.w = *reinterpret_cast<const u32x2 *>(a.codes + row * a.pitch + col);
+    r.e = a.exps[row * a.groups + (col >> 5)];
+}
+__device__ __forceinline__ void unpack_act8(const RawAct8 &r, float (&v)[8])
+{
+    const float step = step_of(r.e);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-        v[k] = (float)((int)(w[k >> 2] << (24 - 8 * (k & 3))) >> 24) * step;
+        v[k] = (float)((int)(r.w[k >> 2] << (24 - 8 * (k & 3))) >> 24) * step;
+}
+__device__ __forceinline__ void restore8(const Act8 &a, int64_t row, int32_t col, float (&v)[8])
+{
+    RawAct8 r;
+    load_act8(a, row, col, r);
+    unpack_act8(r, v);
 }
 
 } // namespace gqt

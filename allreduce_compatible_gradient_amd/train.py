@@ -181,8 +181,15 @@ def _elsewhere(device, stream) -> bool:
     return stream is not None or device.index != torch.cuda.current_device()
 
 
-def _current() -> int:
-    return torch.cuda.current_stream().cuda_stream
+def _current(device) -> int:
+    """The current stream's handle; the accessor that builds no stream object
+    takes 0.1 us of a call's 7, torch.cuda.current_stream 2.5."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _like(x):
+    """A new contiguous tensor of x's shape, dtype and device."""
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 # ---------------------------------------------------------------------------
@@ -252,7 +259,7 @@ def gqt_act8_save(x: torch.Tensor, *, seed=None, out: Act8 | None = None, stream
     if out is None:
         out = Act8.empty(rows, d, x.device)
     _check(lib().gqt_act8_save(x.data_ptr(), dt, rows, d, ldx,
-                               _kept(out, "out", rows, d, x.device, seed), _current()))
+                               _kept(out, "out", rows, d, x.device, seed), _current(x.device)))
     return out
 
 
@@ -268,7 +275,7 @@ def gqt_act8_restore(a: Act8, dtype=torch.bfloat16, *, stream=None) -> torch.Ten
     rows, d = a.shape
     out = torch.empty((rows, d), dtype=dtype, device=device)
     _check(lib().gqt_act8_restore(_kept(a, "a", rows, d, device), rows, d, dt, out.data_ptr(),
-                                  _current()))
+                                  _current(device)))
     return out
 
 
@@ -289,7 +296,7 @@ def gqt_layer_norm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, *
                                   save_y=save_y, seed_y=seed_y)
     rows, d = x.shape
     wdt = _weights(weight, bias, d, device)
-    y = torch.empty((rows, d), dtype=x.dtype, device=device)
+    y = _like(x)
     mean = rstd = None
     if stats:
         mean = torch.empty(rows, dtype=torch.float32, device=device)
@@ -297,7 +304,7 @@ def gqt_layer_norm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, *
     _check(lib().gqt_layer_norm(x.data_ptr(), dt, rows, d, ldx, _ptr(weight), _ptr(bias), wdt,
                                 eps, y.data_ptr(), _ptr(mean), _ptr(rstd),
                                 _kept(save_x, "save_x", rows, d, device, seed_x),
-                                _kept(save_y, "save_y", rows, d, device, seed_y), _current()))
+                                _kept(save_y, "save_y", rows, d, device, seed_y), _current(device)))
     return y, mean, rstd
 
 
@@ -326,7 +333,7 @@ def gqt_layer_norm_backward(dy: torch.Tensor, x, mean: torch.Tensor, rstd: torch
     else:
         _, ldx = _matrix(x, "x", dy.shape, dy.dtype, device)
         xp = x.data_ptr() or None
-    dx = torch.empty((rows, d), dtype=dy.dtype, device=device)
+    dx = _like(dy)
     wt = torch.float32 if weight is None else weight.dtype
     dw = torch.empty(d, dtype=wt, device=device) if weight_grad else None
     db = torch.empty(d, dtype=wt, device=device) if bias_grad else None
@@ -339,7 +346,7 @@ def gqt_layer_norm_backward(dy: torch.Tensor, x, mean: torch.Tensor, rstd: torch
     _check(lib().gqt_layer_norm_backward(dy.data_ptr(), dt, rows, d, lddy, xp, ldx, x8,
                                          mean.data_ptr(), rstd.data_ptr(), _ptr(weight), wdt,
                                          dx.data_ptr(), _ptr(dw), _ptr(db), _ptr(ws), nws,
-                                         _current()))
+                                         _current(device)))
     return dx, dw, db
 
 
@@ -365,10 +372,10 @@ def gqt_gelu(h: torch.Tensor, approximate: str = "none", *, save_h: Act8 | None 
             return gqt_gelu(h, approximate, save_h=save_h, seed_h=seed_h, save_y=save_y,
                             seed_y=seed_y)
     rows, d = h.shape
-    y = torch.empty((rows, d), dtype=h.dtype, device=device)
+    y = _like(h)
     _check(lib().gqt_gelu(h.data_ptr(), dt, rows, d, ldh, form, y.data_ptr(),
                           _kept(save_h, "save_h", rows, d, device, seed_h),
-                          _kept(save_y, "save_y", rows, d, device, seed_y), _current()))
+                          _kept(save_y, "save_y", rows, d, device, seed_y), _current(device)))
     return y
 
 
@@ -390,9 +397,9 @@ def gqt_gelu_backward(dy: torch.Tensor, h, approximate: str = "none", *,
         hp = h.data_ptr() or None
         if hp is None:
             h8 = _CAct8()  # an empty h has no address
-    dh = torch.empty((rows, d), dtype=dy.dtype, device=device)
+    dh = _like(dy)
     _check(lib().gqt_gelu_backward(dy.data_ptr(), dt, rows, d, lddy, hp, ldh, h8, form,
-                                   dh.data_ptr(), _current()))
+                                   dh.data_ptr(), _current(device)))
     return dh
 
 
@@ -428,7 +435,7 @@ def gqt_weight_grad(dy: torch.Tensor, x: Act8, *, dtype=torch.float32, bias: boo
           or workspace.numel() * workspace.element_size() < need):
         raise ValueError(f"workspace must be contiguous, on {device}, of {need} bytes")
     _check(lib().gqt_weight_grad(dy.data_ptr(), dt, m, n, lddy, x8, k, dw.data_ptr(), _ptr(db),
-                                 wdt, _ptr(workspace), max(need, 0), _current()))
+                                 wdt, _ptr(workspace), max(need, 0), _current(device)))
     return dw, db
 
 

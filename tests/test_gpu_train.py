@@ -142,7 +142,7 @@ def test_save_of_a_broadcast_row():
 
 # both sides of every change of the kernel's shape
 LENGTHS = [1, 5, 64, 128, 129, 512, 513, 1000, 1024, 1025, 2047, 2049, 4096, 4097, 8192, 8193,
-           16384, 16385, 20001]
+           16384, 16385, 20001, 7, 8, 9, 31, 32, 33, 65, 256, 257, 1536, 1537, 6144, 6145]
 
 
 @pytest.mark.parametrize("d", LENGTHS)
