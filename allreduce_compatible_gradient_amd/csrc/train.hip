@@ -162,7 +162,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_layer_norm(
         for (int c = 0; c < C; ++c) {
             const int col = 8 * (c * TPR + t);
             if (KEEP && keep_x.keep != kKeepNone)
-                keep8(keep_x, row, col, v[c]);
+                keep8(keep_x, row, col, keep_x.chunk(row, col), v[c]);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 v[c][k] = fmaf((v[c][k] - mean) * rstd, wv[c][k], bv[c][k]);
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_layer_norm(
                 for (int k = 0; k < 8; ++k)
                     if (col + k >= d)
                         v[c][k] = 0.0f;
-                keep8(keep_y, row, col, v[c]);
+                keep8(keep_y, row, col, keep_y.chunk(row, col), v[c]);
             }
         }
     }
@@ -225,7 +225,7 @@ __global__ __launch_bounds__(kLongThreads) void k_layer_norm_long(
             load_weight8(w, wdtype, (int32_t)col, d, 1.0f, wv);
             load_weight8(b, wdtype, (int32_t)col, d, 0.0f, bv);
             if (keep_x.keep != kKeepNone)
-                keep8(keep_x, row, (int32_t)col, v);
+                keep8(keep_x, row, (int32_t)col, keep_x.chunk(row, (int32_t)col), v);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 v[k] = fmaf((v[k] - mean) * rstd, wv[k], bv[k]);
@@ -236,7 +236,7 @@ __global__ __launch_bounds__(kLongThreads) void k_layer_norm_long(
                 for (int k = 0; k < 8; ++k)
                     if (k >= n)
                         v[k] = 0.0f;
-                keep8(keep_y, row, (int32_t)col, v);
+                keep8(keep_y, row, (int32_t)col, keep_y.chunk(row, (int32_t)col), v);
             }
         }
     }
@@ -280,7 +280,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_layer_norm_backward(
             const int col = 8 * (c * TPR + t);
             load_ahead(dy + r * lddy, col, d, raw_g[c]);
             if (ACT8)
-                load_act8(x8, r, col < d ? col : 0, raw_x8[c]);
+                load_act8(x8, x8.chunk(r, col < d ? col : 0), raw_x8[c]);
             else
                 load_ahead(x + r * ldx, col, d, raw_x[c]);
         }
@@ -385,7 +385,7 @@ __global__ __launch_bounds__(kLongThreads) void k_layer_norm_backward_long(
                 float g[8], xh[8], wv[8];
                 load8(dy + row * lddy, (int32_t)col, d, g);
                 if (ACT8)
-                    restore8(x8, row, (int32_t)col, xh);
+                    restore8(x8, x8.chunk(row, (int32_t)col), xh);
                 else
                     load8(x + row * ldx, (int32_t)col, d, xh);
                 load_weight8(w, wdtype, (int32_t)col, d, 1.0f, wv);
@@ -434,7 +434,7 @@ __global__ __launch_bounds__(256) void k_norm_column_sums(
         float g[8], xh[8];
         load8(dy + row * lddy, col, d, g);
         if (ACT8)
-            restore8(x8, row, col, xh);
+            restore8(x8, x8.chunk(row, col), xh);
         else
             load8(x + row * ldx, col, d, xh);
 #pragma unroll
@@ -538,7 +538,7 @@ __global__ __launch_bounds__(kThreads) void k_act8_save(const T *__restrict__ x,
     const Chunk c = chunk_at(i, per_row);
     float v[8];
     load8(x + c.row * ldx, c.col, d, v);
-    keep8(out, c.row, c.col, v);
+    keep8(out, c.row, c.col, i, v);
 }
 
 template <typename T>
@@ -553,7 +553,7 @@ __global__ __launch_bounds__(kThreads) void k_act8_restore(Act8 in, uint32_t chu
     if (c.col >= d)
         return;
     float v[8];
-    restore8(in, c.row, c.col, v);
+    restore8(in, i, v);
     store8(out + c.row * d + c.col, d - c.col, v);
 }
 
@@ -632,14 +632,14 @@ __global__ __launch_bounds__(kThreads) void k_gelu(const T *__restrict__ h, uint
     float v[8];
     load8(h + c.row * ldh, c.col, d, v);
     if (KEEP && keep_h.keep != kKeepNone)
-        keep8(keep_h, c.row, c.col, v);
+        keep8(keep_h, c.row, c.col, i, v);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         v[k] = gelu<FORM>(v[k]);
     if (n > 0)
         store8(y + c.row * d + c.col, n, v); // columns past d: gelu(0) = 0
     if (KEEP && keep_y.keep != kKeepNone)
-        keep8(keep_y, c.row, c.col, v);
+        keep8(keep_y, c.row, c.col, i, v);
 }
 
 template <typename T, int FORM, bool ACT8>
@@ -657,7 +657,7 @@ __global__ __launch_bounds__(kThreads) void k_gelu_backward(
     float g[8], v[8];
     load8(dy + c.row * lddy, c.col, d, g);
     if (ACT8)
-        restore8(h8, c.row, c.col, v);
+        restore8(h8, i, v);
     else
         load8(h + c.row * ldh, c.col, d, v);
 #pragma unroll

@@ -208,7 +208,8 @@ __device__ __forceinline__ uint32_t half16(const uint4 &w, int k)
     return (k & 1) ? (word >> 16) : (word & 0xFFFFu);
 }
 
-// An 8-bit copy as the kernels see it.
+// An 8-bit copy as the kernels see it.  Eight columns are a chunk: chunk i of
+// the whole copy has its codes at 8 i and its exponent at i / 4.
 enum { kKeepNone = 0, kKeepNearest = 1, kKeepRandom = 2 };
 struct Act8 {
     int8_t *codes;
@@ -217,6 +218,11 @@ struct Act8 {
     int32_t groups; // bytes of a row of exps
     int32_t keep;
     uint32_t k0, k1;
+
+    __device__ __forceinline__ int64_t chunk(int64_t row, int32_t col) const
+    {
+        return row * (pitch >> 3) + (col >> 3);
+    }
 };
 
 inline Act8 act8_view(const gqt_act8 *a, int64_t d)
@@ -264,11 +270,12 @@ __device__ __forceinline__ uint32_t pk_sub_u16(uint32_t a, uint32_t b)
                               (u16x2)(__builtin_bit_cast(u16x2, a) - __builtin_bit_cast(u16x2, b)));
 }
 
-// Writes the codes of the eight values at (row, col), col a multiple of 8;
-// the four lanes of a quad hold one group's four parts, all of them active,
-// and columns past d hold 0.  Scaling by a power of two is exact, so the
-// rounding sees x itself.
-__device__ __forceinline__ void keep8(const Act8 &a, int64_t row, int32_t col, const float (&v)[8])
+// Writes the codes of the eight values at (row, col), col a multiple of 8 and
+// `at` their chunk; the four lanes of a quad hold one group's four parts, all
+// of them active, and columns past d hold 0.  Scaling by a power of two is
+// exact, so the rounding sees x itself.
+__device__ __forceinline__ void keep8(const Act8 &a, int64_t row, int32_t col, int64_t at,
+                                      const float (&v)[8])
 {
     uint32_t m = 0;
 #pragma unroll
@@ -339,9 +346,9 @@ __device__ __forceinline__ void keep8(const Act8 &a, int64_t row, int32_t col, c
     }
     if (!finite)
         w = u32x2{0, 0};
-    *reinterpret_cast<u32x2 *>(a.codes + row * a.pitch + col) = w;
+    *reinterpret_cast<u32x2 *>(a.codes + 8 * at) = w;
     if ((col & 24) == 0)
-        a.exps[row * a.groups + (col >> 5)] = (uint8_t)e;
+        a.exps[at >> 2] = (uint8_t)e;
 }
 
 // 2^E of an exponent byte; NaN for 255.
@@ -350,16 +357,15 @@ __device__ __forceinline__ float step_of(uint32_t e)
     return bits_f32(e == 255u ? 0x7FC00000u : e << 23);
 }
 
-// The eight values at (row, col), col a multiple of 8 and below the pitch, as
-// loaded and as floats.
+// The eight values of a chunk, as loaded and as floats.
 struct RawAct8 {
     u32x2 w;
     uint32_t e;
 };
-__device__ __forceinline__ void load_act8(const Act8 &a, int64_t row, int32_t col, RawAct8 &r)
+__device__ __forceinline__ void load_act8(const Act8 &a, int64_t at, RawAct8 &r)
 {
-    r.w = *reinterpret_cast<const u32x2 *>(a.codes + row * a.pitch + col);
-    r.e = a.exps[row * a.groups + (col >> 5)];
+    r.w = *reinterpret_cast<const u32x2 *>(a.codes + 8 * at);
+    r.e = a.exps[at >> 2];
 }
 __device__ __forceinline__ void unpack_act8(const RawAct8 &r, float (&v)[8])
 {
@@ -368,10 +374,10 @@ __device__ __forceinline__ void unpack_act8(const RawAct8 &r, float (&v)[8])
     for (int k = 0; k < 8; ++k)
         v[k] = (float)((int)(r.w[k >> 2] << (24 - 8 * (k & 3))) >> 24) * step;
 }
-__device__ __forceinline__ void restore8(const Act8 &a, int64_t row, int32_t col, float (&v)[8])
+__device__ __forceinline__ void restore8(const Act8 &a, int64_t at, float (&v)[8])
 {
     RawAct8 r;
-    load_act8(a, row, col, r);
+    load_act8(a, at, r);
     unpack_act8(r, v);
 }
 

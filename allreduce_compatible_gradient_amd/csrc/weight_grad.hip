@@ -557,7 +557,7 @@ __global__ __launch_bounds__(256) void k_weight_grad_narrow(
     for (int64_t row = m_begin + t; row < m_end; row += 16) {
         float v[8];
         if (col < k)
-            restore8(x, row, col, v);
+            restore8(x, x.chunk(row, col), v);
         else
 #pragma unroll
             for (int b = 0; b < 8; ++b)
