@@ -673,7 +673,7 @@ int32_t check_sizes(int32_t dtype, int64_t rows, int64_t d)
 {
     if (!dtype_ok(dtype))
         return fail(GQ_ERR_ARG, "dtype %d is neither GQ_IN_F32 nor GQ_IN_BF16", dtype);
-    if (rows < 0 || rows >= ((int64_t)1 << 32) || d < 1 || d > 0x7FFFFFFF - 31)
+    if (rows < 0 || rows >= ((int64_t)1 << 32) || d < 1 || d >= kMaxColumns)
         return fail(GQ_ERR_ARG, "rows = %lld, d = %lld out of range", (long long)rows,
                     (long long)d);
     if (rows > 0 && groups_of(d) >= (kMaxGroups + rows - 1) / rows)
@@ -897,11 +897,11 @@ extern "C" {
 
 const char *gqt_last_error(void) { return g_err; }
 
-int64_t gqt_act8_groups(int64_t d) { return d < 1 || d > 0x7FFFFFFF - 31 ? -1 : groups_of(d); }
+int64_t gqt_act8_groups(int64_t d) { return d < 1 || d >= kMaxColumns ? -1 : groups_of(d); }
 
 int64_t gqt_act8_code_pitch(int64_t d)
 {
-    return d < 1 || d > 0x7FFFFFFF - 31 ? -1 : 32 * groups_of(d);
+    return d < 1 || d >= kMaxColumns ? -1 : 32 * groups_of(d);
 }
 
 int32_t gqt_act8_save(const void *x, int32_t dtype, int64_t rows, int64_t d, int64_t ldx,
@@ -981,7 +981,7 @@ int32_t gqt_layer_norm(const void *x, int32_t dtype, int64_t rows, int64_t d, in
 
 int64_t gqt_layer_norm_backward_workspace_bytes(int64_t rows, int64_t d)
 {
-    if (rows < 0 || rows >= ((int64_t)1 << 32) || d < 1 || d > 0x7FFFFFFF - 31)
+    if (rows < 0 || rows >= ((int64_t)1 << 32) || d < 1 || d >= kMaxColumns)
         return -1;
     return 8 * d * grad_blocks(rows, d);
 }

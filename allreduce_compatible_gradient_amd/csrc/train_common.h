@@ -33,7 +33,8 @@ __attribute__((visibility("hidden"))) int32_t check_act8(const char *name, const
             return try_status;             \
     } while (0)
 
-constexpr int64_t kMaxGroups = (int64_t)1 << 29; // rows ceil(d / 32): 8-column chunks fit 31 bits
+constexpr int64_t kMaxGroups = (int64_t)1 << 29;  // rows ceil(d / 32): 8-column chunks fit 31 bits
+constexpr int64_t kMaxColumns = (int64_t)1 << 27; // a launch over columns stays below 2^32 threads
 
 inline int64_t elem_bytes(int32_t dtype) { return dtype == GQ_IN_F32 ? 4 : 2; }
 inline bool dtype_ok(int32_t dtype) { return dtype == GQ_IN_F32 || dtype == GQ_IN_BF16; }

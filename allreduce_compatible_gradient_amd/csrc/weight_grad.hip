@@ -136,9 +136,21 @@ __device__ __forceinline__ Steps steps_of(const RawX &l, uint32_t up)
     return s;
 }
 
+// Frees `from` for the next loads.  (Two buffers in turn would save the copy,
+// but a loop of two steps has the compiler move the sums between registers.
+// In assembly, so that it stays where it is.)
+__device__ __forceinline__ void copy_codes(RawX &to, const RawX &from)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            asm("v_mov_b32 %0, %1" : "=v"(to.b[j][h]) : "v"(from.b[j][h]));
+}
+
 // Byte B of w as a signed number, in one instruction (the compiler takes
-// two); one wait state ahead of it, so that no forwarding hazard has to be
-// known for it.
+// two).  w comes from memory and all of the result is written, so no
+// forwarding hazard has to be known for it.
 template <int B>
 __device__ __forceinline__ float code_f32(uint32_t w)
 {
@@ -331,9 +343,6 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
         if constexpr (P == 1) {
             // x outside: its fragment b + 1 is decoded while fragment b meets
             // the eight of dy, which stay in registers.
-            // (Two buffers of x in turn would save the copy, but a loop of two
-            // steps has the compiler move the sums between registers.  The copy
-            // is in assembly so that it stays where it is.)
             Steps st = steps_of(rx0, up);
             u32x4 fx = x_fragment(rx0, st, 0);
             for (int s = 0; s < steps; ++s) {
@@ -343,11 +352,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
                 for (int b = 0; b < 8; ++b) {
                     if (b == 7) {
                         st = steps_of(rx1, up);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                asm("v_mov_b32 %0, %1" : "=v"(rx0.b[j][h]) : "v"(rx1.b[j][h]));
+                        copy_codes(rx0, rx1);
                     }
                     const u32x4 fx_next = x_fragment(rx0, st, (b + 1) % 8);
 #pragma unroll
@@ -381,11 +386,16 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
             for (int s = 0; s < steps; ++s) {
                 enter(s);
                 const Steps st = steps_of(rx1, up);
+                copy_codes(rx0, rx1);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    load_codes(rx1, j);
+                load_exps(rx1);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     u32x4 part_next[P];
                     dy_fragment(ry, (c + 1) % 8, part_next);
-                    fx_next[c] = x_fragment(rx1, st, c);
+                    fx_next[c] = x_fragment(rx0, st, c);
 #pragma unroll
                     for (int p = 0; p < P; ++p)
 #pragma unroll
@@ -400,10 +410,6 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
                         for (int j = 0; j < 8; ++j)
                             load_dy(ry, j, c / 4);
                 }
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    load_codes(rx1, j);
-                load_exps(rx1);
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
                     fx[c] = fx_next[c];
@@ -608,14 +614,15 @@ __global__ __launch_bounds__(256) void k_sum_parts(const float *__restrict__ dw_
     const float *const part = second ? db_part : dw_part;
     const int64_t size = second ? n : count;
     const int32_t terms = second ? db_parts : splits;
-    const int64_t i = (int64_t)(blockIdx.x - (second ? dw_blocks : 0)) * 256 + threadIdx.x;
-    if (i >= size)
-        return;
-    float s = 0.0f;
+    const int64_t first = blockIdx.x - (second ? dw_blocks : 0);
+    const int64_t blocks = second ? gridDim.x - dw_blocks : dw_blocks;
+    for (int64_t i = first * 256 + threadIdx.x; i < size; i += blocks * 256) {
+        float s = 0.0f;
 #pragma unroll 4
-    for (int z = 0; z < terms; ++z)
-        s += part[z * size + i];
-    (second ? db : dw)[i] = (O)s;
+        for (int z = 0; z < terms; ++z)
+            s += part[z * size + i];
+        (second ? db : dw)[i] = (O)s;
+    }
 }
 
 // How the work is cut: tiles, and how often the tokens are split.
@@ -644,7 +651,7 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, int32_t dtype)
         const int64_t tn = (n + side - 1) / side, tk = (k + side - 1) / side;
         const int64_t steps = (m + tokens - 1) / tokens;
         const double round_us = shared ? 8.0 : 17.0;
-        const double step_us = dtype == GQ_IN_F32 ? 2.8 : 1.0;
+        const double step_us = dtype == GQ_IN_F32 ? 2.4 : 1.0;
         if (n < 8 && !shared)
             continue;
         for (int64_t s = 1; s <= 256 && s <= steps; ++s) {
@@ -658,7 +665,7 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, int32_t dtype)
                 p.shared = shared;
                 p.splits = (int32_t)splits;
                 p.chunk = chunk * tokens;
-                // n k < 2^40: below 2^27 tiles, or few splits
+                // n k < 2^36: below 2^23 tiles, or few splits
                 p.tiles = {(int32_t)tn, (int32_t)tk, (int32_t)(tn * tk * splits)};
             }
         }
@@ -672,8 +679,8 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, int32_t dtype)
 
 bool sizes_ok(int64_t m, int64_t n, int64_t k)
 {
-    return m >= 0 && m < ((int64_t)1 << 32) && n >= 1 && n <= 0x7FFFFFFF - 255 && k >= 1 &&
-           k <= 0x7FFFFFFF - 255 && k < (((int64_t)1 << 40) + n - 1) / n;
+    return m >= 0 && m < ((int64_t)1 << 32) && n >= 1 && n < kMaxColumns && k >= 1 &&
+           k < kMaxColumns && n * k < ((int64_t)1 << 36);
 }
 
 template <typename T, typename O>
@@ -706,8 +713,9 @@ int32_t launch(const void *dy, int64_t m, int32_t n, int64_t lddy, const Act8 &x
         GQT_TRY(check_launch("k_weight_grad"));
     }
     const int64_t count = (int64_t)n * k;
-    const int64_t dw_blocks = p.dw_part || m == 0 ? (count + 255) / 256 : 0;
-    const int64_t db_blocks = db ? (n + 255) / 256 : 0;
+    const auto blocks = [](int64_t size) { return size < 1 << 30 ? (size + 255) / 256 : 1 << 22; };
+    const int64_t dw_blocks = p.dw_part || m == 0 ? blocks(count) : 0;
+    const int64_t db_blocks = db ? blocks(n) : 0;
     if (dw_blocks + db_blocks == 0)
         return ok();
     k_sum_parts<O><<<dim3((uint32_t)(dw_blocks + db_blocks)), 256, 0, st>>>(

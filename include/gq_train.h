@@ -30,7 +30,7 @@
  *     their element type only, codes 16 bytes.
  *   - dtype: GQ_IN_F32 or GQ_IN_BF16.  Arithmetic and sums are fp32; a
  *     bf16 output is rounded once, to nearest, ties to even.
- *   - Sizes: rows >= 0 and < 2^32, 1 <= d < 2^31, and rows ceil(d / 32)
+ *   - Sizes: rows >= 0 and < 2^32, 1 <= d < 2^27, and rows ceil(d / 32)
  *     < 2^29 (17 G values).  rows == 0 enqueues nothing (the sums over rows
  *     are zeros), and the matrices may then be NULL.
  *   - Memory: device pointers owned by the caller.  The library allocates
@@ -63,7 +63,7 @@ typedef struct gqt_act8 {
 } gqt_act8;
 
 /* G = ceil(d / 32) and 32 G, the bytes of a row's exps and codes; -1 for
- * d outside [1, 2^31).                                                     */
+ * d outside [1, 2^27).                                                     */
 int64_t gqt_act8_groups(int64_t d);
 int64_t gqt_act8_code_pitch(int64_t d);
 
@@ -112,8 +112,8 @@ int32_t gqt_gelu_backward(const void *dy, int32_t dtype, int64_t rows, int64_t d
  * dy[m][n] and the 8-bit copy x8 of x[m][k]:
  *   dw = dy^T x, db = sum over rows of dy (may be NULL), both in wdtype.
  * Every product is exact (an fp32 dy is taken as the sum of three bf16
- * parts) and the sums are fp32.  n and k lie in [1, 2^31), and
- * n k < 2^40.  With m == 0, dw and db are zeros.  dy: lddy >= n, or 0.     */
+ * parts) and the sums are fp32.  n and k lie in [1, 2^27), and
+ * n k < 2^36.  With m == 0, dw and db are zeros.  dy: lddy >= n, or 0.     */
 int64_t gqt_weight_grad_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t dtype);
 int32_t gqt_weight_grad(const void *dy, int32_t dtype, int64_t m, int64_t n, int64_t lddy,
                         const gqt_act8 *x8, int64_t k, void *dw, void *db, int32_t wdtype,

@@ -68,7 +68,7 @@ int main(void)
 def test_sizes():
     for d, g in ((1, 1), (32, 1), (33, 2), (4096, 128)):
         assert train.gqt_act8_groups(d) == g and train.gqt_act8_code_pitch(d) == 32 * g
-    for d in (0, -1, 1 << 31):
+    for d in (0, -1, 1 << 27, 1 << 31):
         assert train.gqt_act8_groups(d) == train.gqt_act8_code_pitch(d) == -1
     L = train.lib()
     ws = L.gqt_layer_norm_backward_workspace_bytes
