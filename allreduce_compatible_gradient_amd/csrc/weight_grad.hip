@@ -230,11 +230,12 @@ struct Tiles {
 // of the row, and so computes some rows that its neighbour stores.
 //
 // db: the tiles that share a tile's columns of dy take turns at adding up
-// its steps, so that none is slower than the others; each leaves a partial.
+// its steps, so that none is slower than the others, and each leaves a
+// partial; or (db_whole) the first of them adds up all.
 template <typename T, typename O, bool SHARED>
 __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
     const T *__restrict__ dy, int64_t m, int32_t n, int64_t lddy, Act8 x, int32_t k, int64_t chunk,
-    Tiles tiles, O *__restrict__ dw, float *__restrict__ db_part)
+    Tiles tiles, O *__restrict__ dw, float *__restrict__ db_part, O *__restrict__ db_whole)
 {
     constexpr int P = parts<T>(), kLoads = sizeof(T) / 2; // 16-byte loads of eight columns
     constexpr int kStepM = step_tokens(SHARED), kSide = SHARED ? 1 : 2;
@@ -307,7 +308,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
     // apart than a lane's offset reaches and tokens that do not fill a step
     // come last, one step at a time.
     const int steps = lddy < ((int64_t)1 << 24) ? (int)((m_end - m_begin) / kStepM) : 0;
-    int next_sum = db_part ? tk : -1; // the step whose tokens this tile adds up next
+    // the step whose tokens this tile adds up next, and the one after
+    int next_sum = db_part ? tk : db_whole && tk == 0 ? 0 : -1;
+    const int turn = db_part ? tiles.k * kSide : 1;
     RawDy<T> ry;
     RawX rx0, rx1;
     if (steps > 0) {
@@ -335,7 +338,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
         const auto enter = [&](int s) GQT_INLINE {
             if (s == next_sum) {
                 add_tokens(ry, sum);
-                next_sum += tiles.k * kSide;
+                next_sum += turn;
             }
             dy_p += s + 1 < steps ? dy_step : 0;
             advance_x(s + 2 < steps);
@@ -439,7 +442,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
                 if (e_col + p >= 0)
                     rx0.e |= (uint32_t)x.exps[row * x.groups + e_col + p] << (8 * p);
         }
-        if (db_part && tk == 0)
+        if ((db_part || db_whole) && tk == 0)
             add_tokens(ry, sum);
         u32x4 fx[8];
         decode(rx0, up, fx);
@@ -512,8 +515,13 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
                 put(e, c, v);
             }
     }
-    if (db_part) {
-        float *const db_out = db_part + ((int64_t)z * tiles.k * kSide + tk) * n;
+    if (db_part || (db_whole && tk == 0)) {
+        const auto put_db = [&](int row, float v) GQT_INLINE {
+            if (db_part)
+                db_part[((int64_t)z * tiles.k * kSide + tk) * n + row] = v;
+            else
+                db_whole[row] = (O)v;
+        };
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             sum[c] += __shfl_xor(sum[c], 16);
@@ -533,14 +541,14 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
                 for (int w = 0; w < kWaves; ++w)
                     v += lds[w * kTile + t];
                 if (row >= n0 + t / 8 * 8 && row < n)
-                    db_out[row] = v;
+                    put_db(row, v);
             }
         } else if (g == 0) {
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 const int row = dy_col + c;
                 if (row >= n0 + 8 * i && row < n)
-                    db_out[row] = sum[c];
+                    put_db(row, sum[c]);
             }
         }
     }
@@ -628,6 +636,7 @@ __global__ __launch_bounds__(256) void k_sum_parts(const float *__restrict__ dw_
 // How the work is cut: tiles, and how often the tokens are split.
 struct Plan {
     bool shared;
+    bool whole_db; // db comes from the tiles themselves
     Tiles tiles;
     int32_t splits;
     int64_t chunk;
@@ -670,7 +679,14 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, int32_t dtype)
             }
         }
     }
-    p.db_parts = n < 8 ? p.splits : p.splits * p.tiles.k * (p.shared ? 1 : 2);
+    // db straight from the tiles, where the first of a column does all its
+    // steps, against partials and a second launch, us (bf16, fp32): 4096 x
+    // 1024 over 128 tokens 11.1 and 12.9 against 14.0 and 15.5, over 1536 (12
+    // steps) 25.4 and 44.1 against 26.8 and 46.7; 4096 x 4096 over 384 (12
+    // steps of squares) 28.6 and 48.7 against 33.0 and 53.8.  What a step
+    // adds eats the launch's 3 us by about 20 steps.
+    p.whole_db = n >= 8 && p.splits == 1 && p.chunk <= 12 * step_tokens(p.shared);
+    p.db_parts = p.whole_db ? 0 : n < 8 ? p.splits : p.splits * p.tiles.k * (p.shared ? 1 : 2);
     p.dw_part = p.splits > 1 || n < 8 ? p.splits * n * k : 0;
     p.db_part = p.db_parts * n;
     p.bytes = 4 * (p.dw_part + p.db_part);
@@ -688,7 +704,8 @@ int32_t launch(const void *dy, int64_t m, int32_t n, int64_t lddy, const Act8 &x
                void *dw, void *db, float *ws, hipStream_t st)
 {
     const Plan p = plan_of(m, n, k, sizeof(T) == 4 ? GQ_IN_F32 : GQ_IN_BF16);
-    float *const db_part = db ? ws + p.dw_part : nullptr;
+    float *const db_part = db && !p.whole_db ? ws + p.dw_part : nullptr;
+    O *const db_whole = p.whole_db ? (O *)db : nullptr;
     const T *const dyt = (const T *)dy;
     if (m == 0) {
         // nothing to launch before the sums
@@ -699,23 +716,23 @@ int32_t launch(const void *dy, int64_t m, int32_t n, int64_t lddy, const Act8 &x
     } else {
         const dim3 grid(p.tiles.total);
         if (p.dw_part && p.shared)
-            k_weight_grad<T, float, true><<<grid, kThreads, 0, st>>>(dyt, m, n, lddy, x, k, p.chunk,
-                                                                     p.tiles, ws, db_part);
+            k_weight_grad<T, float, true><<<grid, kThreads, 0, st>>>(
+                dyt, m, n, lddy, x, k, p.chunk, p.tiles, ws, db_part, nullptr);
         else if (p.dw_part)
             k_weight_grad<T, float, false><<<grid, kThreads, 0, st>>>(
-                dyt, m, n, lddy, x, k, p.chunk, p.tiles, ws, db_part);
+                dyt, m, n, lddy, x, k, p.chunk, p.tiles, ws, db_part, nullptr);
         else if (p.shared)
-            k_weight_grad<T, O, true><<<grid, kThreads, 0, st>>>(dyt, m, n, lddy, x, k, p.chunk,
-                                                                 p.tiles, (O *)dw, db_part);
+            k_weight_grad<T, O, true><<<grid, kThreads, 0, st>>>(
+                dyt, m, n, lddy, x, k, p.chunk, p.tiles, (O *)dw, db_part, db_whole);
         else
-            k_weight_grad<T, O, false><<<grid, kThreads, 0, st>>>(dyt, m, n, lddy, x, k, p.chunk,
-                                                                  p.tiles, (O *)dw, db_part);
+            k_weight_grad<T, O, false><<<grid, kThreads, 0, st>>>(
+                dyt, m, n, lddy, x, k, p.chunk, p.tiles, (O *)dw, db_part, db_whole);
         GQT_TRY(check_launch("k_weight_grad"));
     }
     const int64_t count = (int64_t)n * k;
     const auto blocks = [](int64_t size) { return size < 1 << 30 ? (size + 255) / 256 : 1 << 22; };
     const int64_t dw_blocks = p.dw_part || m == 0 ? blocks(count) : 0;
-    const int64_t db_blocks = db ? blocks(n) : 0;
+    const int64_t db_blocks = db && !p.whole_db ? blocks(n) : 0;
     if (dw_blocks + db_blocks == 0)
         return ok();
     k_sum_parts<O><<<dim3((uint32_t)(dw_blocks + db_blocks)), 256, 0, st>>>(
