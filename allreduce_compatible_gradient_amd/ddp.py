@@ -118,10 +118,11 @@ class GlobalQSGDState:
         return _mix64(_mix64(self.seed ^ (bucket_index << 40)) ^ k)
 
 
-def global_qsgd_hook(state: GlobalQSGDState, bucket) -> torch.futures.Future:
+def global_qsgd_hook(state: GlobalQSGDState, bucket):
     """DDP communication hook (register with `ddp.register_comm_hook(state,
     global_qsgd_hook)`): the bucket's mean gradient over the ranks, through
-    Global-Q codes and an integer all-reduce."""
+    Global-Q codes and an integer all-reduce, as a torch.futures.Future (not
+    annotated: DDP compares annotations with types, and here they are strings)."""
     group = state.process_group if state.process_group is not None else dist.group.WORLD
     world = dist.get_world_size(group)
     rank = dist.get_rank(group)

@@ -1,0 +1,30 @@
+"""MLP blocks with 8-bit activations trained through the Global-QSGD hook:
+the hook as DDP takes it, and examples/train_mlp8.py on one rank."""
+import importlib.util
+import os
+
+import pytest
+
+torch = pytest.importorskip("torch")
+import torch.distributed as dist  # noqa: E402
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture
+def one_rank(request):
+    """A group of this process alone, over the backend that the test asks for."""
+    if request.param == "nccl" and not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    store = dist.TCPStore("127.0.0.1", 0, 1, is_master=True)
+    dist.init_process_group(request.param, store=store, rank=0, world_size=1)
+    yield
+    dist.destroy_process_group()
+
+
+@pytest.mark.parametrize("one_rank", ["gloo"], indirect=True)
+def test_ddp_takes_the_hook_itself(one_rank):
+    """DDP checks a hook's annotations when it is registered."""
+    from allreduce_compatible_gradient_amd.ddp import GlobalQSGDState, global_qsgd_hook
+    model = torch.nn.parallel.DistributedDataParallel(torch.nn.Linear(4, 4))
+    model.register_comm_hook(GlobalQSGDState(), global_qsgd_hook)
