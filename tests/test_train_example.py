@@ -28,3 +28,26 @@ def test_ddp_takes_the_hook_itself(one_rank):
     from allreduce_compatible_gradient_amd.ddp import GlobalQSGDState, global_qsgd_hook
     model = torch.nn.parallel.DistributedDataParallel(torch.nn.Linear(4, 4))
     model.register_comm_hook(GlobalQSGDState(), global_qsgd_hook)
+
+
+def _example():
+    path = os.path.join(ROOT, "examples", "train_mlp8.py")
+    spec = importlib.util.spec_from_file_location("train_mlp8", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("one_rank", ["nccl"], indirect=True)
+@pytest.mark.parametrize("more", [[], ["--nearest"]])
+def test_example_learns(one_rank, more):
+    """Blocks of odd sizes: every loss is finite and the last steps' are below
+    half of the first step's."""
+    torch.cuda.set_device(0)
+    example = _example()
+    losses = example.run(example.arguments(
+        ["--blocks", "2", "--d", "72", "--hidden", "200", "--tokens", "333", "--steps", "60",
+         "--lr", "3e-3"] + more))
+    assert len(losses) == 60 and all(x == x and x < float("inf") for x in losses)
+    assert sum(losses[-5:]) / 5 < 0.5 * losses[0], losses
