@@ -252,9 +252,13 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_layer_norm_backward(
     const void *__restrict__ w, int32_t wdtype, T *__restrict__ dx, float *__restrict__ partial)
 {
     constexpr int kRows = block_threads<TPR>() / TPR;
-    // With one chunk a thread the registers allow the next row's loads to run
-    // ahead; with more, other waves cover them.
-    constexpr bool kAhead = C == 1;
+    // The next row's loads run ahead where a CU holds one block, so that no
+    // other covers them (bf16 8192 x 8192: 80 us, without 104), and with one
+    // chunk a thread where a row's loads are few (bf16 16384 x 2048 from the
+    // copy: 41, without 43).  Two fp32 rows are enough in flight as they are
+    // (32768 x 2048: 151 us, ahead 161), and with more chunks the registers
+    // cost what the loads gain (bf16 87381 x 768 from the copy: 74, ahead 86).
+    constexpr bool kAhead = TPR > 256 || (C == 1 && (sizeof(T) == 2 || ACT8));
     __shared__ float lds[TPR > 64 ? TPR / 64 : 1];
     __shared__ float sums[kRows > 1 ? kRows * TPR * C * 8 : 1];
     const int t = threadIdx.x % TPR, slot = row_slot<TPR>();

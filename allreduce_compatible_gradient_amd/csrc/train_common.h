@@ -40,14 +40,12 @@ inline int64_t elem_bytes(int32_t dtype) { return dtype == GQ_IN_F32 ? 4 : 2; }
 inline bool dtype_ok(int32_t dtype) { return dtype == GQ_IN_F32 || dtype == GQ_IN_BF16; }
 inline bool aligned_to(const void *p, int64_t a) { return ((uintptr_t)p & (uintptr_t)(a - 1)) == 0; }
 inline int64_t groups_of(int64_t d) { return (d + 31) / 32; }
-inline int64_t align256(int64_t b) { return (b + 255) & ~(int64_t)255; }
 
 // ---------------------------------------------------------------------------
 // Device
 
 using bf16 = __bf16;
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
