@@ -583,6 +583,19 @@ __device__ __forceinline__ float scaled_tail(float z)
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhC = 0.79788456080286536f; // sqrt(2 / pi)
 constexpr float kTanhA = 0.044715f;
+constexpr float kLog2E = 1.4426950408889634f;
+
+// 4^x for x <= 0, by squaring 2^x: the part's exponential flushes results
+// below 2^-126, its square does not.  An exponential whose argument is
+// carried in two floats would gain nothing here, where the argument itself
+// was rounded before.
+__device__ __forceinline__ float exp4(float x)
+{
+    const float half = __builtin_amdgcn_exp2f(x);
+    return half * half;
+}
+// e^(-h^2 / 2)
+__device__ __forceinline__ float bell(float h) { return exp4(-0.25f * kLog2E * h * h); }
 
 // The tanh form's logistic function s = s(2 u) and its complement 1 - s, both
 // from e^-|2u|, so that neither is the difference of near numbers.
@@ -591,8 +604,9 @@ struct Gate {
 };
 __device__ __forceinline__ Gate tanh_gate(float h)
 {
-    const float u = kTanhC * h * fmaf(kTanhA * h, h, 1.0f);
-    const float e = expf(-2.0f * fabsf(u));
+    // u log2(e)
+    const float w = h * fmaf(kLog2E * kTanhC * kTanhA * h, h, kLog2E * kTanhC);
+    const float e = exp4(-fabsf(w));
     const float big = __builtin_amdgcn_rcpf(1.0f + e);
     const float small = e * big;
     return h < 0.0f ? Gate{small, big} : Gate{big, small};
@@ -603,7 +617,7 @@ __device__ __forceinline__ float gelu(float h)
 {
     if (FORM == GQT_GELU_TANH)
         return h * tanh_gate(h).s;
-    const float tail = scaled_tail(fabsf(h)) * expf(-0.5f * h * h);
+    const float tail = scaled_tail(fabsf(h)) * bell(h);
     return h * (h < 0.0f ? tail : 1.0f - tail);
 }
 
@@ -618,7 +632,7 @@ __device__ __forceinline__ float gelu_slope(float h)
         const float u = kTanhC * fmaf(3.0f * kTanhA * c, c, 1.0f);
         return fmaf(2.0f * c * u, g.s * g.c, g.s);
     }
-    const float e = expf(-0.5f * h * h);
+    const float e = bell(h);
     const float tail = scaled_tail(fabsf(h)) * e;
     return fmaf(h * kInvSqrt2Pi, e, h < 0.0f ? tail : 1.0f - tail);
 }
