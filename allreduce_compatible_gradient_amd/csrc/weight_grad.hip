@@ -24,6 +24,8 @@ constexpr int kThreads = 64 * kWaves;
 #define GQT_INLINE __attribute__((always_inline))
 
 typedef uint32_t u32_e1 __attribute__((aligned(1)));
+typedef u32x2 u32x2_e2 __attribute__((aligned(2)));
+typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 template <typename T>
 constexpr int parts() { return sizeof(T) == 4 ? 3 : 1; }
@@ -608,8 +610,28 @@ __global__ __launch_bounds__(256) void k_weight_grad_narrow(
     }
 }
 
-// Adds partials in order: `splits` of count values for dw (unless it is
-// whole already), and `parts` of n for db, whose blocks come after dw's.
+__device__ __forceinline__ void store4(float *p, int64_t left, const f32x4 &v)
+{
+    if (left >= 4)
+        *reinterpret_cast<u32x4_e4 *>(p) = __builtin_bit_cast(u32x4, v);
+    else
+        for (int j = 0; j < left; ++j)
+            p[j] = v[j];
+}
+__device__ __forceinline__ void store4(bf16 *p, int64_t left, const f32x4 &v)
+{
+    const bf16x4 h = {(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
+    if (left >= 4)
+        *reinterpret_cast<u32x2_e2 *>(p) = __builtin_bit_cast(u32x2, h);
+    else
+        for (int j = 0; j < left; ++j)
+            p[j] = h[j];
+}
+
+// Adds partials in a fixed order: `splits` of count values for dw (unless it
+// is whole already), and `db_parts` of n for db, whose blocks come after
+// dw's.  256 values a block, four a lane, and a quarter of the partials a
+// wave, so that a long chain of few values has loads enough in flight.
 template <typename O>
 __global__ __launch_bounds__(256) void k_sum_parts(const float *__restrict__ dw_part,
                                                    int32_t splits, int64_t count,
@@ -618,18 +640,41 @@ __global__ __launch_bounds__(256) void k_sum_parts(const float *__restrict__ dw_
                                                    int32_t db_parts, int32_t n,
                                                    O *__restrict__ db)
 {
+    __shared__ f32x4 sums[3][64];
     const bool second = blockIdx.x >= dw_blocks;
     const float *const part = second ? db_part : dw_part;
+    O *const out = second ? db : dw;
     const int64_t size = second ? n : count;
     const int32_t terms = second ? db_parts : splits;
     const int64_t first = blockIdx.x - (second ? dw_blocks : 0);
     const int64_t blocks = second ? gridDim.x - dw_blocks : dw_blocks;
-    for (int64_t i = first * 256 + threadIdx.x; i < size; i += blocks * 256) {
-        float s = 0.0f;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int32_t from = (int32_t)((int64_t)terms * wave / 4);
+    const int32_t to = (int32_t)((int64_t)terms * (wave + 1) / 4);
+    for (int64_t base = first * 256; base < size; base += blocks * 256) {
+        const int64_t i = base + 4 * lane, left = size - i;
+        f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+        const float *p = part + from * size + i;
+        if (left >= 4) {
 #pragma unroll 4
-        for (int z = 0; z < terms; ++z)
-            s += part[z * size + i];
-        (second ? db : dw)[i] = (O)s;
+            for (int32_t z = from; z < to; ++z, p += size)
+                s += __builtin_bit_cast(f32x4, *reinterpret_cast<const u32x4_e4 *>(p));
+        } else if (left > 0) {
+            // the values there are, the last one repeated: a loop over them
+            // inside that over the partials would wait for every load
+            const int32_t j1 = left > 1 ? 1 : 0, j2 = left > 2 ? 2 : j1;
+#pragma unroll 4
+            for (int32_t z = from; z < to; ++z, p += size)
+                s += f32x4{p[0], p[j1], p[j2], 0.0f};
+        }
+        __syncthreads(); // the last turn's sums are read
+        if (wave)
+            sums[wave - 1][lane] = s;
+        __syncthreads();
+        if (wave == 0) {
+            s = ((s + sums[0][lane]) + sums[1][lane]) + sums[2][lane];
+            store4(out + i, left, s);
+        }
     }
 }
 
