@@ -1,5 +1,8 @@
 // train.hip -- layer norm, GELU and the 8-bit activation copies on MI355X
-// (gfx950): the operators of include/gq_train.h that are bound by memory.
+// (gfx950): the operators of include/gq_train.h that stream their matrices.
+// Times in the comments are of the kernel alone unless they say "call"; for
+// comparison a copy of 0.25 to 1 GiB runs at 5.0 to 5.4 TB/s here, and small
+// matrices stay in the cache, where more is possible.
 //
 // Every kernel reads its inputs once and writes its outputs once, eight
 // columns (one 16-byte bf16 load) per lane and step, so that four lanes hold
@@ -46,8 +49,15 @@ namespace {
 // at column 8 (c TPR + t)), so the row is read once and its mean and the sum
 // of squared deviations from it (no cancellation, whatever the mean) are
 // taken in registers.  Rows beyond 16384 columns are
-// read three times by k_layer_norm_long, from the cache after the first.  The
-// shape goes by d alone, so that keeping a copy does not change y.
+// read three times by k_layer_norm_long, from the cache after the first: bf16
+// 4096 x 16384 takes 62 us a call in registers and 94 so, 8192 x 8192 49 and
+// 127.  The shape goes by d alone, so that keeping a copy does not change y.
+//
+// Forward: mean = sum x / d, rstd = 1 / sqrt(sum (x - mean)^2 / d + eps), y =
+// (x - mean) rstd w + b.  Bound by memory: 16384 x 4096 bf16 50 us (5.3 TB/s
+// of one read and one write), 131072 x 64 9.6 us.  With a copy of x at random
+// rounding, whose Philox calls and conversions are most of its instructions,
+// 8191 x 2048 bf16 takes 28 us (3.0 TB/s; VALU 55 % of the issue slots).
 
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float *lds)
@@ -242,9 +252,12 @@ __global__ __launch_bounds__(kLongThreads) void k_layer_norm_long(
     }
 }
 
-// One row's dx from its dy (g = dy w) and xh, given the two row means.
-// The gradient kernels accumulate dw and db per thread over the rows of a
-// block in a fixed order; partial[block][2][d] is reduced by k_sum_partials.
+// Backward: with g = dy w and xh = (x - mean) rstd, dx = rstd (g - mean of g
+// over the row - xh times that of g xh); dw and db are the sums over rows of
+// dy xh and dy.  Each thread adds up its columns over its block's rows in a
+// fixed order; partial[block][2][d] is reduced by k_sum_partials.  Bound by
+// memory: 16384 x 4096 bf16 79 us (5.1 TB/s of dy, x and dx, before 25 MB of
+// partials); 8191 x 2048 bf16 from the copy 22.5 us (3.8 TB/s).
 template <typename T, int TPR, int C, bool ACT8>
 __global__ __launch_bounds__(block_threads<TPR>()) void k_layer_norm_backward(
     const T *__restrict__ dy, int64_t rows, int32_t d, int64_t lddy, const T *__restrict__ x,
@@ -371,7 +384,9 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_layer_norm_backward(
     }
 }
 
-// Rows too long for registers: dx alone, from two readings of the row.
+// Rows of more than 8192 columns, too long for registers: dx alone, from two
+// readings of the row (8192 x 8192: 103 us a call in registers, 161 with this
+// and the column sums below; fp32 155 and 301).
 template <typename T, bool ACT8>
 __global__ __launch_bounds__(kLongThreads) void k_layer_norm_backward_long(
     const T *__restrict__ dy, int64_t rows, int32_t d, int64_t lddy, const T *__restrict__ x,
@@ -420,8 +435,9 @@ __global__ __launch_bounds__(kLongThreads) void k_layer_norm_backward_long(
 }
 
 // and their partial sums for dw and db, 2048 columns a block along x, the rows
-// dealt out along y (adding them up in memory row by row took 265 us at 5461 x
-// 12288, a second reading of dy and x half of that).
+// dealt out along y: a second reading of dy and x (one kernel for both that
+// added them up in memory row by row took 265 us a call at 5461 x 12288, the
+// two take 160).
 template <typename T, bool ACT8>
 __global__ __launch_bounds__(256) void k_norm_column_sums(
     const T *__restrict__ dy, int64_t rows, int32_t d, int64_t lddy, const T *__restrict__ x,
@@ -453,9 +469,10 @@ __global__ __launch_bounds__(256) void k_norm_column_sums(
 }
 
 // dw and db: the blocks' partial sums added in block order, a sixteenth of
-// the blocks a wave, eight loads in flight (one at a time, the chain of
-// loads took 62 us for 1024 blocks whatever d).  64 columns a block along x,
-// dw / db along y.
+// the blocks a wave, eight loads in flight (one at a time in one wave, the
+// chain of loads took 62 us for 1024 blocks whatever d; now 5.5 us for 768 of
+// d = 4096, 3.9 us for 1024 of d = 64).  64 columns a block along x, dw / db
+// along y.
 constexpr int kSumWaves = 16;
 __global__ __launch_bounds__(64 * kSumWaves) void k_sum_partials(
     const float *__restrict__ partial, int32_t blocks, int32_t d, void *__restrict__ dw,
@@ -531,6 +548,8 @@ __device__ __forceinline__ Chunk chunk_at(uint32_t i, const FastDiv &per_row)
 
 constexpr int kThreads = 256;
 
+// A copy of a matrix: bound by memory, 16384 x 4096 bf16 39 us (5.2 TB/s of
+// 2 + 33/32 bytes a value, VALU in 46 % of the issue slots with random rounding).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_act8_save(const T *__restrict__ x, uint32_t chunks,
                                                         FastDiv per_row, int32_t d, int64_t ldx,
@@ -545,6 +564,8 @@ __global__ __launch_bounds__(kThreads) void k_act8_save(const T *__restrict__ x,
     keep8(out, c.row, c.col, i, v);
 }
 
+// The values again, exact in T: bound by memory, 16384 x 4096 to bf16 31 us
+// (6.6 TB/s, much of it within the cache).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_act8_restore(Act8 in, uint32_t chunks,
                                                            FastDiv per_row, int32_t d,
@@ -637,6 +658,11 @@ __device__ __forceinline__ float gelu_slope(float h)
     return fmaf(h * kInvSqrt2Pi, e, h < 0.0f ? tail : 1.0f - tail);
 }
 
+// GELU y = h Phi(h), or in the tanh form h s(2 u), and its gradient dy y'(h)
+// with y' = Phi + h phi or s + 2 h s (1 - s) u'.  With an exponential good to
+// the last bit both kernels were bound by VALU issue (0.98 instructions a CU
+// and clock, 79 us for the step of 8192 x 4096 bf16 in the tanh form with a
+// random copy of h); now the step takes 64 us, 5.3 TB/s of its 338 MB.
 template <typename T, int FORM, bool KEEP>
 __global__ __launch_bounds__(kThreads) void k_gelu(const T *__restrict__ h, uint32_t chunks,
                                                    FastDiv per_row, int32_t d, int64_t ldh,
@@ -793,8 +819,9 @@ int64_t norm_blocks(int64_t rows, int64_t d)
 constexpr int64_t kMostGradColumns = 8192; // beyond, dw and db have a kernel of their own
 
 // Blocks that leave 2 d partial sums each.  As many as their registers let a
-// CU hold at once: a part of a round more costs a round (16384 x 4096 takes
-// 131 us with 3 blocks a CU, 146 with 4).
+// CU hold at once: a part of a round more costs a round (bf16 calls: 16384 x
+// 4096 83 us with 3 blocks a CU, 98 with 4; 10922 x 6144 84 with 2, 93 with
+// 4; 65536 x 1024 80 with 3, 89 with 4).
 int64_t grad_blocks(int64_t rows, int64_t d)
 {
     const int64_t all = (rows + rows_per_block(d) - 1) / rows_per_block(d);

@@ -11,6 +11,14 @@
 // the permutes that narrow the decoded codes to bf16 (x).  A code times its
 // group's power of two is exact in bf16; an fp32 dy is the exact sum of three
 // bf16 parts and takes three MFMAs.  All sums are fp32.
+//
+// What bounds it is the work around the MFMAs: a wave spends as long decoding
+// codes, pairing tokens and waiting as multiplying.  8192 x 4096 x 1024 bf16
+// (tokens, rows and columns of dw) takes 75 us a call, 920 TFLOP/s, with the
+// matrix cores busy about 40 % of the time; the library's product of bf16 operands,
+// x restored before, takes 91 us.  fp32 8192 x 2048 x 2048: 184 us, 373
+// TFLOP/s counting one product a value, three times that in MFMAs (library
+// 457 us).
 #include "train_common.h"
 
 namespace gqt {
@@ -223,8 +231,10 @@ struct Tiles {
 // block have one tile, each takes 32 of a step's 128 tokens, and their sums
 // are added at the end; or they have the four tiles of a 256 x 256 square and
 // the same 32 tokens, which asks half as much of the L2 and ends without a
-// word between them, but leaves fewer blocks.  out: dw itself (one split of
-// the tokens) or the split's fp32 partial.
+// word between them, but leaves fewer blocks.  Which, plan_of estimates; us a
+// call for bf16, shared against squares: 8192 x 4096 x 4096 294, 262; 512 x
+// 4096 x 4096 49, 37; 8192 x 4096 x 1024 76, 93; 1000 x 1001 x 777 18, 28.
+// out: dw itself (one split of the tokens) or the split's fp32 partial.
 //
 // Rows of the tile past n, and columns past the codes' pitch, are not
 // stored, so what they hold is free: every lane loads eight columns that
@@ -556,9 +566,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
     }
 }
 
-// n < 8: too few rows of dw for a tile.  A block's 16 lanes take 128 columns
-// of x, its 16 rows of threads every 16th token, and one product a value is
-// an ordinary fused multiply-add.  out and db_part as above, db by block 0.
+// n < 8: too few rows of dw for a tile, whose lanes load eight columns of dy
+// that exist.  A block's 16 lanes take 128 columns of x, its 16 rows of
+// threads every 16th token, and one product a value is an ordinary fused
+// multiply-add.  Bound by the decoding of x: 16384 x 4 x 1024 27 us a call.
+// db comes from block 0.
 template <typename T>
 __global__ __launch_bounds__(256) void k_weight_grad_narrow(
     const T *__restrict__ dy, int64_t m, int32_t n, int64_t lddy, Act8 x, int32_t k, int64_t chunk,
@@ -631,7 +643,11 @@ __device__ __forceinline__ void store4(bf16 *p, int64_t left, const f32x4 &v)
 // Adds partials in a fixed order: `splits` of count values for dw (unless it
 // is whole already), and `db_parts` of n for db, whose blocks come after
 // dw's.  256 values a block, four a lane, and a quarter of the partials a
-// wave, so that a long chain of few values has loads enough in flight.
+// wave, so that a long chain of few values has loads enough in flight (us a
+// call, against a value a lane and all partials a wave: 100000 x 8 x 32 18 and
+// 25, 16384 x 16 x 4096 32 and 43; at odd sizes up to 0.9 more, fp32 1000 x
+// 1001 x 777 26.3 and 25.4).  Bound by its launch or by reading the partials:
+// 4 of 1024 x 1024 in 7 us.
 template <typename O>
 __global__ __launch_bounds__(256) void k_sum_parts(const float *__restrict__ dw_part,
                                                    int32_t splits, int64_t count,
@@ -692,8 +708,8 @@ struct Plan {
 // The cut with the least estimated time.  A CU holds one block, so blocks
 // run in rounds of 256; a round takes a fixed time and that of its steps, and
 // partials are written and read again at 4 TB/s with 3 us for their launch
-// (all measured).  Without the rounds in the estimate, 4096 x 1056 (288
-// tiles) took two rounds of all tokens, 276 us where 4096 x 1024 took 146.
+// (all measured).  8192 x 4096 x 1056 (288 tiles, so two rounds of whole
+// tokens) takes 105 us cut so; 8192 x 4096 x 1024 (256 tiles) takes 75.
 Plan plan_of(int64_t m, int64_t n, int64_t k, int32_t dtype)
 {
     Plan p{};
