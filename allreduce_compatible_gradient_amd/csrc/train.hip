@@ -662,7 +662,7 @@ __device__ __forceinline__ float gelu_slope(float h)
 // with y' = Phi + h phi or s + 2 h s (1 - s) u'.  With an exponential good to
 // the last bit both kernels were bound by VALU issue (0.98 instructions a CU
 // and clock, 79 us for the step of 8192 x 4096 bf16 in the tanh form with a
-// random copy of h); now the step takes 64 us, 5.3 TB/s of its 338 MB.
+// random copy of h); now the step takes 62 us, 5.4 TB/s of its 338 MB, at 0.81 and 0.70.
 template <typename T, int FORM, bool KEEP>
 __global__ __launch_bounds__(kThreads) void k_gelu(const T *__restrict__ h, uint32_t chunks,
                                                    FastDiv per_row, int32_t d, int64_t ldh,
@@ -773,7 +773,9 @@ constexpr int kCUs = 256;
 
 // Layer norm shapes: threads per row (whole waves from 64 on) and chunks a
 // thread, so that few lanes are idle (at half of them d = 256 and 5120 ran at
-// 3.4 and 2.7 TB/s) and the gradient's sums do not spill.
+// 3.4 and 2.7 TB/s), the gradient's sums do not spill, and registers leave
+// room for waves (bf16 8191 x 2048 forward with a random copy: 25 us a call
+// with 256 threads a row, 34 with one wave and four chunks).
 #define GQT_BY_ROW_LENGTH(LAUNCH, LONG) \
     do {                                \
         if (d <= 32)                    \

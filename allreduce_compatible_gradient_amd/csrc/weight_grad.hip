@@ -14,8 +14,8 @@
 //
 // What bounds it is the work around the MFMAs: a wave spends as long decoding
 // codes, pairing tokens and waiting as multiplying.  8192 x 4096 x 1024 bf16
-// (tokens, rows and columns of dw) takes 75 us a call, 920 TFLOP/s, with the
-// matrix cores busy about 40 % of the time; the library's product of bf16 operands,
+// (tokens, rows and columns of dw) takes 73 us a call, 950 TFLOP/s, with the
+// matrix cores busy 36 % of the time (profiled); the library's product of bf16 operands,
 // x restored before, takes 91 us.  fp32 8192 x 2048 x 2048: 184 us, 373
 // TFLOP/s counting one product a value, three times that in MFMAs (library
 // 457 us).
@@ -647,7 +647,7 @@ __device__ __forceinline__ void store4(bf16 *p, int64_t left, const f32x4 &v)
 // call, against a value a lane and all partials a wave: 100000 x 8 x 32 18 and
 // 25, 16384 x 16 x 4096 32 and 43; at odd sizes up to 0.9 more, fp32 1000 x
 // 1001 x 777 26.3 and 25.4).  Bound by its launch or by reading the partials:
-// 4 of 1024 x 1024 in 7 us.
+// 4 of 1024 x 1024 in 6 us.
 template <typename O>
 __global__ __launch_bounds__(256) void k_sum_parts(const float *__restrict__ dw_part,
                                                    int32_t splits, int64_t count,
@@ -709,7 +709,7 @@ struct Plan {
 // run in rounds of 256; a round takes a fixed time and that of its steps, and
 // partials are written and read again at 4 TB/s with 3 us for their launch
 // (all measured).  8192 x 4096 x 1056 (288 tiles, so two rounds of whole
-// tokens) takes 105 us cut so; 8192 x 4096 x 1024 (256 tiles) takes 75.
+// tokens) takes 105 us cut so; 8192 x 4096 x 1024 (256 tiles) takes 73.
 Plan plan_of(int64_t m, int64_t n, int64_t k, int32_t dtype)
 {
     Plan p{};
