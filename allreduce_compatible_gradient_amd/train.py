@@ -603,7 +603,8 @@ class Mlp8(torch.nn.Module):
 
     random=True rounds them at random without bias, with a stream of its own
     for every copy of every forward pass (seeded by `seed`, the number of the
-    pass, and the four copies in it); otherwise to nearest."""
+    pass, and the four copies in it); otherwise to nearest.  The seeds are
+    the host's: a captured graph draws the same numbers at every replay."""
 
     def __init__(self, d: int, hidden: int, *, eps: float = 1e-5, approximate: str = "tanh",
                  random: bool = True, seed: int = 0, device=None, dtype=torch.bfloat16):
