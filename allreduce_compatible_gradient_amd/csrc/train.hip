@@ -50,7 +50,7 @@ namespace {
 // of squared deviations from it (no cancellation, whatever the mean) are
 // taken in registers.  Rows beyond 16384 columns are
 // read three times by k_layer_norm_long, from the cache after the first: bf16
-// 4096 x 16384 takes 62 us a call in registers and 94 so, 8192 x 8192 49 and
+// 4096 x 16384 takes 48 us a call in registers and 94 so, 8192 x 8192 49 and
 // 127.  The shape goes by d alone, so that keeping a copy does not change y.
 //
 // Forward: mean = sum x / d, rstd = 1 / sqrt(sum (x - mean)^2 / d + eps), y =
@@ -808,14 +808,34 @@ int64_t rows_per_block(int64_t d)
     return d <= 32 ? 64 : d <= 64 ? 32 : d <= 128 ? 16 : d <= 256 ? 8 : d <= 1536 ? 4 : 1;
 }
 
-// Blocks of a layer norm launch: four turns each with the weights in
-// registers where that leaves 8 blocks a CU, so that late blocks even out.
-int64_t norm_blocks(int64_t rows, int64_t d)
+// Chunks of eight columns that a thread holds, in the shapes above.
+int chunks_per_thread(int64_t d)
+{
+    if (d > 6144)
+        return d <= 8192 ? 2 : 4;
+    if (d > 4096 || (d > 1024 && d <= 1536))
+        return 3;
+    return d > 2048 || (d > 512 && d <= 1024) ? 2 : 1;
+}
+
+// Blocks of a layer norm launch.  Up to 8 turns each, as many as the
+// registers let a CU hold at once, as a part of a round more costs a round:
+// us a call for bf16 with a copy, against four turns and at least 8 a CU, 8192
+// x 1024 14.5 and 17.2, 16384 x 1536 38.0 and 42.1, 4096 x 4096 25.3 and 27.2.
+// Beyond, four turns with the weights in registers, so that late blocks even
+// out: forward and backward of 16384 x 4096 131 us, with all that a CU holds
+// 138; fp32 65536 x 2048 with a copy 226 and 244.
+int64_t norm_blocks(int64_t rows, int64_t d, bool keep)
 {
     const int64_t all = (rows + rows_per_block(d) - 1) / rows_per_block(d);
-    const int64_t least = 8 * kCUs;
-    const int64_t want = all / 4 > least ? all / 4 : least;
-    return all < want ? all : want;
+    const int c = chunks_per_thread(d);
+    int64_t held = 8 * kCUs;
+    if (d <= 16384)
+        held = kCUs * (d > 6144 ? 2 : keep ? (c == 1 ? 5 : c == 2 ? 3 : 2)
+                                           : (c == 1 ? 8 : c == 2 ? 5 : 4));
+    if (all <= held)
+        return all;
+    return all <= 8 * held ? held : (all + 3) / 4;
 }
 
 constexpr int64_t kMostGradColumns = 8192; // beyond, dw and db have a kernel of their own
@@ -832,12 +852,8 @@ int64_t grad_blocks(int64_t rows, int64_t d)
         most = (4 * kCUs * 2048 + d - 1) / d;
     else if (d > 6144)
         most = kCUs;
-    else if ((d > 1024 && d <= 1536) || d > 4096) // three chunks
-        most = 2 * kCUs;
-    else if ((d > 512 && d <= 1024) || d > 2048) // two
-        most = 3 * kCUs;
     else
-        most = 4 * kCUs;
+        most = kCUs * (5 - chunks_per_thread(d));
     return all < most ? all : most;
 }
 
@@ -847,10 +863,10 @@ int32_t launch_norm(const void *x, int64_t rows, int32_t d, int64_t ldx, const v
                     const gqt_act8 *sx, const gqt_act8 *sy, hipStream_t st)
 {
     const Act8 kx = act8_view(sx, d), ky = act8_view(sy, d);
-    const dim3 grid((uint32_t)norm_blocks(rows, d));
     const T *xt = (const T *)x;
     T *yt = (T *)y;
     const bool keep = sx || sy;
+    const dim3 grid((uint32_t)norm_blocks(rows, d, keep));
 #define GQT_KERNEL(TPR, C, KEEP)                                                                 \
     k_layer_norm<T, TPR, C, KEEP><<<grid, block_threads<TPR>(), 0, st>>>(                \
         xt, rows, d, ldx, w, b, wdtype, eps, yt, mean, rstd, kx, ky)
