@@ -57,7 +57,7 @@ namespace {
 // (x - mean) rstd w + b.  Bound by memory: 16384 x 4096 bf16 50 us (5.3 TB/s
 // of one read and one write), 131072 x 64 9.6 us.  With a copy of x at random
 // rounding, whose Philox calls and conversions are most of its instructions,
-// 8191 x 2048 bf16 takes 28 us (3.0 TB/s; VALU 55 % of the issue slots).
+// 8191 x 2048 bf16 takes 26 us (3.2 TB/s; VALU 54 % of the issue slots).
 
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float *lds)
@@ -662,7 +662,7 @@ __device__ __forceinline__ float gelu_slope(float h)
 // with y' = Phi + h phi or s + 2 h s (1 - s) u'.  With an exponential good to
 // the last bit both kernels were bound by VALU issue (0.98 instructions a CU
 // and clock, 79 us for the step of 8192 x 4096 bf16 in the tanh form with a
-// random copy of h); now the step takes 62 us, 5.4 TB/s of its 338 MB, at 0.81 and 0.70.
+// random copy of h); now the step takes 64 us, 5.3 TB/s of its 338 MB, at 0.81 and 0.70.
 template <typename T, int FORM, bool KEEP>
 __global__ __launch_bounds__(kThreads) void k_gelu(const T *__restrict__ h, uint32_t chunks,
                                                    FastDiv per_row, int32_t d, int64_t ldh,

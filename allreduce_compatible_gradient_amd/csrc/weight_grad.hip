@@ -14,7 +14,7 @@
 //
 // What bounds it is the work around the MFMAs: a wave spends as long decoding
 // codes, pairing tokens and waiting as multiplying.  8192 x 4096 x 1024 bf16
-// (tokens, rows and columns of dw) takes 73 us a call, 950 TFLOP/s, with the
+// (tokens, rows and columns of dw) takes 76 us a call, 910 TFLOP/s, with the
 // matrix cores busy 36 % of the time (profiled); the library's product of bf16 operands,
 // x restored before, takes 91 us.  fp32 8192 x 2048 x 2048: 184 us, 373
 // TFLOP/s counting one product a value, three times that in MFMAs (library
@@ -709,7 +709,7 @@ struct Plan {
 // run in rounds of 256; a round takes a fixed time and that of its steps, and
 // partials are written and read again at 4 TB/s with 3 us for their launch
 // (all measured).  8192 x 4096 x 1056 (288 tiles, so two rounds of whole
-// tokens) takes 105 us cut so; 8192 x 4096 x 1024 (256 tiles) takes 73.
+// tokens) takes 105 us cut so; 8192 x 4096 x 1024 (256 tiles) takes 76.
 Plan plan_of(int64_t m, int64_t n, int64_t k, int32_t dtype)
 {
     Plan p{};
