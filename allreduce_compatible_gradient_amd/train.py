@@ -22,6 +22,7 @@ Two layers:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -524,30 +525,78 @@ def gelu(h, approximate: str = "none", *, bits=None, seed=None):
     return _Gelu.apply(h, approximate, _bits(bits), seed)
 
 
+def _product_dtype(x):
+    """What autocast casts a product's operands to; None outside autocast."""
+    if not torch.is_autocast_enabled(x.device.type):
+        return None
+    dtype = torch.get_autocast_dtype(x.device.type)
+    _dtype(dtype, "the dtype of autocast")
+    return dtype
+
+
+def _no_autocast(t):
+    """Autocast off where it is on.  Inside a Function it would cast the
+    weights without a graph and keep the casts, so that a later product with
+    the same weights would have no gradient for them; and in a backward pass
+    it would round what the forward pass did not."""
+    kind = t.device.type
+    if torch.is_autocast_enabled(kind):
+        return torch.autocast(kind, enabled=False)
+    return contextlib.nullcontext()
+
+
+def _cast(t, dtype):
+    return t if t is None or dtype is None else t.to(dtype)
+
+
+def _dtypes_of(weight, bias):
+    """Those of a product's parameters, which their gradients have too."""
+    _dtype(weight.dtype, "weight")
+    if bias is None:
+        return weight.dtype, weight.dtype
+    _dtype(bias.dtype, "bias")
+    return weight.dtype, bias.dtype
+
+
+def _parameter_grads(dy, x, dtypes, bias):
+    """(dw, db) in their parameters' dtypes, of which autocast takes two: both
+    are computed in the wider."""
+    dw, db = gqt_weight_grad(dy, x, dtype=torch.promote_types(*dtypes), bias=bias)
+    return dw.to(dtypes[0]), None if db is None else db.to(dtypes[1])
+
+
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, seed):
-        x2 = _rows(x, x.shape[-1])
-        kept = gqt_act8_save(x2, seed=seed)
-        ctx.d = x2.shape[1]
-        ctx.save_for_backward(weight, kept.codes, kept.exps)
-        return torch.nn.functional.linear(x, weight, bias)
+        dtype = _product_dtype(x)
+        ctx.x_dtype, ctx.dtypes = x.dtype, _dtypes_of(weight, bias)
+        with _no_autocast(x):
+            x, weight, bias = _cast(x, dtype), _cast(weight, dtype), _cast(bias, dtype)
+            x2 = _rows(x, x.shape[-1])
+            kept = gqt_act8_save(x2, seed=seed)
+            ctx.d = x2.shape[1]
+            ctx.save_for_backward(weight, kept.codes, kept.exps)
+            return torch.nn.functional.linear(x, weight, bias)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         weight, codes, exps = ctx.saved_tensors
-        dx = dy @ weight if ctx.needs_input_grad[0] else None
-        dw = db = None
-        if ctx.needs_input_grad[1] or ctx.needs_input_grad[2]:
-            dw, db = gqt_weight_grad(_rows(dy, dy.shape[-1]), Act8(codes, exps, ctx.d),
-                                     dtype=weight.dtype, bias=ctx.needs_input_grad[2])
+        dx = dw = db = None
+        with _no_autocast(dy):
+            if ctx.needs_input_grad[0]:
+                dx = (dy @ weight).to(ctx.x_dtype)
+            if ctx.needs_input_grad[1] or ctx.needs_input_grad[2]:
+                dw, db = _parameter_grads(_rows(dy, dy.shape[-1]), Act8(codes, exps, ctx.d),
+                                          ctx.dtypes, ctx.needs_input_grad[2])
         return dx, dw, db, None
 
 
 def linear(x, weight, bias=None, *, seed=None):
     """x w^T + bias (the library's product), differentiable, with x kept for
-    the weight's gradient in 8 bits."""
+    the weight's gradient in 8 bits.  Under autocast the product and the copy
+    are those of the cast x, and the gradients have the dtypes of x, weight
+    and bias; autocast has to be to bf16."""
     return _Linear.apply(x, weight, bias, seed)
 
 
@@ -558,18 +607,26 @@ class _Mlp8(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, nw, nb, w1, b1, w2, b2, eps, approximate, seed):
+        dtype = _product_dtype(x)
         x2 = _rows(x, x.shape[-1])
         rows, d = x2.shape
         ff = w1.shape[0]
         seeds = [None] * 4 if seed is None else [_mix_seed(seed, k) for k in range(4)]
         x8, a8 = _new_copy(x2), _new_copy(x2)
         h8, g8 = Act8.empty(rows, ff, x.device), Act8.empty(rows, ff, x.device)
-        a, mean, rstd = gqt_layer_norm(x2, nw, nb, eps, save_x=x8, seed_x=seeds[0], save_y=a8,
-                                       seed_y=seeds[1])
-        h = torch.nn.functional.linear(a, w1, b1)
-        g = gqt_gelu(h, approximate, save_h=h8, seed_h=seeds[2], save_y=g8, seed_y=seeds[3])
-        y = torch.nn.functional.linear(g, w2, b2)
-        ctx.d, ctx.ff, ctx.approximate = d, ff, approximate
+        ctx.d, ctx.ff, ctx.approximate, ctx.x_dtype = d, ff, approximate, x.dtype
+        ctx.dtypes1, ctx.dtypes2 = _dtypes_of(w1, b1), _dtypes_of(w2, b2)
+        with _no_autocast(x):
+            w1, b1, w2, b2 = (_cast(t, dtype) for t in (w1, b1, w2, b2))
+            cast = dtype is not None and dtype != x.dtype
+            a, mean, rstd = gqt_layer_norm(x2, nw, nb, eps, save_x=x8, seed_x=seeds[0],
+                                           save_y=None if cast else a8, seed_y=seeds[1])
+            if cast:  # the copy is of what the product reads
+                a = a.to(dtype)
+                gqt_act8_save(a, seed=seeds[1], out=a8)
+            h = torch.nn.functional.linear(a, w1, b1)
+            g = gqt_gelu(h, approximate, save_h=h8, seed_h=seeds[2], save_y=g8, seed_y=seeds[3])
+            y = torch.nn.functional.linear(g, w2, b2)
         ctx.save_for_backward(mean, rstd, nw, w1, w2, x8.codes, x8.exps, a8.codes, a8.exps,
                               h8.codes, h8.exps, g8.codes, g8.exps)
         return y.view(*x.shape[:-1], w2.shape[0])
@@ -583,16 +640,18 @@ class _Mlp8(torch.autograd.Function):
         need = ctx.needs_input_grad
         dy2 = _rows(dy, dy.shape[-1])
         dx = dnw = dnb = dw1 = db1 = dw2 = db2 = None
-        if need[5] or need[6]:
-            dw2, db2 = gqt_weight_grad(dy2, g8, dtype=w2.dtype, bias=need[6])
-        if any(need[:5]):
-            dh = gqt_gelu_backward(dy2 @ w2, h8, ctx.approximate)
-            if need[3] or need[4]:
-                dw1, db1 = gqt_weight_grad(dh, a8, dtype=w1.dtype, bias=need[4])
-            if any(need[:3]):
-                dx, dnw, dnb = gqt_layer_norm_backward(dh @ w1, x8, mean, rstd, nw,
-                                                       weight_grad=need[1], bias_grad=need[2])
-                dx = dx.view(*dy.shape[:-1], d)
+        with _no_autocast(dy):
+            if need[5] or need[6]:
+                dw2, db2 = _parameter_grads(dy2, g8, ctx.dtypes2, need[6])
+            if any(need[:5]):
+                dh = gqt_gelu_backward(dy2 @ w2, h8, ctx.approximate)
+                if need[3] or need[4]:
+                    dw1, db1 = _parameter_grads(dh, a8, ctx.dtypes1, need[4])
+                if any(need[:3]):
+                    dx, dnw, dnb = gqt_layer_norm_backward(
+                        (dh @ w1).to(ctx.x_dtype), x8, mean, rstd, nw, weight_grad=need[1],
+                        bias_grad=need[2])
+                    dx = dx.view(*dy.shape[:-1], d)
         return dx, dnw, dnb, dw1, db1, dw2, db2, None, None, None
 
 

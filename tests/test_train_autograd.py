@@ -1,0 +1,159 @@
+"""The training operators under autograd and as modules: autocast, what is
+kept, and what a module calls.  On the CPU with the stand-ins of
+tests/train_standins.py in the operators' place, on the GPU as they are."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import train_plain as plain  # noqa: E402
+import train_standins  # noqa: E402
+from allreduce_compatible_gradient_amd import train  # noqa: E402
+
+F = torch.nn.functional
+
+
+@pytest.fixture(params=["cpu", pytest.param("cuda", marks=pytest.mark.gpu)])
+def device(request, monkeypatch):
+    if request.param == "cpu":
+        train_standins.install(monkeypatch)
+    elif not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return request.param
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def leaf(device, *shape, seed, dtype=torch.float32):
+    x = np.random.default_rng(seed).standard_normal(shape)
+    return torch.from_numpy(x).to(device).to(dtype).requires_grad_()
+
+
+def copy_of(t, seed):
+    """The values that the 8-bit copy of t stands for."""
+    return plain.restore(*plain.save(host(t), seed), t.shape[1])
+
+
+def product_bound(a, b):
+    """|error| of the bf16 product a b summed in fp32: a rounding a term and
+    that of the result."""
+    terms = np.abs(a) @ np.abs(b)
+    return terms * (a.shape[1] + 8) * 2 * plain.U + np.abs(a @ b) * plain.HALF["bf16"] * 1.01
+
+
+def autocast(device, dtype=torch.bfloat16):
+    return torch.autocast(device, dtype)
+
+
+# ---------------------------------------------------------------------------
+# autocast
+
+@pytest.mark.parametrize("backward", ["outside", "inside"])
+@pytest.mark.parametrize("x_dtype", [torch.float32, torch.bfloat16])
+def test_linear_under_autocast(device, x_dtype, backward):
+    """The library's product under autocast, with the gradients in the
+    leaves' own types: dw and db summed in fp32, from the copy of the operand."""
+    x = leaf(device, 12, 40, seed=1, dtype=x_dtype)
+    w, b = leaf(device, 24, 40, seed=2), leaf(device, 24, seed=3)
+    g = leaf(device, 12, 24, seed=4, dtype=torch.bfloat16).detach()
+    with autocast(device):
+        y = train.linear(x, w, b, seed=5)
+        assert y.dtype == torch.bfloat16 and torch.equal(y, F.linear(x, w, b))
+        if backward == "inside":
+            y.backward(g)
+    if backward == "outside":
+        y.backward(g)
+    assert x.grad.dtype == x_dtype and w.grad.dtype == b.grad.dtype == torch.float32
+    gn, kept = host(g), copy_of(x.detach().bfloat16(), 5)
+    for got, want, bound in zip((w.grad, b.grad), plain.weight_grad(gn, kept),
+                                plain.weight_grad_bounds(gn, kept, "f32")):
+        assert (np.abs(host(got) - want) <= bound).all()
+    wn = host(w.bfloat16())
+    assert (np.abs(host(x.grad) - gn @ wn) <= product_bound(gn, wn)).all()
+
+
+def test_a_bias_keeps_its_gradients_precision_under_autocast(device):
+    """A bf16 weight beside an fp32 bias: db is not rounded to bf16 on the way."""
+    x = leaf(device, 12, 40, seed=1)
+    w, b = leaf(device, 24, 40, seed=2, dtype=torch.bfloat16), leaf(device, 24, seed=3)
+    g = leaf(device, 12, 24, seed=4, dtype=torch.bfloat16).detach()
+    with autocast(device):
+        y = train.linear(x, w, b)
+    y.backward(g)
+    assert w.grad.dtype == torch.bfloat16 and b.grad.dtype == torch.float32
+    want, bound = host(g).sum(axis=0), np.abs(host(g)).sum(axis=0) * 20 * 2 * plain.U
+    assert (np.abs(host(b.grad) - want) <= bound).all()
+
+
+def test_linear_leaves_autocasts_cache_alone(device):
+    """A later product with the same weight has its gradient."""
+    x, w = leaf(device, 6, 40, seed=1), leaf(device, 24, 40, seed=2)
+    with autocast(device):
+        train.linear(x, w)
+        F.linear(x, w).float().sum().backward()
+    assert w.grad is not None and host(w.grad).any()
+
+
+def test_mlp8_leaves_autocasts_cache_alone(device):
+    block = train.Mlp8(32, 64, seed=1, device=device, dtype=torch.float32)
+    x = leaf(device, 6, 32, seed=1)
+    with autocast(device):
+        block(x)
+        block.down(F.gelu(block.up(x))).float().sum().backward()
+    for p in (block.up.weight, block.up.bias, block.down.weight, block.down.bias):
+        assert p.grad is not None
+
+
+def test_backward_inside_autocast_of_a_forward_outside(device):
+    """An fp32 forward pass has fp32 gradients wherever backward is called."""
+    grads = []
+    for enabled in (False, True):
+        x, w = leaf(device, 6, 40, seed=1), leaf(device, 24, 40, seed=2)
+        y = train.linear(x, w, seed=3)
+        with torch.autocast(device, torch.bfloat16, enabled=enabled):
+            y.backward(torch.ones_like(y))
+        grads.append((x.grad, w.grad))
+    assert all(torch.equal(a, b) for a, b in zip(*grads))
+
+
+def test_autocast_to_another_type_is_refused(device):
+    """fp16 has no operators here: said before anything is computed."""
+    x, w = leaf(device, 6, 32, seed=1), leaf(device, 24, 32, seed=2)
+    block = train.Mlp8(32, 64, seed=1, device=device, dtype=torch.float32)
+    with autocast(device, torch.float16):
+        for call in (lambda: train.linear(x, w), lambda: block(x)):
+            with pytest.raises(TypeError, match="autocast"):
+                call()
+
+
+@pytest.mark.parametrize("x_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("random", [False, True])
+def test_mlp8_under_autocast(device, x_dtype, random):
+    """fp32 parameters under autocast: the ordinary block's output and, up to
+    the copies' rounding (3 %, as without autocast) and a bf16 rounding of each
+    of the five results on the way (2^-8 each), its gradients."""
+    torch.manual_seed(0)
+    block = train.Mlp8(96, 200, random=random, seed=3, device=device, dtype=torch.float32)
+    x = leaf(device, 5, 8, 96, seed=1, dtype=x_dtype)
+    dy = leaf(device, 5, 8, 96, seed=2).detach()
+    with autocast(device):
+        y = block(x)
+    y.backward(dy.to(y.dtype))
+    got = [x.grad] + [p.grad for p in block.parameters()]
+    assert [g.dtype for g in got] == [x_dtype] + [torch.float32] * 6
+    block.zero_grad()
+    xr = x.detach().requires_grad_()
+    with autocast(device):
+        a = F.layer_norm(xr, (96,), block.norm.weight, block.norm.bias, 1e-5)
+        ref = xr + block.down(F.gelu(block.up(a), approximate="tanh"))
+    assert y.dtype == ref.dtype
+    # y - x passes five roundings to bf16, two of sums over 96 and 200 terms
+    # of its size: 8 half steps of the largest value, and the last addition's
+    scale = float((ref - xr).detach().abs().max() + ref.detach().abs().max())
+    assert float((y - ref).detach().abs().max()) < 8 * 2.0**-8 * scale
+    ref.backward(dy.to(ref.dtype))
+    want = [xr.grad] + [p.grad for p in block.parameters()]
+    for g, e in zip(got, want):
+        assert float((g - e).float().norm() / e.float().norm()) < 0.03 + 5 * 2.0**-8
