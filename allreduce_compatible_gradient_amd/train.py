@@ -171,11 +171,10 @@ class _Elsewhere:
     def __exit__(self, *exc):
         self.ctx.__exit__(*exc)
         for t in self.tensors:
-            if isinstance(t, Act8):
-                t.codes.record_stream(self.stream)
-                t.exps.record_stream(self.stream)
-            elif isinstance(t, torch.Tensor):
-                t.record_stream(self.stream)
+            for part in (t.codes, t.exps) if isinstance(t, Act8) else (t,):
+                # a host tensor, refused inside, has no stream to be kept for
+                if isinstance(part, torch.Tensor) and part.is_cuda:
+                    part.record_stream(self.stream)
 
 
 def _elsewhere(device, stream) -> bool:
