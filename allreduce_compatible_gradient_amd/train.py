@@ -161,6 +161,8 @@ class _Elsewhere:
         elif not hasattr(stream, "cuda_stream"):
             stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
                       else torch.cuda.default_stream(device))
+        elif stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
         self.stream, self.tensors = stream, tensors
 
     def __enter__(self):

@@ -38,3 +38,11 @@ def test_refusals_on_another_stream():
                      lambda: train.gqt_weight_grad(x, host8, stream=stream)):
             with pytest.raises(ValueError):
                 call()
+
+
+def test_a_stream_of_another_device_is_refused():
+    """It would switch the device, and the work would then run on that of the
+    tensors, on a stream that the caller did not name."""
+    with pytest.raises(ValueError, match="stream"):
+        train._Elsewhere(torch.device("cuda", 0), Stream(1), ())
+    assert train._Elsewhere(torch.device("cuda", 1), Stream(1), ()).stream.cuda_stream == 1
