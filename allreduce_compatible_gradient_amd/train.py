@@ -451,6 +451,11 @@ def _mix_seed(seed: int, k: int) -> int:
     return _mix64(_mix64(seed & 0xFFFFFFFFFFFFFFFF) ^ k)
 
 
+def _copy_seeds(seed):
+    """Those of an MLP block's four copies in a pass."""
+    return [None] * 4 if seed is None else [_mix_seed(seed, k) for k in range(4)]
+
+
 def _rows(t: torch.Tensor, d: int) -> torch.Tensor:
     """t as [rows, d] with unit column stride (a copy where its strides do
     not allow it, such as a gradient expanded from a scalar)."""
@@ -612,7 +617,7 @@ class _Mlp8(torch.autograd.Function):
         x2 = _rows(x, x.shape[-1])
         rows, d = x2.shape
         ff = w1.shape[0]
-        seeds = [None] * 4 if seed is None else [_mix_seed(seed, k) for k in range(4)]
+        seeds = _copy_seeds(seed)
         x8, a8 = _new_copy(x2), _new_copy(x2)
         h8, g8 = Act8.empty(rows, ff, x.device), Act8.empty(rows, ff, x.device)
         ctx.d, ctx.ff, ctx.approximate, ctx.x_dtype = d, ff, approximate, x.dtype
@@ -656,6 +661,15 @@ class _Mlp8(torch.autograd.Function):
         return dx, dnw, dnb, dw1, db1, dw2, db2, None, None, None
 
 
+def _is_plain(module, kind) -> bool:
+    """Whether calling the module does what a `kind` does and no more: no
+    other class (an adapter, a parametrization), forward or hook."""
+    return (type(module) is kind and "forward" not in module.__dict__
+            and not (module._forward_hooks or module._forward_pre_hooks
+                     or module._backward_hooks or module._backward_pre_hooks
+                     or torch.nn.modules.module._has_any_global_hook()))
+
+
 class Mlp8(torch.nn.Module):
     """A transformer's MLP block, x + down(gelu(up(norm(x)))), that keeps
     its activations for the backward pass in 8 bits: x, norm(x), up(...) and
@@ -664,7 +678,11 @@ class Mlp8(torch.nn.Module):
     random=True rounds them at random without bias, with a stream of its own
     for every copy of every forward pass (seeded by `seed`, the number of the
     pass, and the four copies in it); otherwise to nearest.  The seeds are
-    the host's: a captured graph draws the same numbers at every replay."""
+    the host's: a captured graph draws the same numbers at every replay.
+
+    norm, up and down run together as one operator.  One that was replaced or
+    has hooks is called as it is instead, and keeps what it keeps; the others
+    keep the same copies as before."""
 
     def __init__(self, d: int, hidden: int, *, eps: float = 1e-5, approximate: str = "tanh",
                  random: bool = True, seed: int = 0, device=None, dtype=torch.bfloat16):
@@ -677,11 +695,22 @@ class Mlp8(torch.nn.Module):
         self.approximate, self.random, self.seed, self.passes = approximate, random, seed, 0
 
     def forward(self, x):
-        if not torch.is_grad_enabled():
-            a = layer_norm(x, self.norm.weight, self.norm.bias, self.norm.eps)
-            return x + self.down(gelu(self.up(a), self.approximate))
-        seed = _mix_seed(self.seed, self.passes) if self.random else None
-        self.passes += 1
-        return x + _Mlp8.apply(x, self.norm.weight, self.norm.bias, self.up.weight, self.up.bias,
-                               self.down.weight, self.down.bias, self.norm.eps, self.approximate,
-                               seed)
+        norm, up, down = self.norm, self.up, self.down
+        own_norm = _is_plain(norm, torch.nn.LayerNorm)
+        own_up, own_down = _is_plain(up, torch.nn.Linear), _is_plain(down, torch.nn.Linear)
+        seed, bits = None, None
+        if torch.is_grad_enabled():
+            bits = 8
+            if self.random:
+                seed = _mix_seed(self.seed, self.passes)
+            self.passes += 1
+            if own_norm and own_up and own_down:
+                return x + _Mlp8.apply(x, norm.weight, norm.bias, up.weight, up.bias, down.weight,
+                                       down.bias, norm.eps, self.approximate, seed)
+        seeds = _copy_seeds(seed)
+        a = (layer_norm(x, norm.weight, norm.bias, norm.eps, bits=bits, seed=seeds[0]) if own_norm
+             else norm(x))
+        h = linear(a, up.weight, up.bias, seed=seeds[1]) if bits and own_up else up(a)
+        g = gelu(h, self.approximate, bits=bits, seed=seeds[2])
+        return x + (linear(g, down.weight, down.bias, seed=seeds[3]) if bits and own_down
+                    else down(g))

@@ -157,3 +157,101 @@ def test_mlp8_under_autocast(device, x_dtype, random):
     want = [xr.grad] + [p.grad for p in block.parameters()]
     for g, e in zip(got, want):
         assert float((g - e).float().norm() / e.float().norm()) < 0.03 + 5 * 2.0**-8
+
+
+# ---------------------------------------------------------------------------
+# what Mlp8 calls
+
+class Adapter(torch.nn.Module):
+    """A linear layer with a low-rank addition, as fine-tuning puts in its place."""
+
+    def __init__(self, base):
+        super().__init__()
+        n, k = base.weight.shape
+        kw = {"device": base.weight.device, "dtype": base.weight.dtype}
+        self.base, self.weight, self.bias = base, base.weight, base.bias
+        self.a = torch.nn.Parameter(torch.randn(2, k, **kw))
+        self.b = torch.nn.Parameter(torch.randn(n, 2, **kw))
+
+    def forward(self, x):
+        return self.base(x) + x @ self.a.t() @ self.b.t()
+
+
+def mlp8(device, **kw):
+    torch.manual_seed(0)
+    return train.Mlp8(64, 96, device=device, dtype=torch.float32, **{"seed": 3, **kw})
+
+
+@pytest.mark.parametrize("which", ["norm", "up", "down"])
+def test_mlp8_calls_the_hooks_of_its_parts(device, which):
+    """With and without gradients, and what a hook returns counts."""
+    block, x = mlp8(device), leaf(device, 6, 64, seed=1)
+    plain_y = block(x)
+    part, seen = getattr(block, which), []
+    handles = [part.register_forward_pre_hook(lambda m, a: seen.append("pre")),
+               part.register_forward_hook(lambda m, a, y: seen.append("post") or 2 * y)]
+    y = block(x)
+    assert seen == ["pre", "post"]
+    with torch.no_grad():
+        z = block(x)
+    assert seen == ["pre", "post"] * 2
+    # fp32, other products: rounded differently
+    assert torch.allclose(y, z, rtol=1e-4, atol=1e-4) and not torch.allclose(y, plain_y, atol=1e-2)
+    for h in handles:
+        h.remove()
+    grads = []
+    part.register_full_backward_hook(lambda m, gi, go: grads.append(go[0].shape))
+    block(x).sum().backward()
+    assert len(grads) == 1 and x.grad is not None
+
+
+@pytest.mark.parametrize("which", ["up", "down"])
+def test_mlp8_calls_a_part_put_in_another_ones_place(device, which):
+    block, x = mlp8(device, random=False), leaf(device, 6, 64, seed=1)
+    adapter = Adapter(getattr(block, which))
+    setattr(block, which, adapter)
+    y = block(x)
+    with torch.no_grad():
+        z = block(x)
+    assert torch.allclose(y, z, rtol=1e-4, atol=1e-4)
+    y.sum().backward()
+    for p in block.parameters():
+        assert p.grad is not None and host(p.grad).any()
+
+
+def test_mlp8_takes_parametrized_parts_and_replaced_forwards(device):
+    block, x = mlp8(device), leaf(device, 6, 64, seed=1)
+
+    class Twice(torch.nn.Module):
+        def forward(self, w):
+            return 2 * w
+
+    torch.nn.utils.parametrize.register_parametrization(block.up, "weight", Twice())
+    old = block.down.forward
+    block.down.forward = lambda v: 3 * old(v)
+    y = block(x)
+    with torch.no_grad():
+        z = block(x)
+    assert torch.allclose(y, z, rtol=1e-4, atol=1e-4)
+    y.sum().backward()
+    original = block.up.parametrizations.weight.original
+    assert original.grad is not None and host(original.grad).any()
+
+
+def test_mlp8_in_parts_is_the_fused_block(device):
+    """A hook that changes nothing changes nothing: the parts that are not
+    called keep the same 8-bit copies, of the same streams."""
+    x, results = leaf(device, 6, 64, seed=1), []
+    for which in (None, "norm", "up", "down"):
+        block = mlp8(device)
+        if which:
+            getattr(block, which).register_forward_hook(lambda m, a, y: None)
+        y = block(x)
+        x.grad = None
+        y.sum().backward()
+        results.append([y, x.grad, *(p.grad for p in block.parameters())])
+    for other in results[1:]:
+        assert torch.allclose(results[0][0], other[0], rtol=1e-4, atol=1e-4)
+        for g, e in zip(other[1:], results[0][1:]):
+            # a copy that is not taken leaves out its rounding: 3 % as above
+            assert float((g - e).norm() / e.norm()) < 0.03
