@@ -24,6 +24,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import itertools
 import os
 
 import torch
@@ -670,22 +671,38 @@ def _is_plain(module, kind) -> bool:
                      or torch.nn.modules.module._has_any_global_hook()))
 
 
+_modules = itertools.count()  # numbers the blocks whose seed was not given
+
+
+def _rank() -> int:
+    dist = torch.distributed
+    return dist.get_rank() if dist.is_available() and dist.is_initialized() else 0
+
+
 class Mlp8(torch.nn.Module):
     """A transformer's MLP block, x + down(gelu(up(norm(x)))), that keeps
     its activations for the backward pass in 8 bits: x, norm(x), up(...) and
     gelu(...) take 33 bytes per 32 values, where bf16 copies take 64.
 
     random=True rounds them at random without bias, with a stream of its own
-    for every copy of every forward pass (seeded by `seed`, the number of the
-    pass, and the four copies in it); otherwise to nearest.  The seeds are
-    the host's: a captured graph draws the same numbers at every replay.
+    for every copy of every forward pass (seeded by the block's seed, the
+    number of the pass, and the four copies in it); otherwise to nearest.
+    Without `seed` each block has its own, from torch's seed and the order of
+    the blocks' first passes, and each rank of the default process group draws
+    other numbers, so that rounding errors are independent; a copy of a block
+    that has run shares its streams.  A `seed` is taken as it is: give each
+    block, and each rank, another.  The number of passes (and a seed that was
+    not given) is in the state dict, so that a resumed run goes on with new
+    numbers.  The seeds are the host's: a captured graph draws the same
+    numbers at every replay.
 
     norm, up and down run together as one operator.  One that was replaced or
     has hooks is called as it is instead, and keeps what it keeps; the others
     keep the same copies as before."""
 
     def __init__(self, d: int, hidden: int, *, eps: float = 1e-5, approximate: str = "tanh",
-                 random: bool = True, seed: int = 0, device=None, dtype=torch.bfloat16):
+                 random: bool = True, seed: int | None = None, device=None,
+                 dtype=torch.bfloat16):
         super().__init__()
         _form(approximate)
         kw = {"device": device, "dtype": dtype}
@@ -693,6 +710,34 @@ class Mlp8(torch.nn.Module):
         self.up = torch.nn.Linear(d, hidden, **kw)
         self.down = torch.nn.Linear(hidden, d, **kw)
         self.approximate, self.random, self.seed, self.passes = approximate, random, seed, 0
+        self._drawn = None  # the seed of a block that was given none
+
+    def _pass_seed(self) -> int:
+        if self.seed is not None:
+            return _mix_seed(self.seed, self.passes)
+        return _mix_seed(_mix_seed(self._draw(), _rank()), self.passes)
+
+    def _draw(self) -> int:
+        # not when the block is made: copies of one block would share it
+        if self._drawn is None:
+            self._drawn = _mix_seed(torch.initial_seed(), next(_modules))
+        return self._drawn
+
+    def get_extra_state(self) -> torch.Tensor:
+        """The number of passes; whether the block drew its seed; that seed."""
+        drew = self.random and self.seed is None
+        drawn = self._draw() if drew else 0
+        return torch.tensor([self.passes, drew, drawn - (drawn >> 63 << 64)], device="cpu")
+
+    def set_extra_state(self, state: torch.Tensor):
+        self.passes, drew, drawn = (int(v) for v in state.tolist())
+        if drew:
+            self._drawn = drawn & 0xFFFFFFFFFFFFFFFF
+
+    def _load_from_state_dict(self, state_dict, prefix, *args):
+        # a state without them leaves them as they are
+        state_dict.setdefault(prefix + "_extra_state", self.get_extra_state())
+        super()._load_from_state_dict(state_dict, prefix, *args)
 
     def forward(self, x):
         norm, up, down = self.norm, self.up, self.down
@@ -702,7 +747,7 @@ class Mlp8(torch.nn.Module):
         if torch.is_grad_enabled():
             bits = 8
             if self.random:
-                seed = _mix_seed(self.seed, self.passes)
+                seed = self._pass_seed()
             self.passes += 1
             if own_norm and own_up and own_down:
                 return x + _Mlp8.apply(x, norm.weight, norm.bias, up.weight, up.bias, down.weight,

@@ -1,6 +1,8 @@
 """The training operators under autograd and as modules: autocast, what is
 kept, and what a module calls.  On the CPU with the stand-ins of
 tests/train_standins.py in the operators' place, on the GPU as they are."""
+import itertools
+
 import numpy as np
 import pytest
 
@@ -255,3 +257,112 @@ def test_mlp8_in_parts_is_the_fused_block(device):
         for g, e in zip(other[1:], results[0][1:]):
             # a copy that is not taken leaves out its rounding: 3 % as above
             assert float((g - e).norm() / e.norm()) < 0.03
+
+
+# ---------------------------------------------------------------------------
+# the streams of random numbers
+
+def keys_of(block, x, monkeypatch):
+    """The Philox keys that a pass of the block draws its copies' numbers from."""
+    keys, forward = [], train.gqt_layer_norm
+    with monkeypatch.context() as m:
+        m.setattr(train, "_mix_seed", lambda s, k, mix=train._mix_seed:
+                  keys.append(mix(s, k)) or keys[-1])
+        block(x)
+    assert train.gqt_layer_norm is forward
+    return keys[-4:]
+
+
+def default_block(device):
+    return train.Mlp8(32, 64, device=device, dtype=torch.float32)
+
+
+def test_blocks_draw_from_streams_of_their_own(device, monkeypatch):
+    """Blocks made with the defaults, also as copies of one, and their passes."""
+    import copy
+    x = leaf(device, 2, 32, seed=1).detach()
+    first = default_block(device)
+    blocks = [first, default_block(device), copy.deepcopy(first)]
+    keys = [k for _ in range(3) for b in blocks for k in keys_of(b, x, monkeypatch)]
+    assert len(keys) == len(set(keys)) == 36
+
+
+def test_ranks_draw_from_streams_of_their_own(device, monkeypatch):
+    """The same block on another rank of a process group; a seed that the
+    caller gave is taken as it is."""
+    import copy
+    x = leaf(device, 2, 32, seed=1).detach()
+    blocks = {"default": default_block(device),
+              "given": train.Mlp8(32, 64, seed=5, device=device, dtype=torch.float32)}
+    blocks["default"].get_extra_state()
+    keys = {name: [] for name in blocks}
+    for rank in range(3):
+        with monkeypatch.context() as m:
+            m.setattr(torch.distributed, "is_initialized", lambda: True)
+            m.setattr(torch.distributed, "get_rank", lambda: rank)
+            for name, block in blocks.items():
+                keys[name] += keys_of(copy.deepcopy(block), x, monkeypatch)
+    assert len(set(keys["default"])) == 12 and len(set(keys["given"])) == 4
+
+
+def test_the_defaults_follow_torchs_seed(device, monkeypatch):
+    """Without taking a number from its generator: what is drawn after stays."""
+    x, runs = leaf(device, 2, 32, seed=1).detach(), []
+    for seed in (7, 8, 7):
+        monkeypatch.setattr(train, "_modules", itertools.count())
+        torch.manual_seed(seed)
+        block = default_block(device)
+        keys = keys_of(block, x, monkeypatch)
+        runs.append((keys, float(torch.rand(()))))
+    assert runs[0] == runs[2] and runs[0][0] != runs[1][0]
+    torch.manual_seed(7)
+    given = train.Mlp8(32, 64, seed=1, device=device, dtype=torch.float32)
+    given(x)
+    assert float(torch.rand(())) == runs[0][1]
+
+
+@pytest.mark.parametrize("seed", [None, 11])
+def test_a_resumed_block_goes_on_with_its_numbers(device, seed, monkeypatch, tmp_path):
+    x = leaf(device, 2, 32, seed=1).detach()
+
+    def make():
+        return torch.nn.Sequential(train.Mlp8(32, 64, seed=seed, device=device,
+                                              dtype=torch.float32))
+    model = make()
+    for _ in range(3):
+        model(x)
+    torch.save(model.state_dict(), tmp_path / "state.pt")
+    want = keys_of(model[0], x, monkeypatch)
+    resumed = make()
+    resumed(x)
+    resumed.load_state_dict(torch.load(tmp_path / "state.pt", weights_only=True))
+    assert resumed[0].passes == 3
+    assert keys_of(resumed[0], x, monkeypatch) == want
+
+
+def test_a_state_before_the_first_pass_fixes_the_streams(device, monkeypatch):
+    x = leaf(device, 2, 32, seed=1).detach()
+    block, other = default_block(device), default_block(device)
+    other.load_state_dict(block.state_dict())
+    assert keys_of(other, x, monkeypatch) == keys_of(block, x, monkeypatch)
+
+
+def test_a_given_seed_outlives_another_blocks_state(device, monkeypatch):
+    """A rank that loads rank 0's state keeps the seed it was made with."""
+    x = leaf(device, 2, 32, seed=1).detach()
+    blocks = [train.Mlp8(32, 64, seed=s, device=device, dtype=torch.float32) for s in (1, 2, 2)]
+    blocks[0](x)
+    blocks[2](x)
+    blocks[1].load_state_dict(blocks[0].state_dict())
+    assert blocks[1].passes == 1
+    assert keys_of(blocks[1], x, monkeypatch) == keys_of(blocks[2], x, monkeypatch)
+
+
+def test_a_state_without_the_count_is_taken(device):
+    """One saved before the block kept it: the weights are loaded, strictly."""
+    block, other = default_block(device), default_block(device)
+    state = {k: v for k, v in block.state_dict().items() if not k.endswith("_extra_state")}
+    assert len(state) == 6
+    other(leaf(device, 2, 32, seed=1))
+    other.load_state_dict(state, strict=True)
+    assert torch.equal(other.up.weight, block.up.weight) and other.passes == 1
