@@ -470,16 +470,20 @@ def _new_copy(t: torch.Tensor) -> Act8:
     return Act8.empty(t.shape[0], t.shape[1], t.device)
 
 
+def _parts(a):
+    """What a copy holds, for save_for_backward."""
+    return (None, None) if a is None else (a.codes, a.exps)
+
+
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps, bits, seed):
         x2 = _rows(x, x.shape[-1])
-        kept = _new_copy(x2) if bits == 8 else None
+        kept = _new_copy(x2) if bits == 8 and any(ctx.needs_input_grad) else None
         y, mean, rstd = gqt_layer_norm(x2, weight, bias, eps, save_x=kept, seed_x=seed)
         ctx.bits, ctx.d = bits, x2.shape[1]
         ctx.bias_dtype = None if bias is None else bias.dtype
-        ctx.save_for_backward(mean, rstd, weight,
-                              *((kept.codes, kept.exps) if bits == 8 else (x2,)))
+        ctx.save_for_backward(mean, rstd, weight, *(_parts(kept) if bits == 8 else (x2,)))
         return y.view(x.shape)
 
     @staticmethod
@@ -496,9 +500,10 @@ class _LayerNorm(torch.autograd.Function):
 
 
 def _bits(bits):
+    """`bits`, checked; None where there is no backward pass to keep for."""
     if bits not in (None, 8):
         raise ValueError(f"bits must be None or 8, got {bits!r}")
-    return bits
+    return bits if torch.is_grad_enabled() else None
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, *, bits=None, seed=None):
@@ -512,10 +517,10 @@ class _Gelu(torch.autograd.Function):
     @staticmethod
     def forward(ctx, h, approximate, bits, seed):
         h2 = _rows(h, h.shape[-1])
-        kept = _new_copy(h2) if bits == 8 else None
+        kept = _new_copy(h2) if bits == 8 and ctx.needs_input_grad[0] else None
         y = gqt_gelu(h2, approximate, save_h=kept, seed_h=seed)
         ctx.bits, ctx.d, ctx.approximate = bits, h2.shape[1], approximate
-        ctx.save_for_backward(*((kept.codes, kept.exps) if bits == 8 else (h2,)))
+        ctx.save_for_backward(*(_parts(kept) if bits == 8 else (h2,)))
         return y.view(h.shape)
 
     @staticmethod
@@ -574,15 +579,20 @@ def _parameter_grads(dy, x, dtypes, bias):
 
 class _Linear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, bias, seed):
+    def forward(ctx, x, weight, bias, seed, grad):
         dtype = _product_dtype(x)
+        need = ctx.needs_input_grad
         ctx.x_dtype, ctx.dtypes = x.dtype, _dtypes_of(weight, bias)
         with _no_autocast(x):
             x, weight, bias = _cast(x, dtype), _cast(weight, dtype), _cast(bias, dtype)
             x2 = _rows(x, x.shape[-1])
-            kept = gqt_act8_save(x2, seed=seed)
+            if grad and (need[1] or need[2]):
+                kept = gqt_act8_save(x2, seed=seed)
+            else:
+                _matrix(x2, "x")  # refuses what the copy would
+                kept = None
             ctx.d = x2.shape[1]
-            ctx.save_for_backward(weight, kept.codes, kept.exps)
+            ctx.save_for_backward(weight if need[0] else None, *_parts(kept))
             return torch.nn.functional.linear(x, weight, bias)
 
     @staticmethod
@@ -596,21 +606,22 @@ class _Linear(torch.autograd.Function):
             if ctx.needs_input_grad[1] or ctx.needs_input_grad[2]:
                 dw, db = _parameter_grads(_rows(dy, dy.shape[-1]), Act8(codes, exps, ctx.d),
                                           ctx.dtypes, ctx.needs_input_grad[2])
-        return dx, dw, db, None
+        return dx, dw, db, None, None
 
 
 def linear(x, weight, bias=None, *, seed=None):
     """x w^T + bias (the library's product), differentiable, with x kept for
-    the weight's gradient in 8 bits.  Under autocast the product and the copy
-    are those of the cast x, and the gradients have the dtypes of x, weight
-    and bias; autocast has to be to bf16."""
-    return _Linear.apply(x, weight, bias, seed)
+    the weight's gradient, where there is one, in 8 bits.  Under autocast the
+    product and the copy are those of the cast x, and the gradients have the
+    dtypes of x, weight and bias; autocast has to be to bf16."""
+    return _Linear.apply(x, weight, bias, seed, torch.is_grad_enabled())
 
 
 class _Mlp8(torch.autograd.Function):
     """norm -> up -> GELU -> down.  The norm and GELU leave the 8-bit copies
     of their input (for their own backward) and of their output (for the
-    weight gradient of the product that reads it) in one pass each."""
+    weight gradient of the product that reads it) in one pass each, as far as
+    a gradient reads them."""
 
     @staticmethod
     def forward(ctx, x, nw, nb, w1, b1, w2, b2, eps, approximate, seed):
@@ -619,8 +630,11 @@ class _Mlp8(torch.autograd.Function):
         rows, d = x2.shape
         ff = w1.shape[0]
         seeds = _copy_seeds(seed)
-        x8, a8 = _new_copy(x2), _new_copy(x2)
-        h8, g8 = Act8.empty(rows, ff, x.device), Act8.empty(rows, ff, x.device)
+        need = ctx.needs_input_grad
+        x8 = _new_copy(x2) if any(need[:3]) else None
+        a8 = _new_copy(x2) if need[3] or need[4] else None
+        h8 = Act8.empty(rows, ff, x.device) if any(need[:5]) else None
+        g8 = Act8.empty(rows, ff, x.device) if need[5] or need[6] else None
         ctx.d, ctx.ff, ctx.approximate, ctx.x_dtype = d, ff, approximate, x.dtype
         ctx.dtypes1, ctx.dtypes2 = _dtypes_of(w1, b1), _dtypes_of(w2, b2)
         with _no_autocast(x):
@@ -630,12 +644,14 @@ class _Mlp8(torch.autograd.Function):
                                            save_y=None if cast else a8, seed_y=seeds[1])
             if cast:  # the copy is of what the product reads
                 a = a.to(dtype)
-                gqt_act8_save(a, seed=seeds[1], out=a8)
+                if a8 is not None:
+                    gqt_act8_save(a, seed=seeds[1], out=a8)
             h = torch.nn.functional.linear(a, w1, b1)
             g = gqt_gelu(h, approximate, save_h=h8, seed_h=seeds[2], save_y=g8, seed_y=seeds[3])
             y = torch.nn.functional.linear(g, w2, b2)
-        ctx.save_for_backward(mean, rstd, nw, w1, w2, x8.codes, x8.exps, a8.codes, a8.exps,
-                              h8.codes, h8.exps, g8.codes, g8.exps)
+        ctx.save_for_backward(mean, rstd, nw, w1 if any(need[:3]) else None,
+                              w2 if any(need[:5]) else None, *_parts(x8), *_parts(a8),
+                              *_parts(h8), *_parts(g8))
         return y.view(*x.shape[:-1], w2.shape[0])
 
     @staticmethod

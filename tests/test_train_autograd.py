@@ -366,3 +366,97 @@ def test_a_state_without_the_count_is_taken(device):
     other(leaf(device, 2, 32, seed=1))
     other.load_state_dict(state, strict=True)
     assert torch.equal(other.up.weight, block.up.weight) and other.passes == 1
+
+
+# ---------------------------------------------------------------------------
+# copies that nobody reads
+
+def kept_bytes(call):
+    """The result of a call, and the bytes that it holds for the backward pass."""
+    held = []
+    with torch.autograd.graph.saved_tensors_hooks(
+            lambda t: held.append(t) or t, lambda t: t):
+        y = call()
+    return y, sum(t.numel() for t in held if t.dtype in (torch.int8, torch.uint8))
+
+
+@pytest.fixture
+def copies(device, monkeypatch):
+    """The copies written, by the operator that writes them."""
+    written = []
+    for name in ("save", "layer_norm", "gelu"):
+        name = "gqt_act8_save" if name == "save" else "gqt_" + name
+
+        def op(*args, real=getattr(train, name), name=name, **kw):
+            if name == "gqt_act8_save" or kw.get("save_x") or kw.get("save_h"):
+                written.append(name)
+            return real(*args, **kw)
+        monkeypatch.setattr(train, name, op)
+    return written
+
+
+def test_linear_keeps_what_its_gradients_read(device, copies):
+    x, w, b = (leaf(device, *s, seed=1) for s in ((6, 40), (24, 40), (24,)))
+    g = leaf(device, 6, 24, seed=2).detach()
+    want = train.linear(x, w, b, seed=3)
+    assert copies.pop() == "gqt_act8_save"
+    with torch.no_grad():
+        assert torch.equal(train.linear(x, w, b, seed=3), want)
+    assert torch.equal(train.linear(x.detach(), w.detach(), b.detach()), want)
+    y, held = kept_bytes(lambda: train.linear(x, w.detach(), b.detach(), seed=3))
+    assert held == 0 and not copies and torch.equal(y, want)
+    y.backward(g)
+    frozen = x.grad
+    x.grad = None
+    want.backward(g)
+    assert torch.equal(frozen, x.grad)
+    # the bias alone: its gradient comes with the product that reads the copy
+    y, held = kept_bytes(lambda: train.linear(x.detach(), w.detach(), b, seed=3))
+    full, b.grad = b.grad, None
+    y.backward(g)
+    assert torch.equal(b.grad, full)
+
+
+def test_layer_norm_keeps_what_its_gradients_read(device, copies):
+    x, w, b = (leaf(device, *s, seed=1) for s in ((6, 40), (40,), (40,)))
+    with torch.no_grad():
+        y = train.layer_norm(x, w, b, bits=8)
+    frozen = train.layer_norm(x.detach(), w.detach(), b.detach(), bits=8)
+    assert not copies and torch.equal(y, frozen)
+    y, held = kept_bytes(lambda: train.layer_norm(x.detach(), w, b, bits=8))
+    assert copies == ["gqt_layer_norm"] and held == 6 * (64 + 2)
+    y.sum().backward()
+    assert host(w.grad).any() and host(b.grad).any()
+
+
+def test_gelu_keeps_what_its_gradient_reads(device, copies):
+    h = leaf(device, 6, 40, seed=1)
+    with torch.no_grad():
+        y = train.gelu(h, bits=8)
+    assert torch.equal(y, train.gelu(h.detach(), bits=8)) and not copies
+    assert torch.equal(y, train.gelu(h, bits=8)) and copies == ["gqt_gelu"]
+
+
+def test_mlp8_keeps_what_its_gradients_read(device, copies):
+    """With frozen weights, those of the activations that the norm and GELU
+    read; in evaluation, none."""
+    block, x = mlp8(device, random=False), leaf(device, 6, 64, seed=1)
+    y, held = kept_bytes(lambda: block(x))
+    assert held == 6 * 2 * (64 + 2 + 96 + 3)
+    y.sum().backward()
+    full, x.grad = x.grad, None
+    block.requires_grad_(False)
+    z, held = kept_bytes(lambda: block(x))
+    assert held == 6 * (64 + 2 + 96 + 3) and torch.equal(y, z)
+    z.sum().backward()
+    assert torch.equal(x.grad, full)
+    del copies[:]
+    z, held = kept_bytes(lambda: block(x.detach()))
+    assert held == 0 and not copies and torch.equal(y, z)
+
+
+def test_linear_without_a_copy_refuses_the_same():
+    w = torch.ones(24, 40)
+    for x in (torch.ones(6, 40), torch.ones(6, 40, requires_grad=True)):
+        with pytest.raises(ValueError, match="device tensor"):
+            train.linear(x, w)
