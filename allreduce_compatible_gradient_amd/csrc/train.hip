@@ -604,56 +604,78 @@ __device__ __forceinline__ float scaled_tail(float z)
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhC = 0.79788456080286536f; // sqrt(2 / pi)
 constexpr float kTanhA = 0.044715f;
+constexpr float kTanh1 = 2 * 0.79788456080286536; // the tanh form's 2 u = kTanh1 h + kTanh3 h^3
+constexpr float kTanh3 = 2 * 0.79788456080286536 * 0.044715;
 constexpr float kLog2E = 1.4426950408889634f;
 
 // 4^x for x <= 0, by squaring 2^x: the part's exponential flushes results
-// below 2^-126, its square does not.  An exponential whose argument is
-// carried in two floats would gain nothing here, where the argument itself
-// was rounded before.
+// below 2^-126, its square does not.
 __device__ __forceinline__ float exp4(float x)
 {
     const float half = __builtin_amdgcn_exp2f(x);
     return half * half;
 }
+
+// The exponentials of a T: bf16 by exp4, whose few more roundings are far
+// below the result's; fp32 by one that is good to the last bit and takes the
+// argument with the fewest roundings, which are the result's error in the
+// tail.  bf16 would be bound by VALU issue with it (see k_gelu); fp32, bound by
+// memory, takes as long (8192 x 4096: erf 43 us a call and 45 with exp4, tanh
+// 46 and 44, with a random copy 53 and 52, backward 70 and 70) but for the erf
+// form with two random copies (64 and 56).
+//
 // e^(-h^2 / 2)
-__device__ __forceinline__ float bell(float h) { return exp4(-0.25f * kLog2E * h * h); }
+template <typename T>
+__device__ __forceinline__ float bell(float h)
+{
+    if (sizeof(T) == 4)
+        return expf(-0.5f * h * h);
+    return exp4(-0.25f * kLog2E * h * h);
+}
+// e^-|2u|, u = sqrt(2 / pi) (h + 0.044715 h^3)
+template <typename T>
+__device__ __forceinline__ float tanh_exp(float h)
+{
+    if (sizeof(T) == 4)
+        return expf(-fabsf(h * fmaf(kTanh3 * h, h, kTanh1)));
+    return exp4(-fabsf(h * fmaf(kLog2E * kTanhC * kTanhA * h, h, kLog2E * kTanhC)));
+}
 
 // The tanh form's logistic function s = s(2 u) and its complement 1 - s, both
 // from e^-|2u|, so that neither is the difference of near numbers.
 struct Gate {
     float s, c;
 };
+template <typename T>
 __device__ __forceinline__ Gate tanh_gate(float h)
 {
-    // u log2(e)
-    const float w = h * fmaf(kLog2E * kTanhC * kTanhA * h, h, kLog2E * kTanhC);
-    const float e = exp4(-fabsf(w));
+    const float e = tanh_exp<T>(h);
     const float big = __builtin_amdgcn_rcpf(1.0f + e);
     const float small = e * big;
     return h < 0.0f ? Gate{small, big} : Gate{big, small};
 }
 
-template <int FORM>
+template <typename T, int FORM>
 __device__ __forceinline__ float gelu(float h)
 {
     if (FORM == GQT_GELU_TANH)
-        return h * tanh_gate(h).s;
-    const float tail = scaled_tail(fabsf(h)) * bell(h);
+        return h * tanh_gate<T>(h).s;
+    const float tail = scaled_tail(fabsf(h)) * bell<T>(h);
     return h * (h < 0.0f ? tail : 1.0f - tail);
 }
 
-template <int FORM>
+template <typename T, int FORM>
 __device__ __forceinline__ float gelu_slope(float h)
 {
     if (FORM == GQT_GELU_TANH) {
-        const Gate g = tanh_gate(h);
+        const Gate g = tanh_gate<T>(h);
         // s (1 - s) is 0 in fp32 long before |h| = 64, where h u' would go
         // on to overflow; a NaN comes through g
         const float c = fminf(fmaxf(h, -64.0f), 64.0f);
         const float u = kTanhC * fmaf(3.0f * kTanhA * c, c, 1.0f);
         return fmaf(2.0f * c * u, g.s * g.c, g.s);
     }
-    const float e = bell(h);
+    const float e = bell<T>(h);
     const float tail = scaled_tail(fabsf(h)) * e;
     return fmaf(h * kInvSqrt2Pi, e, h < 0.0f ? tail : 1.0f - tail);
 }
@@ -679,7 +701,7 @@ __global__ __launch_bounds__(kThreads) void k_gelu(const T *__restrict__ h, uint
         keep8(keep_h, c.row, c.col, i, v);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-        v[k] = gelu<FORM>(v[k]);
+        v[k] = gelu<T, FORM>(v[k]);
     if (n > 0)
         store8(y + c.row * d + c.col, n, v); // columns past d: gelu(0) = 0
     if (KEEP && keep_y.keep != kKeepNone)
@@ -706,7 +728,7 @@ __global__ __launch_bounds__(kThreads) void k_gelu_backward(
         load8(h + c.row * ldh, c.col, d, v);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-        g[k] *= gelu_slope<FORM>(v[k]);
+        g[k] *= gelu_slope<T, FORM>(v[k]);
     store8(dh + c.row * d + c.col, n, g);
 }
 
