@@ -9,8 +9,9 @@
 // lane i of a row of 16 takes columns 8 i to 8 i + 7; fragment c is column
 // 8 i + c, put together by four byte permutes of pairs of tokens (dy), or by
 // the permutes that narrow the decoded codes to bf16 (x).  A code times its
-// group's power of two is exact in bf16; an fp32 dy is the exact sum of three
-// bf16 parts and takes three MFMAs.  All sums are fp32.
+// group's power of two is exact in bf16; an fp32 dy is the sum of three bf16
+// parts (exact from 2^-110 on, where its last bit is bf16's last place, 2^-133)
+// and takes three MFMAs.  All sums are fp32.
 //
 // What bounds it is the work around the MFMAs: a wave spends as long decoding
 // codes, pairing tokens and waiting as multiplying.  8192 x 4096 x 1024 bf16
@@ -77,8 +78,9 @@ __device__ __forceinline__ void dy_fragment(const RawDy<bf16> &l, int c, u32x4 (
 }
 
 // A float's leading 8, middle 8 and last 8 significant bits: truncated, so
-// that each rest is exact.  An inf stays in the first part alone; a NaN's
-// rest is one too.
+// that each rest is exact.  Below 2^-110 the last part drops what lies under
+// 2^-133; subnormal parts count in the MFMA as they are.  An inf stays in the
+// first part alone; a NaN's rest is one too.
 __device__ __forceinline__ void dy_fragment(const RawDy<float> &l, int c, u32x4 (&part)[3])
 {
     uint32_t b[3][8];

@@ -111,8 +111,9 @@ int32_t gqt_gelu_backward(const void *dy, int32_t dtype, int64_t rows, int64_t d
 /* Gradient of y = x w^T + bias with respect to w[n][k] and bias[n], from
  * dy[m][n] and the 8-bit copy x8 of x[m][k]:
  *   dw = dy^T x, db = sum over rows of dy (may be NULL), both in wdtype.
- * Every product is exact (an fp32 dy is taken as the sum of three bf16
- * parts) and the sums are fp32.  n and k lie in [1, 2^27), and
+ * Products are exact (an fp32 dy is taken as the sum of three bf16 parts,
+ * which hold it whole from |dy| = 2^-110 on; below, what lies under 2^-133
+ * is left out) and the sums are fp32.  n and k lie in [1, 2^27), and
  * n k < 2^36.  With m == 0, dw and db are zeros.  dy: lddy >= n, or 0.     */
 int64_t gqt_weight_grad_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t dtype);
 int32_t gqt_weight_grad(const void *dy, int32_t dtype, int64_t m, int64_t n, int64_t lddy,
