@@ -460,3 +460,77 @@ def test_linear_without_a_copy_refuses_the_same():
     for x in (torch.ones(6, 40), torch.ones(6, 40, requires_grad=True)):
         with pytest.raises(ValueError, match="device tensor"):
             train.linear(x, w)
+
+
+# ---------------------------------------------------------------------------
+# bf16, the blocks' own type
+
+def test_linear_in_bf16(device):
+    x, w, b = (leaf(device, *s, seed=i, dtype=torch.bfloat16)
+               for i, s in enumerate(((12, 40), (24, 40), (24,))))
+    g = leaf(device, 12, 24, seed=4, dtype=torch.bfloat16).detach()
+    y = train.linear(x, w, b, seed=5)
+    assert torch.equal(y, F.linear(x, w, b))
+    y.backward(g)
+    gn, kept = host(g), copy_of(x.detach(), 5)
+    for got, want, bound in zip((w.grad, b.grad), plain.weight_grad(gn, kept),
+                                plain.weight_grad_bounds(gn, kept, "bf16")):
+        assert got.dtype == torch.bfloat16 and (np.abs(host(got) - want) <= bound).all()
+    assert (np.abs(host(x.grad) - gn @ host(w)) <= product_bound(gn, host(w))).all()
+
+
+@pytest.mark.parametrize("bits", [None, 8])
+def test_layer_norm_and_gelu_in_bf16(device, bits):
+    x, w, b = (leaf(device, *s, seed=i, dtype=torch.bfloat16)
+               for i, s in enumerate(((9, 50), (50,), (50,))))
+    g = leaf(device, 9, 50, seed=4, dtype=torch.bfloat16).detach()
+    kept = copy_of(x.detach(), 9) if bits else host(x)
+    y = train.layer_norm(x, w, b, 1e-5, bits=bits, seed=9 if bits else None)
+    wn, bn = host(w)[None], host(b)[None]
+    assert (np.abs(host(y) - plain.layer_norm(host(x), wn, bn, 1e-5))
+            <= plain.layer_norm_bound(host(x), wn, bn, 1e-5, "bf16")).all()
+    y.backward(g)
+    mean, rstd = plain.norm_stats(host(x), 1e-5)
+    args = host(g), kept, mean, rstd, wn
+    # the statistics, inputs of the bounds, are themselves off in fp32: by less
+    # than 64 U of the terms, far below a bf16 rounding
+    for got, want, bound in zip((x.grad, w.grad, b.grad), plain.layer_norm_backward(*args),
+                                plain.layer_norm_backward_bounds(*args, "bf16", "bf16")):
+        assert got.dtype == torch.bfloat16
+        assert (np.abs(host(got) - want) <= bound + 64 * plain.U * 50).all()
+    for form in ("none", "tanh"):
+        x.grad = None
+        y = train.gelu(x, form, bits=bits, seed=9 if bits else None)
+        y.backward(g)
+        want = host(g) * plain.gelu_slope(kept, form)
+        bound = np.abs(host(g)) * plain.gelu_bounds(kept, form)[1]
+        assert x.grad.dtype == torch.bfloat16
+        assert (np.abs(host(x.grad) - want)
+                <= bound + np.abs(want) * plain.HALF["bf16"] * 1.01 + 2.0**-126).all()
+
+
+@pytest.mark.parametrize("random", [False, True])
+def test_mlp8_in_bf16(device, random):
+    """The default type: as under autocast, and a rounding more of the
+    gradients themselves."""
+    torch.manual_seed(0)
+    block = train.Mlp8(96, 200, random=random, device=device)
+    assert all(p.dtype == torch.bfloat16 for p in block.parameters())
+    x = leaf(device, 5, 8, 96, seed=1, dtype=torch.bfloat16)
+    dy = leaf(device, 5, 8, 96, seed=2, dtype=torch.bfloat16).detach()
+    y = block(x)
+    y.backward(dy)
+    got = [x.grad] + [p.grad for p in block.parameters()]
+    assert all(g.dtype == torch.bfloat16 for g in got)
+    # the ordinary block in fp32, from the same values
+    ref = torch.nn.ModuleDict({"norm": torch.nn.LayerNorm(96), "up": torch.nn.Linear(96, 200),
+                               "down": torch.nn.Linear(200, 96)}).to(device)
+    ref.load_state_dict({k: v.float() for k, v in block.state_dict().items()
+                         if not k.endswith("_extra_state")})
+    xr = x.detach().float().requires_grad_()
+    z = xr + ref.down(F.gelu(ref.up(ref.norm(xr)), approximate="tanh"))
+    scale = float((z - xr).detach().abs().max() + z.detach().abs().max())
+    assert float((y.float() - z).detach().abs().max()) < 8 * 2.0**-8 * scale
+    z.backward(dy.float())
+    for g, e in zip(got, [xr.grad] + [p.grad for p in ref.parameters()]):
+        assert float((g.float() - e).norm() / e.norm()) < 0.03 + 6 * 2.0**-8
