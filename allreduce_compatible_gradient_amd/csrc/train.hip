@@ -55,9 +55,11 @@ namespace {
 //
 // Forward: mean = sum x / d, rstd = 1 / sqrt(sum (x - mean)^2 / d + eps), y =
 // (x - mean) rstd w + b.  Bound by memory: 16384 x 4096 bf16 50 us (5.3 TB/s
-// of one read and one write), 131072 x 64 9.6 us.  With a copy of x at random
-// rounding, whose Philox calls and conversions are most of its instructions,
-// 8191 x 2048 bf16 takes 26 us (3.2 TB/s; VALU 54 % of the issue slots).
+// of one read and one write), 131072 x 64 9.6 us.  Copies take instructions:
+// bf16 8191 x 2048 15 us without, 19 with one to nearest (VALU in 50 % of the
+// issue slots), 25 with one at random (55 %), 36 with two at random (63 %;
+// 32768 x 2048 89 %).  Between, neither memory (3.2 TB/s with one at random)
+// nor VALU is full; a block has one row, whose two sums cost four barriers.
 
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float *lds)
@@ -548,8 +550,9 @@ __device__ __forceinline__ Chunk chunk_at(uint32_t i, const FastDiv &per_row)
 
 constexpr int kThreads = 256;
 
-// A copy of a matrix: bound by memory, 16384 x 4096 bf16 39 us (5.2 TB/s of
-// 2 + 33/32 bytes a value, VALU in 46 % of the issue slots with random rounding).
+// A copy of a matrix, 16384 x 4096 bf16: to nearest bound by memory, 35 to 39
+// us (5.2 to 5.8 TB/s of 2 + 33/32 bytes a value; VALU in 46 % of the issue
+// slots); at random 46 us (71 %).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_act8_save(const T *__restrict__ x, uint32_t chunks,
                                                         FastDiv per_row, int32_t d, int64_t ldx,
@@ -684,7 +687,10 @@ __device__ __forceinline__ float gelu_slope(float h)
 // with y' = Phi + h phi or s + 2 h s (1 - s) u'.  With an exponential good to
 // the last bit both kernels were bound by VALU issue (0.98 instructions a CU
 // and clock, 79 us for the step of 8192 x 4096 bf16 in the tanh form with a
-// random copy of h); now the step takes 64 us, 5.3 TB/s of its 338 MB, at 0.81 and 0.70.
+// random copy of h); now the step takes 64 us, 5.3 TB/s of its 338 MB, at 0.81
+// and 0.70.  More instructions are bound by their issue: the erf form takes 29
+// us forward without a copy (0.71) and 41 with a random one (0.91), the tanh
+// form with two 50 (0.87).
 template <typename T, int FORM, bool KEEP>
 __global__ __launch_bounds__(kThreads) void k_gelu(const T *__restrict__ h, uint32_t chunks,
                                                    FastDiv per_row, int32_t d, int64_t ldh,
@@ -795,8 +801,10 @@ constexpr int kCUs = 256;
 
 // Layer norm shapes: threads per row (whole waves from 64 on) and chunks a
 // thread, so that few lanes are idle (at half of them d = 256 and 5120 ran at
-// 3.4 and 2.7 TB/s), the gradient's sums do not spill, and registers leave
-// room for waves (bf16 8191 x 2048 forward with a random copy: 25 us a call
+// 3.4 and 2.7 TB/s; just past 512 and 2048 it is still so: bf16 64527 x 520
+// forward runs at 3.1 TB/s, d = 768 at 4.8, 2056 at 3.8, 2304 at 4.1, 2560 at
+// 4.6, 1024 and 4096 at 5.6), the gradient's sums do not spill, and registers
+// leave room for waves (bf16 8191 x 2048 forward with a random copy: 25 us a call
 // with 256 threads a row, 34 with one wave and four chunks).
 #define GQT_BY_ROW_LENGTH(LAUNCH, LONG) \
     do {                                \

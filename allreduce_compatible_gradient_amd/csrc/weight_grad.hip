@@ -571,8 +571,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(
 // n < 8: too few rows of dw for a tile, whose lanes load eight columns of dy
 // that exist.  A block's 16 lanes take 128 columns of x, its 16 rows of
 // threads every 16th token, and one product a value is an ordinary fused
-// multiply-add.  Bound by the decoding of x: 16384 x 4 x 1024 27 us a call.
-// db comes from block 0.
+// multiply-add.  16384 x 4 x 1024 takes 27 to 38 us a call (two boxes), bound
+// by waiting for its loads: plan_of cuts it as it cuts the large tiles, a block
+// a CU, so that a SIMD has one wave, which loads nothing ahead (VALU in 14 % of
+// the issue slots).  db comes from block 0.
 template <typename T>
 __global__ __launch_bounds__(256) void k_weight_grad_narrow(
     const T *__restrict__ dy, int64_t m, int32_t n, int64_t lddy, Act8 x, int32_t k, int64_t chunk,
