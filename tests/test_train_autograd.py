@@ -534,3 +534,33 @@ def test_mlp8_in_bf16(device, random):
     z.backward(dy.float())
     for g, e in zip(got, [xr.grad] + [p.grad for p in ref.parameters()]):
         assert float((g.float() - e).norm() / e.norm()) < 0.03 + 6 * 2.0**-8
+
+
+def test_no_rows(device):
+    """An empty batch: empty results, and gradients of zeros."""
+    block = train.Mlp8(32, 64, seed=1, device=device, dtype=torch.float32)
+    x = torch.empty((0, 3, 32), device=device, requires_grad=True)
+    w, b = leaf(device, 24, 32, seed=2), leaf(device, 24, seed=3)
+    for y, shape in ((block(x), (0, 3, 32)), (train.linear(x, w, b), (0, 3, 24)),
+                     (train.layer_norm(x, bits=8), (0, 3, 32)), (train.gelu(x, bits=8), (0, 3, 32))):
+        assert y.shape == shape
+        x.grad = None
+        y.sum().backward()
+        assert x.grad.shape == x.shape
+    for p in (w, b, *block.parameters()):
+        assert p.grad is not None and not p.grad.any()
+
+
+@pytest.mark.parametrize("reentrant", [False, True])
+def test_mlp8_under_activation_checkpointing(device, reentrant):
+    """The backward pass reads the copies of the recomputed pass: to nearest,
+    the same gradients (up to the order of the library's sums)."""
+    from torch.utils.checkpoint import checkpoint
+    block, grads = mlp8(device, random=False), []
+    for kept in (True, False):
+        x = leaf(device, 6, 64, seed=1)
+        block.zero_grad()
+        y = block(x) if kept else checkpoint(block, x, use_reentrant=reentrant)
+        y.sum().backward()
+        grads.append([x.grad, *(p.grad.clone() for p in block.parameters())])
+    assert all(torch.allclose(a, b, rtol=1e-5, atol=1e-5) for a, b in zip(*grads))
