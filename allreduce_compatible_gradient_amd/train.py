@@ -552,13 +552,14 @@ def _no_autocast(t):
     the same weights would have no gradient for them; and in a backward pass
     it would round what the forward pass did not."""
     kind = t.device.type
-    if torch.is_autocast_enabled(kind):
-        return torch.autocast(kind, enabled=False)
-    return contextlib.nullcontext()
+    return torch.autocast(kind, enabled=False) if torch.is_autocast_enabled(kind) else _AS_IT_IS
+
+
+_AS_IT_IS = contextlib.nullcontext()
 
 
 def _cast(t, dtype):
-    return t if t is None or dtype is None else t.to(dtype)
+    return t if t is None or dtype is None or t.dtype == dtype else t.to(dtype)
 
 
 def _dtypes_of(weight, bias):
@@ -573,8 +574,10 @@ def _dtypes_of(weight, bias):
 def _parameter_grads(dy, x, dtypes, bias):
     """(dw, db) in their parameters' dtypes, of which autocast takes two: both
     are computed in the wider."""
+    if dtypes[0] == dtypes[1]:
+        return gqt_weight_grad(dy, x, dtype=dtypes[0], bias=bias)
     dw, db = gqt_weight_grad(dy, x, dtype=torch.promote_types(*dtypes), bias=bias)
-    return dw.to(dtypes[0]), None if db is None else db.to(dtypes[1])
+    return _cast(dw, dtypes[0]), _cast(db, dtypes[1])
 
 
 class _Linear(torch.autograd.Function):
@@ -583,7 +586,7 @@ class _Linear(torch.autograd.Function):
         dtype = _product_dtype(x)
         need = ctx.needs_input_grad
         ctx.x_dtype, ctx.dtypes = x.dtype, _dtypes_of(weight, bias)
-        with _no_autocast(x):
+        with _AS_IT_IS if dtype is None else _no_autocast(x):
             x, weight, bias = _cast(x, dtype), _cast(weight, dtype), _cast(bias, dtype)
             x2 = _rows(x, x.shape[-1])
             if grad and (need[1] or need[2]):
@@ -602,7 +605,7 @@ class _Linear(torch.autograd.Function):
         dx = dw = db = None
         with _no_autocast(dy):
             if ctx.needs_input_grad[0]:
-                dx = (dy @ weight).to(ctx.x_dtype)
+                dx = _cast(dy @ weight, ctx.x_dtype)
             if ctx.needs_input_grad[1] or ctx.needs_input_grad[2]:
                 dw, db = _parameter_grads(_rows(dy, dy.shape[-1]), Act8(codes, exps, ctx.d),
                                           ctx.dtypes, ctx.needs_input_grad[2])
@@ -637,7 +640,7 @@ class _Mlp8(torch.autograd.Function):
         g8 = Act8.empty(rows, ff, x.device) if need[5] or need[6] else None
         ctx.d, ctx.ff, ctx.approximate, ctx.x_dtype = d, ff, approximate, x.dtype
         ctx.dtypes1, ctx.dtypes2 = _dtypes_of(w1, b1), _dtypes_of(w2, b2)
-        with _no_autocast(x):
+        with _AS_IT_IS if dtype is None else _no_autocast(x):
             w1, b1, w2, b2 = (_cast(t, dtype) for t in (w1, b1, w2, b2))
             cast = dtype is not None and dtype != x.dtype
             a, mean, rstd = gqt_layer_norm(x2, nw, nb, eps, save_x=x8, seed_x=seeds[0],
@@ -672,7 +675,7 @@ class _Mlp8(torch.autograd.Function):
                     dw1, db1 = _parameter_grads(dh, a8, ctx.dtypes1, need[4])
                 if any(need[:3]):
                     dx, dnw, dnb = gqt_layer_norm_backward(
-                        (dh @ w1).to(ctx.x_dtype), x8, mean, rstd, nw, weight_grad=need[1],
+                        _cast(dh @ w1, ctx.x_dtype), x8, mean, rstd, nw, weight_grad=need[1],
                         bias_grad=need[2])
                     dx = dx.view(*dy.shape[:-1], d)
         return dx, dnw, dnb, dw1, db1, dw2, db2, None, None, None
