@@ -12,6 +12,9 @@ LIB_PATH = os.path.join(PKG, "libgq.so")
 # the training operators (include/gq_train.h), a library of their own
 TRAIN_SOURCES = [os.path.join(PKG, "csrc", f) for f in ("train.hip", "weight_grad.hip")]
 TRAIN_LIB_PATH = os.path.join(PKG, "libgq_train.so")
+# the ends of a training step (include/gq_step.h), a library of their own
+STEP_SOURCES = [os.path.join(PKG, "csrc", f) for f in ("fp8.hip", "adamw.hip")]
+STEP_LIB_PATH = os.path.join(PKG, "libgq_step.so")
 # measurement kernels (read and VALU-issue ceilings), a library of their own
 PROBE_SOURCES = [os.path.join(PKG, "csrc", "probe.hip")]
 PROBE_LIB_PATH = os.path.join(PKG, "libgq_probe.so")
@@ -58,6 +61,10 @@ def build_train(verbose: bool = False) -> str:
     return build_library(verbose, TRAIN_SOURCES, TRAIN_LIB_PATH)
 
 
+def build_step(verbose: bool = False) -> str:
+    return build_library(verbose, STEP_SOURCES, STEP_LIB_PATH)
+
+
 def build_probe(verbose: bool = False) -> str:
     return build_library(verbose, PROBE_SOURCES, PROBE_LIB_PATH)
 
@@ -65,4 +72,5 @@ def build_probe(verbose: bool = False) -> str:
 if __name__ == "__main__":
     print(build_library(verbose=True))
     print(build_train(verbose=True))
+    print(build_step(verbose=True))
     print(build_probe(verbose=True))

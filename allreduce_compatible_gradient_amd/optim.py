@@ -1,0 +1,210 @@
+"""AdamW over many tensors at once, with moments in 32 or 8 bits, and the
+gradients' norm and clipping factor (libgq_step.so, ``include/gq_step.h``).
+
+They take what ``ddp.global_qsgd_hook`` leaves in the gradients.  A moment in
+8 bits (``Moment8``) is one byte a value and a power of two for each 128: e4m3
+for the first, 5 exponent and 3 mantissa bits for the second, which is never
+negative.  Both are rounded at random without bias, with the compressor's
+Philox uniforms; to nearest, a second moment that decays by a thousandth a
+step would never move.  A bf16 parameter may be rounded at random too, so that
+updates below its last place count in expectation.
+
+``gqs_*`` are the C entry points on lists of device tensors, in place, on
+torch's current stream or a given one, with no synchronization.  ``AdamW`` is
+the optimizer.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from ._step import CAdamWArgs, check, lib
+from .train import _current, _dtype, _Elsewhere, _elsewhere, _mix_seed
+
+_E4M3 = torch.float8_e4m3fn
+
+
+class Moment8:
+    """A moment of a tensor of n elements in 8 bits: ``codes`` [128 G]
+    (float8_e4m3fn for a first moment, uint8 for a second) and ``exps`` uint8
+    [G], G = ceil(n / 128)."""
+
+    __slots__ = ("codes", "exps", "n")
+
+    def __init__(self, codes: torch.Tensor, exps: torch.Tensor, n: int):
+        self.codes, self.exps, self.n = codes, exps, int(n)
+
+    @classmethod
+    def zeros(cls, n: int, device, second: bool) -> "Moment8":
+        blocks = (int(n) + 127) // 128
+        codes = torch.zeros(128 * blocks, dtype=torch.uint8, device=device)
+        return cls(codes if second else codes.view(_E4M3),
+                   torch.full((blocks,), 19 if second else 10, dtype=torch.uint8, device=device),
+                   n)
+
+    @property
+    def second(self) -> bool:
+        return self.codes.dtype == torch.uint8
+
+    def __repr__(self):
+        return f"Moment8({self.n}, {'second' if self.second else 'first'}, {self.codes.device})"
+
+
+def _arrays(tensors, name: str, device, dtype=None):
+    """(dtype, sizes, addresses) of contiguous device tensors of one dtype."""
+    for t in tensors:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} must be device tensors")
+        if t.device != device:
+            raise ValueError(f"{name}: a tensor is on {t.device}, expected {device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    types = {t.dtype for t in tensors}
+    if len(types) > 1 or (dtype is not None and types != {dtype}):
+        want = "one dtype" if dtype is None else str(dtype)
+        raise TypeError(f"{name} must have {want}, got {sorted(map(str, types))}")
+    return types.pop(), [t.numel() for t in tensors], [t.data_ptr() for t in tensors]
+
+
+def _moments(moments, name: str, sizes, device, second: bool):
+    """(bits, codes or values, exps) of a list of moments."""
+    if len(moments) != len(sizes):
+        raise ValueError(f"{len(moments)} {name}, {len(sizes)} tensors")
+    if not any(isinstance(m, Moment8) for m in moments):
+        _, counts, at = _arrays(moments, name, device, torch.float32)
+        if counts != sizes:
+            raise ValueError(f"{name} must have their parameters' sizes")
+        return 32, at, [0] * len(at)
+    if not all(isinstance(m, Moment8) for m in moments):
+        raise TypeError(f"{name} must be all Moment8 or all tensors")
+    if [m.n for m in moments] != sizes:
+        raise ValueError(f"{name} must have their parameters' sizes")
+    kind = torch.uint8 if second else _E4M3
+    _, counts, codes = _arrays([m.codes for m in moments], f"{name}' codes", device, kind)
+    _, groups, exps = _arrays([m.exps for m in moments], f"{name}' exps", device, torch.uint8)
+    blocks = [(n + 127) // 128 for n in sizes]
+    if groups != blocks or counts != [128 * b for b in blocks]:
+        raise ValueError(f"{name} must hold a code for each of 128 G elements and G exps")
+    return 8, codes, exps
+
+
+def _scalar(t, name: str, dtype, device):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype or t.numel() != 1:
+        raise ValueError(f"{name} must be one {dtype} on {device}")
+    return t.data_ptr()
+
+
+def _tensors_of(*lists):
+    held = []
+    for given in lists:
+        for t in given if isinstance(given, (list, tuple)) else (given,):
+            held.extend((t.codes, t.exps) if isinstance(t, Moment8) else (t,))
+    return held
+
+
+def _device_of(tensors, name: str):
+    first = tensors[0]
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        raise ValueError(f"{name} must be device tensors")
+    return first.device
+
+
+def gqs_adamw(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, betas=(0.9, 0.999),
+              eps: float = 1e-8, weight_decay: float = 1e-2, scale=None, seed=None,
+              stream=None) -> None:
+    """One AdamW step, in place, over lists of tensors: params of one dtype
+    and grads of one dtype (fp32 or bf16 each), moments as fp32 tensors or
+    Moment8, all contiguous on one device, no two overlapping.
+
+    scale: a device float, the gradients' factor.  step counts from 1; it and
+    lr may be device tensors (int64 and float32, one element), which a
+    captured graph reads at every replay.  A `seed` is needed with Moment8; a
+    bf16 parameter is rounded at random where one is given, to nearest
+    otherwise.  Calls of one step with one seed share random numbers between
+    tensors of the same number in their lists: give each list its own."""
+    params, grads = list(params), list(grads)
+    if len(params) != len(grads):
+        raise ValueError(f"{len(params)} params, {len(grads)} grads")
+    if not params:
+        return
+    device = _device_of(params, "params")
+    if _elsewhere(device, stream):
+        with _Elsewhere(device, stream, _tensors_of(params, grads, exp_avgs, exp_avg_sqs, scale,
+                                                    step, lr)):
+            return gqs_adamw(params, grads, exp_avgs, exp_avg_sqs, step=step, lr=lr, betas=betas,
+                             eps=eps, weight_decay=weight_decay, scale=scale, seed=seed)
+    p_type, sizes, p_at = _arrays(params, "params", device)
+    g_type, g_sizes, g_at = _arrays(grads, "grads", device)
+    if g_sizes != sizes:
+        raise ValueError("grads must have their parameters' sizes")
+    bits, m_at, m_exps = _moments(exp_avgs, "exp_avgs", sizes, device, False)
+    v_bits, v_at, v_exps = _moments(exp_avg_sqs, "exp_avg_sqs", sizes, device, True)
+    if bits != v_bits:
+        raise TypeError("exp_avgs and exp_avg_sqs must be both Moment8 or both tensors")
+    if bits == 8 and seed is None:
+        raise ValueError("moments in 8 bits are rounded at random: a seed is needed")
+    args = CAdamWArgs(0.0, betas[0], betas[1], eps, weight_decay, 0,
+                      _scalar(scale, "scale", torch.float32, device), None, None,
+                      0 if seed is None else int(seed) & 0xFFFFFFFFFFFFFFFF, seed is not None, bits)
+    workspace = None
+    if isinstance(lr, torch.Tensor):
+        args.lr_device = _scalar(lr, "lr", torch.float32, device)
+    else:
+        args.lr = lr
+    if isinstance(step, torch.Tensor):
+        args.step_device = _scalar(step, "step", torch.int64, device)
+    else:
+        args.step = step
+    if args.lr_device or args.step_device:
+        workspace = torch.empty(16, dtype=torch.uint8, device=device)
+    words = [w for t in zip(p_at, g_at, m_at, v_at, m_exps, v_exps, sizes) for w in t]
+    check(lib().gqs_adamw((ctypes.c_uint64 * len(words))(*words), len(sizes),
+                          _dtype(p_type, "params"), _dtype(g_type, "grads"), args,
+                          None if workspace is None else workspace.data_ptr(), 16,
+                          _current(device)))
+
+
+def gqs_moment8_restore(moment: Moment8, dtype=torch.bfloat16, *, stream=None) -> torch.Tensor:
+    """The values a moment stands for, [n] (exact in either dtype)."""
+    dt = _dtype(dtype, "dtype")
+    if not isinstance(moment, Moment8) or not moment.codes.is_cuda:
+        raise ValueError("moment must be a Moment8 on a device")
+    device = moment.codes.device
+    if _elsewhere(device, stream):
+        with _Elsewhere(device, stream, _tensors_of(moment)):
+            return gqs_moment8_restore(moment, dtype)
+    second = moment.second
+    _, (codes,), (exps,) = _moments([moment], "moment", [moment.n], device, second)
+    out = torch.empty(moment.n, dtype=dtype, device=device)
+    check(lib().gqs_moment8_restore(codes, exps, moment.n, second, dt, out.data_ptr(),
+                                    _current(device)))
+    return out
+
+
+def gqs_grad_norm(grads, *, max_norm=None, stream=None):
+    """(norm, scale) over a list of contiguous gradients of one dtype on one
+    device, both fp32 device tensors of one element: their 2-norm, summed in
+    fp64, and with `max_norm` the factor min(1, max_norm / (norm + 1e-6)) that
+    clips them (None without), which gqs_adamw reads where it is."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grads is empty")
+    device = _device_of(grads, "grads")
+    if _elsewhere(device, stream):
+        with _Elsewhere(device, stream, grads):
+            return gqs_grad_norm(grads, max_norm=max_norm)
+    kind, sizes, at = _arrays(grads, "grads", device)
+    words = [w for g, n in zip(at, sizes) for w in (0, g, 0, 0, 0, 0, n)]
+    tensors = (ctypes.c_uint64 * len(words))(*words)
+    need = lib().gqs_grad_norm_workspace_bytes(tensors, len(sizes))
+    workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    out = torch.empty(2, dtype=torch.float32, device=device)
+    norm, scale = out[0], out[1] if max_norm is not None else None
+    check(lib().gqs_grad_norm(tensors, len(sizes), _dtype(kind, "grads"),
+                              0.0 if max_norm is None else max_norm, norm.data_ptr(),
+                              None if scale is None else scale.data_ptr(), workspace.data_ptr(),
+                              max(need, 0), _current(device)))
+    return norm, scale
