@@ -169,7 +169,12 @@ __global__ __launch_bounds__(kThreads) void k_fp8_restore(const uint8_t *__restr
 // fragment stands for: with F fragments it is row F (l % 16) + i for fragment
 // i, which puts a lane's exponent bytes, and its columns of y, side by side.
 
+#define GQT_INLINE __attribute__((always_inline))
+
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef u32x2 u32x2_e2 __attribute__((aligned(2)));
+typedef u32x2 u32x2_e4 __attribute__((aligned(4)));
+typedef uint32_t u32_e2 __attribute__((aligned(2)));
 typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 struct Operand {
@@ -308,7 +313,7 @@ struct Product {
 // blocks in turn and add their sums in LDS.  Fragments come straight from
 // memory.  MADE: x's copy is made on the way (FM = 1).
 template <typename T, int FM, int FN, bool MADE>
-__global__ __launch_bounds__(1024) void k_product_split(const Product a, T *__restrict__ y)
+__global__ __launch_bounds__(FM * FN >= 16 ? 512 : 1024) void k_product_split(const Product a, T *__restrict__ y)
 {
     constexpr bool kExact = sizeof(T) == 4;
     extern __shared__ __align__(16) float sums[];
@@ -399,6 +404,279 @@ __global__ __launch_bounds__(1024) void k_product_split(const Product a, T *__re
 }
 
 // ---------------------------------------------------------------------------
+// The tiled product: four waves hold 2 x 2 parts of a tile of y, each FM x FN
+// fragments of 32 x 32 sums; steps of 128 columns of both operands come
+// through LDS, written there by the loads themselves, and are multiplied in
+// two halves (an MFMA of 32 x 32 x 64 takes 32 values a lane).
+//
+// With F fragments, row F (l % 32) + i of a wave's rows belongs to fragment i.
+// Sixteen-byte pieces of a row of 128 are stored at their number xor that of
+// the row (of its F) modulo 8, so that the lanes of a fragment's read, F rows
+// apart, take turns at the banks.
+
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+template <int F>
+struct Panel { // 64 F rows of an operand's step
+    static constexpr int kRows = 64 * F, kBytes = kRows * 128, kLoads = 2 * F;
+
+    // Where this lane's pieces of the wave's loads lie, as offsets from the
+    // panel's first row; rows past the last are the last.
+    static __device__ __forceinline__ void offsets(uint32_t (&at)[kLoads], int wave, int lane,
+                                                   int64_t rows_left, int64_t pitch)
+    {
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) {
+            const int row = 8 * (kLoads * wave + q) + lane / 8;
+            const int piece = (lane & 7) ^ (row / F & 7);
+            at[q] = (uint32_t)(min((int64_t)row, rows_left - 1) * pitch) + 16 * piece;
+        }
+    }
+
+    // Enqueues this wave's share of a step into `to`, its part of the panel.
+    // In assembly, for the compiler makes every read of LDS wait for such
+    // loads, into whichever panel they go; land() waits for them.
+    static __device__ __forceinline__ void load(uint32_t to, const u32x4 &from,
+                                                const uint32_t (&at)[kLoads], int32_t step)
+    {
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q)
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
+                         "buffer_load_dwordx4 %1, %2, %3 offen lds"
+                         :
+                         : "s"(to + 1024 * q), "v"(at[q]), "s"(from), "s"(128 * step)
+                         : "memory", "m0");
+    }
+
+    // Half u of fragment i, `row` being the first of this lane's F rows.
+    static __device__ __forceinline__ i32x8 fragment(const uint8_t *row, int u, int i, int lane)
+    {
+        const int piece = 4 * u + 2 * (lane >> 5), turn = lane & 7;
+        const u32x4 a = *reinterpret_cast<const u32x4 *>(row + 128 * i + 16 * (piece ^ turn));
+        const u32x4 b = *reinterpret_cast<const u32x4 *>(row + 128 * i + 16 * ((piece + 1) ^ turn));
+        i32x8 f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            f[k] = (int)a[k];
+            f[4 + k] = (int)b[k];
+        }
+        return f;
+    }
+};
+
+// Waits until all this block's loads into LDS have landed and all its reads
+// of LDS so far are done.
+__device__ __forceinline__ void land()
+{
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+}
+
+// The descriptor of `rows` rows of `pitch` bytes from p on, 2^30 bytes at most.
+__device__ __forceinline__ u32x4 rows_at(const uint8_t *p, int64_t rows, int64_t pitch)
+{
+    const uint64_t at = (uint64_t)p;
+    return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32)),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(rows * pitch)), 0x00020000u};
+}
+
+// Where block t of a grid of tiles works: each XCD takes a contiguous run,
+// and runs go down groups of kGroup tiles before they go across, so that the
+// blocks at work on an XCD share rows and columns in its L2.
+constexpr int kGroup = 8;
+__device__ __forceinline__ void tile_of(int32_t block, int32_t tiles_m, int32_t tiles_n,
+                                        int32_t &tm, int32_t &tn)
+{
+    const int32_t total = tiles_m * tiles_n;
+    const int32_t xcd = block % 8, q = total / 8, rem = total % 8;
+    const int32_t t = xcd * q + min(xcd, rem) + block / 8;
+    const int32_t wide = kGroup * tiles_n;
+    const int32_t first = t / wide * kGroup, high = min(tiles_m - first, kGroup);
+    tm = first + t % wide % high;
+    tn = t % wide / high;
+}
+
+// N consecutive results of a row, of which `left` exist.
+template <int N>
+__device__ __forceinline__ void store_row(bf16 *p, const float (&v)[N], int32_t left)
+{
+    if (left >= N) {
+        uint32_t w[N / 2];
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) {
+            const bf16x2 h = {(bf16)v[2 * k], (bf16)v[2 * k + 1]};
+            w[k] = __builtin_bit_cast(uint32_t, h);
+        }
+        if constexpr (N == 4)
+            *reinterpret_cast<u32x2_e2 *>(p) = u32x2{w[0], w[1]};
+        else
+            *reinterpret_cast<u32_e2 *>(p) = w[0];
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if (k < left)
+            p[k] = (bf16)v[k];
+}
+template <int N>
+__device__ __forceinline__ void store_row(float *p, const float (&v)[N], int32_t left)
+{
+    if (left >= N) {
+        if constexpr (N == 4)
+            *reinterpret_cast<u32x4_e4 *>(p) =
+                u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3])};
+        else
+            *reinterpret_cast<u32x2_e4 *>(p) = u32x2{__float_as_uint(v[0]), __float_as_uint(v[1])};
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if (k < left)
+            p[k] = v[k];
+}
+
+template <typename T, int FM, int FN>
+__global__ __launch_bounds__(kThreads, FM * FN >= 8 ? 1 : 2) void k_product_tile(
+    const Product a, int32_t tiles_m, T *__restrict__ y)
+{
+    constexpr bool kExact = sizeof(T) == 4;
+    constexpr int kX = Panel<FM>::kBytes, kW = Panel<FN>::kBytes, kTurns = 2 * FM;
+    extern __shared__ __align__(1024) uint8_t lds[]; // two panels of x, two of w
+    const int lane = threadIdx.x & 63, r = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    int32_t tm, tn;
+    tile_of(blockIdx.x, tiles_m, a.tiles_n, tm, tn);
+    const int64_t row0 = (int64_t)tm * 64 * FM;
+    const int32_t col0 = tn * 64 * FN;
+    const int64_t rows_left = a.m - row0, cols_left = a.cols - col0;
+
+    uint32_t x_at[Panel<FM>::kLoads], w_at[Panel<FN>::kLoads];
+    Panel<FM>::offsets(x_at, wave, lane, rows_left, a.x.pitch);
+    Panel<FN>::offsets(w_at, wave, lane, cols_left, a.w.pitch);
+    const u32x4 x_rsrc =
+        rows_at(a.x.codes + row0 * a.x.pitch, min(rows_left, (int64_t)64 * FM), a.x.pitch);
+    const u32x4 w_rsrc =
+        rows_at(a.w.codes + col0 * a.w.pitch, min(cols_left, (int64_t)64 * FN), a.w.pitch);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8 *)lds;
+    const uint32_t x_to = lds0 + wave * (kX / 4), w_to = lds0 + 2 * kX + wave * (kW / 4);
+    const uint8_t *const xs = lds + (32 * FM * wm + FM * r) * 128;
+    const uint8_t *const ws = lds + 2 * kX + (32 * FN * wn + FN * r) * 128;
+    // rows past the last have no bytes of their own: they are not stored
+    const uint8_t *const ep = a.x.exps + min(row0 + 32 * FM * wm + FM * r, a.epitch - FM);
+    const int32_t w_block = min((col0 + 32 * FN * wn) >> 7, (a.cols - 1) >> 7);
+    const int32_t last = a.blocks - 1;
+
+    f32x16 acc[FM][FN] = {};
+    // x's fragments in turn, w's of a step's first and second half
+    i32x8 fx[3], fw[2][FN];
+    uint32_t ex[FM], ew, next_ex[FM], next_ew;
+
+    Panel<FM>::load(x_to, x_rsrc, x_at, 0);
+    Panel<FN>::load(w_to, w_rsrc, w_at, 0);
+    Panel<FM>::load(x_to + kX, x_rsrc, x_at, min(1, last));
+    Panel<FN>::load(w_to + kW, w_rsrc, w_at, min(1, last));
+    load_bytes<FM>(ep, ex);
+    ew = a.squares.at(w_block, 0);
+    land();
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+        fw[0][j] = Panel<FN>::fragment(ws, 0, j, lane);
+    fx[0] = Panel<FM>::fragment(xs, 0, 0, lane);
+
+    for (int32_t s = 0; s <= last; ++s) {
+        const uint8_t *const x_now = xs + (s & 1) * kX, *const x_next = xs + (~s & 1) * kX;
+        const uint8_t *const w_now = ws + (s & 1) * kW, *const w_next = ws + (~s & 1) * kW;
+        bf16x8 wide[kExact ? FN : 1][4];
+        // Turn t multiplies fragment t % FM of half t / FM, while those of the
+        // turns behind it are read.  Before the last two all of this step has
+        // been read, and all of the next has landed; where this one lay goes
+        // the one after.
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t) {
+            const int u = t / FM, i = t % FM;
+            if (t == kTurns - 2) {
+                land();
+                if (s + 2 <= last) {
+                    Panel<FM>::load(x_to + (s & 1) * kX, x_rsrc, x_at, s + 2);
+                    Panel<FN>::load(w_to + (s & 1) * kW, w_rsrc, w_at, s + 2);
+                }
+            }
+            if (t < kTurns - 3)
+                fx[(t + 1) & 1] = Panel<FM>::fragment(x_now, (t + 1) / FM, (t + 1) % FM, lane);
+            if (t == kTurns - 3) {
+                fx[0] = Panel<FM>::fragment(x_now, 1, FM - 2, lane);
+                fx[2] = Panel<FM>::fragment(x_now, 1, FM - 1, lane);
+            }
+            if (t == kTurns - 1)
+                fx[0] = Panel<FM>::fragment(x_next, 0, 0, lane);
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                if (t == j * FM / FN)
+                    fw[1][j] = Panel<FN>::fragment(w_now, 1, j, lane);
+                if (t == kTurns - 2 + 2 * j / FN)
+                    fw[0][j] = Panel<FN>::fragment(w_next, 0, j, lane);
+            }
+            if (t == 0) {
+                const int32_t n = min(s + 1, last);
+                load_bytes<FM>(ep + n * a.epitch, next_ex);
+                next_ew = a.squares.at(w_block, n);
+            }
+            const i32x8 &x = fx[t == kTurns - 1 ? 2 : t & 1];
+            if constexpr (kExact) {
+                if (i == 0) {
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+#pragma unroll
+                        for (int part = 0; part < 4; ++part)
+                            wide[j][part] = widen(fw[u][j], part, step_of(ew));
+                }
+#pragma unroll
+                for (int part = 0; part < 4; ++part) {
+                    const bf16x8 bx = widen(x, part, step_of(ex[i]));
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bx, wide[j][part],
+                                                                            acc[i][j], 0, 0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        x, fw[u][j], acc[i][j], 0, 0, 0, (int)ex[i], 0, (int)ew);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            ex[i] = next_ex[i];
+        ew = next_ew;
+    }
+
+    const int32_t col = col0 + 32 * FN * wn + FN * r;
+    float bias[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+        bias[j] = a.bias && col + j < a.cols ? bias_at(a.bias, a.bias_dtype, col + j) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+            const int of = 8 * (q / 4) + 4 * (lane >> 5) + q % 4;
+            const int64_t row = row0 + 32 * FM * wm + FM * of + i;
+            float v[FN];
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                v[j] = acc[i][j][q] + bias[j];
+            if (row < a.m)
+                store_row<FN>(y + row * a.cols + col, v, a.cols - col);
+        }
+}
+
+// ---------------------------------------------------------------------------
 // host
 
 int32_t check_sides(int32_t dtype, int64_t rows, int64_t d)
@@ -464,6 +742,17 @@ int32_t launch_rows(const void *x, int32_t dtype, int64_t rows, int64_t d, int64
     return check_launch("k_fp8_rows");
 }
 
+// Lets a kernel have more than 64 KB of LDS.
+template <typename K>
+int32_t allow_lds(K *kernel, const char *name, uint32_t bytes)
+{
+    if (bytes <= 65536)
+        return GQ_OK;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    return e == hipSuccess ? GQ_OK : fail(GQ_ERR_DEVICE, "%s: %s", name, hipGetErrorString(e));
+}
+
 template <typename T, int FM, int FN, bool MADE>
 int32_t launch_split(Product a, T *y, hipStream_t st)
 {
@@ -473,15 +762,23 @@ int32_t launch_split(Product a, T *y, hipStream_t st)
     const uint32_t lds = (uint32_t)waves * FM * FN * 1024;
     if (grid >= ((int64_t)1 << 31) / (64 * 16))
         return fail(GQ_ERR_UNSUPPORTED, "%lld tiles", (long long)grid);
-    if (lds > 65536) {
-        const hipError_t e = hipFuncSetAttribute(
-            reinterpret_cast<const void *>(&k_product_split<T, FM, FN, MADE>),
-            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-        if (e != hipSuccess)
-            return fail(GQ_ERR_DEVICE, "k_product_split: %s", hipGetErrorString(e));
-    }
+    GQT_TRY(allow_lds(&k_product_split<T, FM, FN, MADE>, "k_product_split", lds));
     k_product_split<T, FM, FN, MADE><<<(uint32_t)grid, 64 * waves, lds, st>>>(a, y);
     return check_launch("k_product_split");
+}
+
+template <typename T, int FM, int FN>
+int32_t launch_tile(Product a, T *y, hipStream_t st)
+{
+    const int64_t tiles_m = (a.m + 64 * FM - 1) / (64 * FM);
+    a.tiles_n = (a.cols + 64 * FN - 1) / (64 * FN);
+    if (tiles_m * a.tiles_n >= ((int64_t)1 << 31) / kThreads)
+        return fail(GQ_ERR_UNSUPPORTED, "%lld tiles", (long long)(tiles_m * a.tiles_n));
+    constexpr uint32_t kLds = 2 * (Panel<FM>::kBytes + Panel<FN>::kBytes);
+    GQT_TRY(allow_lds(&k_product_tile<T, FM, FN>, "k_product_tile", kLds));
+    k_product_tile<T, FM, FN><<<(uint32_t)(tiles_m * a.tiles_n), kThreads, kLds, st>>>(
+        a, (int32_t)tiles_m, y);
+    return check_launch("k_product_tile");
 }
 
 template <typename T>
@@ -495,6 +792,13 @@ int32_t launch_product(const Product &a, void *y, hipStream_t st)
         return launch_split<T, 2, 1, false>(a, out, st);
     if (a.m <= 64)
         return launch_split<T, 4, 2, false>(a, out, st);
+    const int64_t squares = ((a.m + 127) / 128) * ((a.cols + 127) / 128);
+    if (squares >= 64) {
+        if constexpr (sizeof(T) == 2)
+            if (squares >= 1024)
+                return launch_tile<T, 4, 4>(a, out, st);
+        return launch_tile<T, 2, 2>(a, out, st);
+    }
     return launch_split<T, 8, 2, false>(a, out, st);
 }
 
