@@ -19,14 +19,16 @@ constexpr int kRowBlocks = 4; // of a thread: as many loads in flight
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_fp8_rows(const T *__restrict__ x, int64_t rows,
                                                        int32_t d, int64_t ldx, int32_t random,
-                                                       uint32_t k0, uint32_t k1, uint32_t across,
+                                                       uint32_t k0, uint32_t k1, FastDiv across,
                                                        int64_t epitch, uint8_t *__restrict__ codes,
                                                        uint8_t *__restrict__ exps)
 {
-    const int64_t row = (int64_t)(blockIdx.x / across) * 16 + threadIdx.x / 16;
+    const uint32_t down = divide(blockIdx.x, across);
+    const int64_t row = (int64_t)down * 16 + threadIdx.x / 16;
     if (row >= rows)
         return; // whole blocks of sixteen lanes
-    const int32_t first = blockIdx.x % across * kRowBlocks * 128 + threadIdx.x % 16 * 8;
+    const int32_t first =
+        (blockIdx.x - down * across.d) * kRowBlocks * 128 + threadIdx.x % 16 * 8;
     const int32_t pitch = (d + 127) / 128 * 128;
     const T *const p = x + row * ldx;
     float v[kRowBlocks][8];
@@ -142,15 +144,15 @@ __global__ __launch_bounds__(kThreads) void k_fp8_weight(const T *__restrict__ w
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_fp8_restore(const uint8_t *__restrict__ codes,
                                                           const uint8_t *__restrict__ exps,
-                                                          uint32_t chunks, uint32_t per_row,
+                                                          uint32_t chunks, FastDiv per_row,
                                                           int32_t d, int32_t squares,
                                                           int64_t epitch, T *__restrict__ out)
 {
     const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
     if (i >= chunks)
         return;
-    const uint32_t row = i / per_row;
-    const int32_t col = 8 * (i % per_row);
+    const uint32_t row = divide(i, per_row);
+    const int32_t col = 8 * (i - row * per_row.d);
     const int64_t block = col >> 7;
     const uint8_t e = squares ? exps[(row >> 7) * epitch + block] : exps[block * epitch + row];
     const int64_t pitch = (d + 127) / 128 * 128;
@@ -224,41 +226,47 @@ __device__ __forceinline__ bf16x8 widen(const i32x8 &f, int part, float step)
     return r;
 }
 
-// N bytes from p on (N = 1, 2, 4 or 8).
+// N exponent bytes side by side.
 template <int N>
-__device__ __forceinline__ void load_bytes(const uint8_t *p, uint32_t (&b)[N])
-{
-    if constexpr (N == 8) {
-        const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            b[k] = w[k >> 2] >> (8 * (k & 3)) & 0xFFu;
-    } else if constexpr (N == 4) {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            b[k] = w >> (8 * k) & 0xFFu;
-    } else if constexpr (N == 2) {
-        const uint32_t w = *reinterpret_cast<const uint16_t *>(p);
-        b[0] = w & 0xFFu;
-        b[1] = w >> 8;
-    } else {
-        b[0] = *p;
+struct Bytes;
+template <>
+struct Bytes<1> {
+    uint8_t b;
+    __device__ __forceinline__ uint32_t byte(int) const { return b; }
+};
+template <>
+struct Bytes<2> {
+    uint16_t b;
+    __device__ __forceinline__ uint32_t byte(int i) const { return b >> (8 * i) & 0xFFu; }
+};
+template <>
+struct Bytes<4> {
+    uint32_t b;
+    __device__ __forceinline__ uint32_t byte(int i) const { return b >> (8 * i) & 0xFFu; }
+};
+template <>
+struct Bytes<8> {
+    u32x2 b;
+    __device__ __forceinline__ uint32_t byte(int i) const
+    {
+        return b[i >> 2] >> (8 * (i & 3)) & 0xFFu;
     }
-}
+};
 
-// Row r's 32 columns from `col` on of x as its copy holds them, made here:
-// lanes r, r + 16, r + 32 and r + 48 have the block's four parts.
+// Row `row`'s 32 columns from `col` on of x as its copy holds them, made of
+// what load_ahead read: lanes r, r + 16, r + 32 and r + 48 have the block's
+// four parts.
 template <typename T>
-__device__ __forceinline__ i32x8 make_fragment(const T *p, int32_t row, int32_t col, int32_t d,
-                                               int32_t random, uint32_t k0, uint32_t k1,
-                                               uint32_t &e)
+__device__ __forceinline__ i32x8 make_fragment(Raw8<T> (&raw)[4], const T *p, int32_t row,
+                                               int32_t col, int32_t d, int32_t random, uint32_t k0,
+                                               uint32_t k1, uint32_t &e)
 {
     float v[4][8];
     uint32_t m = 0;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        load8(p, col + 8 * q, d, v[q]);
+        settle(p, col + 8 * q, d, raw[q]);
+        unpack(raw[q], v[q]);
         m = max(m, abs_bits(v[q]));
     }
     m = max(m, (uint32_t)__shfl_xor((int)m, 16));
@@ -298,7 +306,10 @@ struct Product {
     Squares squares;
     const void *bias;
     int32_t bias_dtype;
-    int32_t tiles_n; // tiles along the columns
+    uint32_t tiles_m;                      // tiles along the rows
+    FastDiv by_tiles, by_group, by_rest;   // all, those of kGroup rows, rows of the last group
+    int32_t splits, steps;    // parts of the depth, and blocks of one
+    float *parts;             // where they leave their sums [splits][m][cols]
     // x as its row copy
     Operand x;
     int64_t epitch;
@@ -313,14 +324,15 @@ struct Product {
 // blocks in turn and add their sums in LDS.  Fragments come straight from
 // memory.  MADE: x's copy is made on the way (FM = 1).
 template <typename T, int FM, int FN, bool MADE>
-__global__ __launch_bounds__(FM * FN >= 16 ? 512 : 1024) void k_product_split(const Product a, T *__restrict__ y)
+__global__ __launch_bounds__(FM * FN >= 8 ? 512 : 1024) void k_product_split(const Product a, T *__restrict__ y)
 {
     constexpr bool kExact = sizeof(T) == 4;
     extern __shared__ __align__(16) float sums[];
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-    const int32_t col0 = (int32_t)(blockIdx.x % a.tiles_n) * 16 * FN;
-    const int64_t row0 = (int64_t)(blockIdx.x / a.tiles_n) * 16 * FM;
+    const uint32_t tm = divide(blockIdx.x, a.by_tiles);
+    const int32_t col0 = (int32_t)(blockIdx.x - tm * a.by_tiles.d) * 16 * FN;
+    const int64_t row0 = (int64_t)tm * 16 * FM;
     const uint8_t *xp[FM], *wp[FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -333,32 +345,48 @@ __global__ __launch_bounds__(FM * FN >= 16 ? 512 : 1024) void k_product_split(co
     // a tile's last rows may have no bytes: they are not stored, and read others'
     const uint8_t *const ep = MADE ? nullptr : a.x.exps + min(row0 + FM * r, a.epitch - FM);
     f32x4 acc[FM][FN] = {};
-    for (int32_t s = wave; s < a.blocks; s += waves) {
+    struct Step {
         i32x8 fx[FM], fw[FN];
-        uint32_t ex[FM];
+        Raw8<T> raw[4];
+        Bytes<FM> ex;
+        uint32_t ew;
+    };
+    const auto fetch = [&](Step &k, int32_t s) GQT_INLINE {
         if constexpr (MADE) {
-            fx[0] = make_fragment(raw, (int32_t)made_row, 128 * s + 32 * g, a.depth, a.random,
-                                  a.k0, a.k1, ex[0]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                load_ahead(raw, 128 * s + 32 * g + 8 * q, a.depth, k.raw[q]);
         } else {
 #pragma unroll
             for (int i = 0; i < FM; ++i)
-                fx[i] = load_fragment(xp[i] + 128 * (int64_t)s);
-            load_bytes<FM>(ep + s * a.epitch, ex);
+                k.fx[i] = load_fragment(xp[i] + 128 * (int64_t)s);
+            k.ex = *reinterpret_cast<const Bytes<FM> *>(ep + s * a.epitch);
         }
 #pragma unroll
         for (int j = 0; j < FN; ++j)
-            fw[j] = load_fragment(wp[j] + 128 * (int64_t)s);
-        const uint32_t ew = a.squares.at(col0 >> 7, s);
+            k.fw[j] = load_fragment(wp[j] + 128 * (int64_t)s);
+        k.ew = a.squares.at(col0 >> 7, s);
+    };
+    const auto multiply = [&](Step &k, int32_t s) GQT_INLINE {
+        uint32_t ex[FM];
+        if constexpr (MADE) {
+            k.fx[0] = make_fragment(k.raw, raw, (int32_t)made_row, 128 * s + 32 * g, a.depth,
+                                    a.random, a.k0, a.k1, ex[0]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+                ex[i] = k.ex.byte(i);
+        }
         if constexpr (kExact) {
 #pragma unroll
             for (int part = 0; part < 4; ++part) {
                 bf16x8 bw[FN];
 #pragma unroll
                 for (int j = 0; j < FN; ++j)
-                    bw[j] = widen(fw[j], part, step_of(ew));
+                    bw[j] = widen(k.fw[j], part, step_of(k.ew));
 #pragma unroll
                 for (int i = 0; i < FM; ++i) {
-                    const bf16x8 bx = widen(fx[i], part, step_of(ex[i]));
+                    const bf16x8 bx = widen(k.fx[i], part, step_of(ex[i]));
 #pragma unroll
                     for (int j = 0; j < FN; ++j)
                         acc[i][j] =
@@ -371,7 +399,21 @@ __global__ __launch_bounds__(FM * FN >= 16 ? 512 : 1024) void k_product_split(co
 #pragma unroll
                 for (int j = 0; j < FN; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        fx[i], fw[j], acc[i][j], 0, 0, 0, (int)ex[i], 0, (int)ew);
+                        k.fx[i], k.fw[j], acc[i][j], 0, 0, 0, (int)ex[i], 0, (int)k.ew);
+        }
+    };
+    // The next of the wave's blocks is on its way while one is multiplied.
+    Step one, two;
+    if (wave < a.blocks)
+        fetch(one, wave);
+    for (int32_t s = wave; s < a.blocks; s += 2 * waves) {
+        if (s + waves < a.blocks)
+            fetch(two, s + waves);
+        multiply(one, s);
+        if (s + waves < a.blocks) {
+            if (s + 2 * waves < a.blocks)
+                fetch(one, s + 2 * waves);
+            multiply(two, s + waves);
         }
     }
     // sums[wave][i][q][lane][j]
@@ -404,57 +446,91 @@ __global__ __launch_bounds__(FM * FN >= 16 ? 512 : 1024) void k_product_split(co
 }
 
 // ---------------------------------------------------------------------------
-// The tiled product: four waves hold 2 x 2 parts of a tile of y, each FM x FN
-// fragments of 32 x 32 sums; steps of 128 columns of both operands come
-// through LDS, written there by the loads themselves, and are multiplied in
-// two halves (an MFMA of 32 x 32 x 64 takes 32 values a lane).
+// The tiled product: WM x WN waves hold as many parts of a tile of y, each FM x
+// FN fragments of 32 x 32 sums.  Steps of 128 columns of both operands come
+// through LDS, written there by the loads themselves, STAGES - 1 steps ahead,
+// and are multiplied in two halves (an MFMA of 32 x 32 x 64 takes 32 values a
+// lane).  A block goes from tile to tile without a pause in its loads.
 //
 // With F fragments, row F (l % 32) + i of a wave's rows belongs to fragment i.
-// Sixteen-byte pieces of a row of 128 are stored at their number xor that of
-// the row (of its F) modulo 8, so that the lanes of a fragment's read, F rows
-// apart, take turns at the banks.
+// LDS gives 256 bytes a cycle, sixteen lanes their sixteen bytes.  A lane's F
+// rows lie in F lines of 128 bytes, for the second eight of sixteen lanes with
+// neighbours changed about, and a row's sixteen-byte pieces at their number xor
+// the lane's modulo 8, so that the lanes of a fragment's read find all banks.
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-template <int F>
-struct Panel { // 64 F rows of an operand's step
-    static constexpr int kRows = 64 * F, kBytes = kRows * 128, kLoads = 2 * F;
+// Loads from memory to LDS: `to` and what follows it for the other lanes.  In
+// assembly, for the compiler makes every read of LDS wait for such loads,
+// wherever they go, and does not count others behind them; land() waits.
+// Lanes past the descriptor's end give zeros.
+__device__ __forceinline__ void load_lds16(uint32_t to, const u32x4 &from, uint32_t at, uint32_t base)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(to), "v"(at), "s"(from), "s"(base) : "memory");
+}
+__device__ __forceinline__ void load_lds4(uint32_t to, const u32x4 &from, uint32_t at, uint32_t base)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                 :: "s"(to), "v"(at), "s"(from), "s"(base) : "memory");
+}
+__device__ __forceinline__ void load_lds1(uint32_t to, const u32x4 &from, uint32_t at, uint32_t base)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, %3 offen lds"
+                 :: "s"(to), "v"(at), "s"(from), "s"(base) : "memory");
+}
 
-    // Where this lane's pieces of the wave's loads lie, as offsets from the
-    // panel's first row; rows past the last are the last.
+// Until all but the last LEFT of this wave's loads have landed, and all waves
+// are here with their reads of LDS done.
+template <int LEFT>
+__device__ __forceinline__ void land()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
+}
+
+__device__ __forceinline__ u32x4 descriptor(const uint8_t *p, uint32_t bytes)
+{
+    const uint64_t at = (uint64_t)p;
+    return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32)),
+                 (uint32_t)__builtin_amdgcn_readfirstlane(bytes), 0x00020000u};
+}
+
+template <int F, int ROWS, int WAVES>
+struct Panel { // an operand's step
+    static constexpr int kBytes = ROWS * 128, kLoads = ROWS / 8 / WAVES;
+
+    // What the lane of rows F r on does to its lines' and pieces' numbers.
+    static __device__ __forceinline__ int change(int r) { return F > 1 ? r >> 3 & 1 : 0; }
+    static __device__ __forceinline__ int turn(int r) { return F > 1 ? r & 7 : r >> 1 & 7; }
+
+    // Where this lane's pieces of the wave's loads lie, from the first row on.
     static __device__ __forceinline__ void offsets(uint32_t (&at)[kLoads], int wave, int lane,
-                                                   int64_t rows_left, int64_t pitch)
+                                                   int64_t pitch)
     {
 #pragma unroll
         for (int q = 0; q < kLoads; ++q) {
-            const int row = 8 * (kLoads * wave + q) + lane / 8;
-            const int piece = (lane & 7) ^ (row / F & 7);
-            at[q] = (uint32_t)(min((int64_t)row, rows_left - 1) * pitch) + 16 * piece;
+            const int line = 8 * (kLoads * wave + q) + lane / 8;
+            const int row = line ^ change(line / F), piece = (lane & 7) ^ turn(line / F);
+            at[q] = (uint32_t)(row * pitch) + 16 * piece;
         }
     }
 
-    // Enqueues this wave's share of a step into `to`, its part of the panel.
-    // In assembly, for the compiler makes every read of LDS wait for such
-    // loads, into whichever panel they go; land() waits for them.
-    static __device__ __forceinline__ void load(uint32_t to, const u32x4 &from,
-                                                const uint32_t (&at)[kLoads], int32_t step)
+    // Where this lane's F lines begin, with its turn: what to xor for a piece.
+    static __device__ __forceinline__ uint32_t lines(int half, int lane)
     {
-#pragma unroll
-        for (int q = 0; q < kLoads; ++q)
-            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
-                         "buffer_load_dwordx4 %1, %2, %3 offen lds"
-                         :
-                         : "s"(to + 1024 * q), "v"(at[q]), "s"(from), "s"(128 * step)
-                         : "memory", "m0");
+        const int r = lane & 31;
+        return (32 * half + r) * F * 128 + 128 * change(r) + 16 * (turn(r) ^ (lane >> 5 << 1));
     }
 
-    // Half u of fragment i, `row` being the first of this lane's F rows.
-    static __device__ __forceinline__ i32x8 fragment(const uint8_t *row, int u, int i, int lane)
+    // Half u of fragment i.
+    static __device__ __forceinline__ i32x8 fragment(uint32_t at, int u, int i)
     {
-        const int piece = 4 * u + 2 * (lane >> 5), turn = lane & 7;
-        const u32x4 a = *reinterpret_cast<const u32x4 *>(row + 128 * i + 16 * (piece ^ turn));
-        const u32x4 b = *reinterpret_cast<const u32x4 *>(row + 128 * i + 16 * ((piece + 1) ^ turn));
+        const uint32_t of = 128 * (i & 1) + 64 * u, beyond = 128 * (i & ~1);
+        const u32x4 a = *(const lds_u32x4 *)(uintptr_t)((at ^ of) + beyond);
+        const u32x4 b = *(const lds_u32x4 *)(uintptr_t)((at ^ (of + 16)) + beyond);
         i32x8 f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -465,45 +541,37 @@ struct Panel { // 64 F rows of an operand's step
     }
 };
 
-// Waits until all this block's loads into LDS have landed and all its reads
-// of LDS so far are done.
-__device__ __forceinline__ void land()
+// What work item `number` of a grid is: a tile, and a part of the depth.  Each
+// XCD takes a contiguous run, and runs go down groups of kGroup tiles before
+// they go across, so that the blocks at work on an XCD share rows and columns
+// in its L2.
+struct Item {
+    int32_t tm, tn, split, first, end; // blocks of the depth from first to end
+};
+constexpr int kGroup = 4;
+__device__ __forceinline__ Item item_of(uint32_t number, const Product &a)
 {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-}
-
-// The descriptor of `rows` rows of `pitch` bytes from p on, 2^30 bytes at most.
-__device__ __forceinline__ u32x4 rows_at(const uint8_t *p, int64_t rows, int64_t pitch)
-{
-    const uint64_t at = (uint64_t)p;
-    return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at),
-                 (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32)),
-                 (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(rows * pitch)), 0x00020000u};
-}
-
-// Where block t of a grid of tiles works: each XCD takes a contiguous run,
-// and runs go down groups of kGroup tiles before they go across, so that the
-// blocks at work on an XCD share rows and columns in its L2.
-constexpr int kGroup = 8;
-__device__ __forceinline__ void tile_of(int32_t block, int32_t tiles_m, int32_t tiles_n,
-                                        int32_t &tm, int32_t &tn)
-{
-    const int32_t total = tiles_m * tiles_n;
-    const int32_t xcd = block % 8, q = total / 8, rem = total % 8;
-    const int32_t t = xcd * q + min(xcd, rem) + block / 8;
-    const int32_t wide = kGroup * tiles_n;
-    const int32_t first = t / wide * kGroup, high = min(tiles_m - first, kGroup);
-    tm = first + t % wide % high;
-    tn = t % wide / high;
+    const uint32_t tiles = a.by_tiles.d, total = tiles * a.splits, xcd = number % 8;
+    const uint32_t at = xcd * (total / 8) + min(xcd, total % 8) + number / 8;
+    Item w;
+    w.split = (int32_t)divide(at, a.by_tiles);
+    uint32_t t = at - w.split * tiles;
+    const uint32_t group = divide(t, a.by_group), first = group * kGroup;
+    t -= group * a.by_group.d;
+    const uint32_t high = min(a.tiles_m - first, (uint32_t)kGroup);
+    w.tn = (int32_t)(high == kGroup ? t / kGroup : divide(t, a.by_rest));
+    w.tm = (int32_t)(first + t - w.tn * high);
+    w.first = w.split * a.steps;
+    w.end = min(w.first + a.steps, a.blocks);
+    return w;
 }
 
 // N consecutive results of a row, of which `left` exist.
 template <int N>
 __device__ __forceinline__ void store_row(bf16 *p, const float (&v)[N], int32_t left)
 {
-    if (left >= N) {
-        uint32_t w[N / 2];
+    if (N > 1 && left >= N) {
+        uint32_t w[(N + 1) / 2];
 #pragma unroll
         for (int k = 0; k < N / 2; ++k) {
             const bf16x2 h = {(bf16)v[2 * k], (bf16)v[2 * k + 1]};
@@ -511,7 +579,7 @@ __device__ __forceinline__ void store_row(bf16 *p, const float (&v)[N], int32_t 
         }
         if constexpr (N == 4)
             *reinterpret_cast<u32x2_e2 *>(p) = u32x2{w[0], w[1]};
-        else
+        else if constexpr (N == 2)
             *reinterpret_cast<u32_e2 *>(p) = w[0];
         return;
     }
@@ -523,12 +591,12 @@ __device__ __forceinline__ void store_row(bf16 *p, const float (&v)[N], int32_t 
 template <int N>
 __device__ __forceinline__ void store_row(float *p, const float (&v)[N], int32_t left)
 {
-    if (left >= N) {
+    if (N > 1 && left >= N) {
         if constexpr (N == 4)
             *reinterpret_cast<u32x4_e4 *>(p) =
                 u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
                       __float_as_uint(v[3])};
-        else
+        else if constexpr (N == 2)
             *reinterpret_cast<u32x2_e4 *>(p) = u32x2{__float_as_uint(v[0]), __float_as_uint(v[1])};
         return;
     }
@@ -538,142 +606,258 @@ __device__ __forceinline__ void store_row(float *p, const float (&v)[N], int32_t
             p[k] = v[k];
 }
 
-template <typename T, int FM, int FN>
-__global__ __launch_bounds__(kThreads, FM * FN >= 8 ? 1 : 2) void k_product_tile(
-    const Product a, int32_t tiles_m, T *__restrict__ y)
+// What a tile's kernel needs of LDS: STAGES of both panels and of the exponent
+// bytes, of rows first, then of squares, in words.
+template <int WM, int WN, int FM, int FN, int STAGES>
+struct Stages {
+    static constexpr int kWaves = WM * WN, kRows = 32 * FM * WM, kCols = 32 * FN * WN;
+    using X = Panel<FM, kRows, kWaves>;
+    using W = Panel<FN, kCols, kWaves>;
+    static constexpr int kPanels = X::kBytes + W::kBytes, kStage = kPanels + 512;
+    static constexpr int kLoads = X::kLoads + W::kLoads; // of a wave, panels alone
+    static constexpr uint32_t kLds = STAGES * kStage;
+};
+
+// The shapes, and what they are for; see plan_of.  PANELS: turns at the end of
+// a step that multiply what has been read already, while its panels are given
+// to later loads, and OVER: the turns over which those go out (all at once
+// they hold up the MFMAs behind them).
+template <int WM, int WN, int FM, int FN, int STAGES, int PANELS, int OVER>
+struct Shape : Stages<WM, WN, FM, FN, STAGES> {
+    static constexpr int kWM = WM, kWN = WN, kFM = FM, kFN = FN, kStages = STAGES;
+    static constexpr int kFree = PANELS, kOver = OVER;
+    static constexpr int kBlocksPerCu = WM * WN == 4 && STAGES == 2 ? 2 : 1;
+};
+
+// O: what is stored, y's type, or float where the depth is split.
+template <typename S, bool EXACT, typename O>
+__global__ __launch_bounds__(64 * S::kWaves, S::kWaves *S::kBlocksPerCu / 4) void k_product_tile(
+    const Product a, O *__restrict__ y)
 {
-    constexpr bool kExact = sizeof(T) == 4;
-    constexpr int kX = Panel<FM>::kBytes, kW = Panel<FN>::kBytes, kTurns = 2 * FM;
-    extern __shared__ __align__(1024) uint8_t lds[]; // two panels of x, two of w
+    using X = typename S::X;
+    using W = typename S::W;
+    constexpr int WN = S::kWN, FM = S::kFM, FN = S::kFN, kTurns = 2 * FM, kFree = S::kFree;
+    constexpr int kAhead = (S::kStages - 2) * S::kLoads; // may be in flight at a step's end
+    extern __shared__ __align__(1024) uint8_t lds[];
     const int lane = threadIdx.x & 63, r = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave >> 1, wn = wave & 1;
-    int32_t tm, tn;
-    tile_of(blockIdx.x, tiles_m, a.tiles_n, tm, tn);
-    const int64_t row0 = (int64_t)tm * 64 * FM;
-    const int32_t col0 = tn * 64 * FN;
-    const int64_t rows_left = a.m - row0, cols_left = a.cols - col0;
+    const int wm = wave / WN, wn = wave % WN;
+    const int32_t total = a.by_tiles.d * a.splits;
 
-    uint32_t x_at[Panel<FM>::kLoads], w_at[Panel<FN>::kLoads];
-    Panel<FM>::offsets(x_at, wave, lane, rows_left, a.x.pitch);
-    Panel<FN>::offsets(w_at, wave, lane, cols_left, a.w.pitch);
-    const u32x4 x_rsrc =
-        rows_at(a.x.codes + row0 * a.x.pitch, min(rows_left, (int64_t)64 * FM), a.x.pitch);
-    const u32x4 w_rsrc =
-        rows_at(a.w.codes + col0 * a.w.pitch, min(cols_left, (int64_t)64 * FN), a.w.pitch);
+    // What is loaded: a step of an item, and where it lies.
+    uint32_t x_at[X::kLoads], w_at[W::kLoads];
+    X::offsets(x_at, wave, lane, a.x.pitch);
+    W::offsets(w_at, wave, lane, a.w.pitch);
+    u32x4 x_from, w_from;
+    const u32x4 xe_from = descriptor(a.x.exps, 0xFFFFFFFFu);
+    const u32x4 we_from = descriptor(a.squares.exps, 0xFFFFFFFFu);
+    uint32_t e_at; // wave 0: the rows' exponents, wave 1: the squares'
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8 *)lds;
-    const uint32_t x_to = lds0 + wave * (kX / 4), w_to = lds0 + 2 * kX + wave * (kW / 4);
-    const uint8_t *const xs = lds + (32 * FM * wm + FM * r) * 128;
-    const uint8_t *const ws = lds + 2 * kX + (32 * FN * wn + FN * r) * 128;
-    // rows past the last have no bytes of their own: they are not stored
-    const uint8_t *const ep = a.x.exps + min(row0 + 32 * FM * wm + FM * r, a.epitch - FM);
-    const int32_t w_block = min((col0 + 32 * FN * wn) >> 7, (a.cols - 1) >> 7);
-    const int32_t last = a.blocks - 1;
+    int32_t number_ahead = blockIdx.x, step_ahead, end_ahead; // below 2^31 + the grid
+    uint32_t to = lds0; // the stage
+    const auto aim = [&]() GQT_INLINE {
+        const Item w = item_of(number_ahead, a);
+        const int64_t row0 = (int64_t)w.tm * S::kRows;
+        const int32_t col0 = w.tn * S::kCols;
+        const uint32_t rows = (uint32_t)min(a.m - row0, (int64_t)S::kRows);
+        const uint32_t cols = (uint32_t)min(a.cols - col0, S::kCols);
+        x_from = descriptor(a.x.codes + row0 * a.x.pitch, rows * (uint32_t)a.x.pitch);
+        w_from = descriptor(a.w.codes + col0 * a.w.pitch, cols * (uint32_t)a.w.pitch);
+        // rows past the last have no bytes of their own: they are not stored
+        e_at = wave == 0 ? (uint32_t)min(row0 + 4 * lane, a.epitch - 4)
+                         : (uint32_t)(min((col0 >> 7) + lane, (a.cols - 1) >> 7) * a.squares.by_cols);
+        step_ahead = w.first;
+        end_ahead = w.end;
+    };
+    // Loads `first` to `end` of the step's S::kLoads; two of the waves have one
+    // more.
+    const auto load = [&](int first, int end) GQT_INLINE {
+#pragma unroll
+        for (int c = 0; c < S::kLoads; ++c) {
+            if (c < first || c >= end)
+                continue;
+            if (c < X::kLoads)
+                load_lds16(to + 1024 * (X::kLoads * wave + c), x_from, x_at[c], 128 * step_ahead);
+            else
+                load_lds16(to + X::kBytes + 1024 * (W::kLoads * wave + c - X::kLoads), w_from,
+                           w_at[c - X::kLoads], 128 * step_ahead);
+        }
+    };
+    const auto load_exponents = [&]() GQT_INLINE {
+        if (wave == 0)
+            load_lds4(to + S::kPanels, xe_from, e_at, (uint32_t)(step_ahead * a.epitch));
+        else if (wave == 1)
+            load_lds1(to + S::kPanels + 256, we_from, e_at, step_ahead * a.squares.by_depth);
+    };
+    const auto advance = [&]() GQT_INLINE {
+        to = to == lds0 + (S::kStages - 1) * S::kStage ? lds0 : to + S::kStage;
+        if (++step_ahead >= end_ahead) {
+            number_ahead += gridDim.x;
+            if (number_ahead < total) {
+                aim();
+            } else { // nothing is left: zeros that nobody reads
+                x_from[2] = w_from[2] = 0;
+                step_ahead = end_ahead - 1;
+            }
+        }
+    };
 
-    f32x16 acc[FM][FN] = {};
-    // x's fragments in turn, w's of a step's first and second half
-    i32x8 fx[3], fw[2][FN];
-    uint32_t ex[FM], ew, next_ex[FM], next_ew;
+    // What is read: the places of this lane's lines and bytes in a stage.
+    const uint32_t xs = lds0 + X::lines(wm, lane), ws = lds0 + X::kBytes + W::lines(wn, lane);
+    const uint8_t *const xe = lds + S::kPanels + 32 * FM * wm + FM * r;
+    const uint8_t *const we = lds + S::kPanels + 256 + 4 * (32 * FN * wn >> 7);
+    constexpr int kRing = kFree == 2 ? 3 : 2;
+    i32x8 fx[kRing], fw[2][FN]; // x's fragments in turn, w's of the two halves
+    Bytes<FM> ex;
+    uint32_t ew;
 
-    Panel<FM>::load(x_to, x_rsrc, x_at, 0);
-    Panel<FN>::load(w_to, w_rsrc, w_at, 0);
-    Panel<FM>::load(x_to + kX, x_rsrc, x_at, min(1, last));
-    Panel<FN>::load(w_to + kW, w_rsrc, w_at, min(1, last));
-    load_bytes<FM>(ep, ex);
-    ew = a.squares.at(w_block, 0);
-    land();
+    constexpr auto share = [](int turn) { // loads that have gone out before a turn
+        return std::min(S::kLoads * turn / S::kOver, S::kLoads);
+    };
+    aim();
+#pragma unroll
+    for (int s = 0; s < S::kStages; ++s) {
+        load_exponents();
+        load(0, s < S::kStages - 1 ? S::kLoads : share(kFree));
+        if (s < S::kStages - 1)
+            advance();
+    }
+    land<kAhead + share(kFree)>();
 #pragma unroll
     for (int j = 0; j < FN; ++j)
-        fw[0][j] = Panel<FN>::fragment(ws, 0, j, lane);
-    fx[0] = Panel<FM>::fragment(xs, 0, 0, lane);
+        fw[0][j] = W::fragment(ws, 0, j);
+    fx[0] = X::fragment(xs, 0, 0);
+    ex = *reinterpret_cast<const Bytes<FM> *>(xe);
+    ew = *reinterpret_cast<const uint32_t *>(we);
+    uint32_t now = 0; // the stage
 
-    for (int32_t s = 0; s <= last; ++s) {
-        const uint8_t *const x_now = xs + (s & 1) * kX, *const x_next = xs + (~s & 1) * kX;
-        const uint8_t *const w_now = ws + (s & 1) * kW, *const w_next = ws + (~s & 1) * kW;
-        bf16x8 wide[kExact ? FN : 1][4];
-        // Turn t multiplies fragment t % FM of half t / FM, while those of the
-        // turns behind it are read.  Before the last two all of this step has
-        // been read, and all of the next has landed; where this one lay goes
-        // the one after.
+    for (int32_t number = blockIdx.x; number < total; number += gridDim.x) {
+        const Item w = item_of(number, a);
+        f32x16 acc[FM][FN] = {};
+        for (int32_t s = w.first; s < w.end; ++s) {
+            const uint32_t next = now == (S::kStages - 1) * S::kStage ? 0 : now + S::kStage;
+            Bytes<FM> next_ex;
+            uint32_t next_ew;
+            bf16x8 wide[EXACT ? FN : 1][4];
+            // Turn t multiplies fragment t % FM of half t / FM, while those of
+            // the turns behind it are read.  Before the last kFree all of this
+            // step has been read, and all of the next has landed; where this
+            // one lay goes the one kStages after.
 #pragma unroll
-        for (int t = 0; t < kTurns; ++t) {
-            const int u = t / FM, i = t % FM;
-            if (t == kTurns - 2) {
-                land();
-                if (s + 2 <= last) {
-                    Panel<FM>::load(x_to + (s & 1) * kX, x_rsrc, x_at, s + 2);
-                    Panel<FN>::load(w_to + (s & 1) * kW, w_rsrc, w_at, s + 2);
+            for (int t = 0; t < kTurns; ++t) {
+                const int u = t / FM, i = t % FM, out = t - (kTurns - kFree);
+                if (out == 0) {
+                    land<kAhead>();
+                    advance();
+                    load_exponents();
                 }
-            }
-            if (t < kTurns - 3)
-                fx[(t + 1) & 1] = Panel<FM>::fragment(x_now, (t + 1) / FM, (t + 1) % FM, lane);
-            if (t == kTurns - 3) {
-                fx[0] = Panel<FM>::fragment(x_now, 1, FM - 2, lane);
-                fx[2] = Panel<FM>::fragment(x_now, 1, FM - 1, lane);
-            }
-            if (t == kTurns - 1)
-                fx[0] = Panel<FM>::fragment(x_next, 0, 0, lane);
+                load(share(out < 0 ? t + kFree : out), share(out < 0 ? t + kFree + 1 : out + 1));
+                if (out < -1 || (kFree == 1 && out == -1))
+                    fx[(t + 1) & 1] = X::fragment(xs + now, (t + 1) / FM, (t + 1) % FM);
+                if (kFree == 2 && out == -1) {
+                    fx[0] = X::fragment(xs + now, 1, FM - 2);
+                    fx[kRing - 1] = X::fragment(xs + now, 1, FM - 1);
+                }
+                if (t == kTurns - 1) {
+                    fx[0] = X::fragment(xs + next, 0, 0);
+                    next_ex = *reinterpret_cast<const Bytes<FM> *>(xe + next);
+                    next_ew = *reinterpret_cast<const uint32_t *>(we + next);
+                }
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                if (t == j * FM / FN)
-                    fw[1][j] = Panel<FN>::fragment(w_now, 1, j, lane);
-                if (t == kTurns - 2 + 2 * j / FN)
-                    fw[0][j] = Panel<FN>::fragment(w_next, 0, j, lane);
-            }
-            if (t == 0) {
-                const int32_t n = min(s + 1, last);
-                load_bytes<FM>(ep + n * a.epitch, next_ex);
-                next_ew = a.squares.at(w_block, n);
-            }
-            const i32x8 &x = fx[t == kTurns - 1 ? 2 : t & 1];
-            if constexpr (kExact) {
-                if (i == 0) {
+                for (int j = 0; j < FN; ++j) {
+                    if (t == j * FM / FN)
+                        fw[1][j] = W::fragment(ws + now, 1, j);
+                    if (out == kFree * j / FN)
+                        fw[0][j] = W::fragment(ws + next, 0, j);
+                }
+                const i32x8 &x = fx[t == kTurns - 1 ? kRing - 1 : t & 1];
+                if constexpr (EXACT) {
+                    if (i == 0) {
+#pragma unroll
+                        for (int j = 0; j < FN; ++j)
+#pragma unroll
+                            for (int part = 0; part < 4; ++part)
+                                wide[j][part] = widen(fw[u][j], part, step_of(ew));
+                    }
+#pragma unroll
+                    for (int part = 0; part < 4; ++part) {
+                        const bf16x8 bx = widen(x, part, step_of(ex.byte(i)));
+#pragma unroll
+                        for (int j = 0; j < FN; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                                bx, wide[j][part], acc[i][j], 0, 0, 0);
+                    }
+                } else {
 #pragma unroll
                     for (int j = 0; j < FN; ++j)
-#pragma unroll
-                        for (int part = 0; part < 4; ++part)
-                            wide[j][part] = widen(fw[u][j], part, step_of(ew));
+                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                            x, fw[u][j], acc[i][j], 0, 0, 0, (int)ex.byte(i), 0, (int)ew);
                 }
-#pragma unroll
-                for (int part = 0; part < 4; ++part) {
-                    const bf16x8 bx = widen(x, part, step_of(ex[i]));
-#pragma unroll
-                    for (int j = 0; j < FN; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bx, wide[j][part],
-                                                                            acc[i][j], 0, 0, 0);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                        x, fw[u][j], acc[i][j], 0, 0, 0, (int)ex[i], 0, (int)ew);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            __builtin_amdgcn_sched_barrier(0);
+            ex = next_ex;
+            ew = next_ew;
+            now = next;
         }
+
+        const int32_t col = w.tn * S::kCols + 32 * FN * wn + FN * r;
+        O *const out = y + (int64_t)w.split * a.m * a.cols; // split 0 unless O are partial sums
+        float bias[FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            bias[j] = a.bias && col + j < a.cols ? bias_at(a.bias, a.bias_dtype, col + j) : 0.0f;
+        // waits for them here: where no row is stored the next item's first
+        // steps would, and for all their own loads with them
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            asm volatile("" : "+v"(bias[j]));
 #pragma unroll
         for (int i = 0; i < FM; ++i)
-            ex[i] = next_ex[i];
-        ew = next_ew;
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+                const int of = 8 * (q / 4) + 4 * (lane >> 5) + q % 4;
+                const int64_t row = (int64_t)w.tm * S::kRows + 32 * FM * wm + FM * of + i;
+                float v[FN];
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                    v[j] = acc[i][j][q] + bias[j];
+                if (row < a.m)
+                    store_row<FN>(out + row * a.cols + col, v, a.cols - col);
+            }
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); // nothing may land in LDS after the end
+}
 
-    const int32_t col = col0 + 32 * FN * wn + FN * r;
-    float bias[FN];
+// Adds the parts' sums of a row, in their order, and the bias.
+constexpr int kSumColumns = 4;
+template <typename O>
+__global__ __launch_bounds__(kThreads) void k_sum_splits(const Product a, O *__restrict__ y)
+{
+    const int32_t col = kSumColumns * (blockIdx.x * kThreads + threadIdx.x);
+    const int64_t row = blockIdx.y;
+    if (col >= a.cols)
+        return;
+    const float *p = a.parts + row * a.cols + col;
+    float v[kSumColumns] = {};
+    if (col + kSumColumns <= a.cols) {
+        for (int z = 0; z < a.splits; ++z, p += a.m * a.cols) {
+            const u32x4 w = *reinterpret_cast<const u32x4_e4 *>(p);
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-        bias[j] = a.bias && col + j < a.cols ? bias_at(a.bias, a.bias_dtype, col + j) : 0.0f;
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int q = 0; q < 16; ++q) {
-            const int of = 8 * (q / 4) + 4 * (lane >> 5) + q % 4;
-            const int64_t row = row0 + 32 * FM * wm + FM * of + i;
-            float v[FN];
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-                v[j] = acc[i][j][q] + bias[j];
-            if (row < a.m)
-                store_row<FN>(y + row * a.cols + col, v, a.cols - col);
+            for (int k = 0; k < kSumColumns; ++k)
+                v[k] += bits_f32(w[k]);
         }
+    } else {
+        for (int z = 0; z < a.splits; ++z, p += a.m * a.cols)
+#pragma unroll
+            for (int k = 0; k < kSumColumns; ++k)
+                if (col + k < a.cols)
+                    v[k] += p[k];
+    }
+#pragma unroll
+    for (int k = 0; k < kSumColumns; ++k)
+        if (a.bias && col + k < a.cols)
+            v[k] += bias_at(a.bias, a.bias_dtype, col + k);
+    store_row<kSumColumns>(y + row * a.cols + col, v, a.cols - col);
 }
 
 // ---------------------------------------------------------------------------
@@ -728,8 +912,8 @@ int32_t check_rounding(int32_t rounding)
 int32_t launch_rows(const void *x, int32_t dtype, int64_t rows, int64_t d, int64_t ldx,
                     int32_t rounding, uint64_t seed, uint8_t *codes, uint8_t *exps, hipStream_t st)
 {
-    const uint32_t across = (uint32_t)((blocks_of(d) + kRowBlocks - 1) / kRowBlocks);
-    const uint32_t grid = (uint32_t)((rows + 15) / 16) * across;
+    const FastDiv across = fast_div((uint32_t)((blocks_of(d) + kRowBlocks - 1) / kRowBlocks));
+    const uint32_t grid = (uint32_t)((rows + 15) / 16) * across.d;
     const int32_t random = rounding == GQS_ROUND_RANDOM;
     const uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
     if (dtype == GQ_IN_F32)
@@ -756,9 +940,9 @@ int32_t allow_lds(K *kernel, const char *name, uint32_t bytes)
 template <typename T, int FM, int FN, bool MADE>
 int32_t launch_split(Product a, T *y, hipStream_t st)
 {
-    a.tiles_n = (int32_t)((a.cols + 16 * FN - 1) / (16 * FN));
-    const int64_t grid = (a.m + 16 * FM - 1) / (16 * FM) * a.tiles_n;
-    const int waves = std::min(FM * FN >= 16 ? 8 : 16, std::max(1, (int)a.blocks));
+    a.by_tiles = fast_div((uint32_t)((a.cols + 16 * FN - 1) / (16 * FN))); // of a row of them
+    const int64_t grid = (a.m + 16 * FM - 1) / (16 * FM) * a.by_tiles.d;
+    const int waves = std::min(FM * FN >= 8 ? 8 : 16, std::max(1, (int)a.blocks));
     const uint32_t lds = (uint32_t)waves * FM * FN * 1024;
     if (grid >= ((int64_t)1 << 31) / (64 * 16))
         return fail(GQ_ERR_UNSUPPORTED, "%lld tiles", (long long)grid);
@@ -767,39 +951,146 @@ int32_t launch_split(Product a, T *y, hipStream_t st)
     return check_launch("k_product_split");
 }
 
-template <typename T, int FM, int FN>
-int32_t launch_tile(Product a, T *y, hipStream_t st)
+constexpr int kCUs = 256;
+
+// What takes a product: fragments straight from memory, or tiles of a shape,
+// with the depth in `splits` parts where that fills the card.
+enum Way { kDirect, kRows64, kSquare128, kSquare128x2, kSquare256, kWide256, kWays };
+struct Plan {
+    Way way;
+    int32_t splits;
+    int64_t bytes; // of the workspace
+};
+
+using Rows64 = Shape<2, 4, 1, 1, 4, 1, 2>;
+using Square128 = Shape<4, 2, 1, 2, 4, 1, 2>;
+using Square128x2 = Shape<2, 2, 2, 2, 2, 1, 2>;
+using Square256 = Shape<4, 2, 2, 4, 2, 2, 2>;
+using Wide256 = Shape<4, 2, 2, 2, 3, 1, 2>;
+
+// The measured microseconds of a way: a block of the depth, and a tile's
+// beginning and end, while at most `at_once` tiles are at work.
+struct Cost {
+    int32_t rows, cols, at_once;
+    float step, tile;
+};
+constexpr Cost kCosts[2][kWays] = {
+    // exact products of fp32 results
+    {{}, {64, 128, kCUs, 0.62f, 1.5f}, {128, 128, kCUs, 0.95f, 2.6f}, {}, {},
+     {256, 128, kCUs, 1.57f, 4.1f}},
+    // 8-bit products of bf16 ones
+    {{}, {64, 128, kCUs, 0.34f, 1.4f}, {128, 128, kCUs, 0.55f, 1.8f},
+     {128, 128, 2 * kCUs, 0.9f, 4.4f}, {256, 256, kCUs, 1.6f, 5.8f}, {}},
+};
+constexpr Cost kDirectCosts[4] = { // of 16, 32, 64 and 128 rows: one block of loads a wave
+    {16, 16, kCUs, 0.1f, 0.2f}, {32, 16, kCUs, 0.16f, 0.2f}, {64, 16, kCUs, 0.26f, 0.2f},
+    {128, 16, kCUs, 0.43f, 0.3f}};
+
+// What costs least: rounds of tiles, and, where the depth is split, a second
+// kernel that adds up the parts.  Microseconds in a graph, the ways forced: bf16
+// 4096 x 1024 x 1024 Rows64 11.3, Square128 9.2, Square128x2 10.7, Square256
+// 17.7; 2048 x 4096 x 4096 53, 40, 36, 51; 8192 x 4096 x 1024 71, 51, 50, 40;
+// 512 x 4096 x 4096 15.6, 20.9, 24.7, 29; 96 x 1024 x 4096 10.1, 11.7, 13.9,
+// 16.7, directly 17; 96 x 1024 x 1024 6.2, 9.7, 10.3, 12.5, 6.7.  fp32 8192 x
+// 4096 x 1024 Rows64 110, Square128 83, Wide256 70; 1024 x 4096 x 4096 46, 36,
+// 42; 96 x 1024 x 1024 9.5, 10.2, 11.4, directly 7.1.
+Plan plan_of(int64_t m, int64_t cols, int64_t depth, int32_t dtype)
 {
-    const int64_t tiles_m = (a.m + 64 * FM - 1) / (64 * FM);
-    a.tiles_n = (a.cols + 64 * FN - 1) / (64 * FN);
-    if (tiles_m * a.tiles_n >= ((int64_t)1 << 31) / kThreads)
-        return fail(GQ_ERR_UNSUPPORTED, "%lld tiles", (long long)(tiles_m * a.tiles_n));
-    constexpr uint32_t kLds = 2 * (Panel<FM>::kBytes + Panel<FN>::kBytes);
-    GQT_TRY(allow_lds(&k_product_tile<T, FM, FN>, "k_product_tile", kLds));
-    k_product_tile<T, FM, FN><<<(uint32_t)(tiles_m * a.tiles_n), kThreads, kLds, st>>>(
-        a, (int32_t)tiles_m, y);
+    const int64_t blocks = blocks_of(depth);
+    Plan best{kDirect, 1, 0};
+    if (m <= 16)
+        return best;
+    const auto time = [&](const Cost &c, int64_t z) {
+        const int64_t tiles = ((m + c.rows - 1) / c.rows) * ((cols + c.cols - 1) / c.cols);
+        const int64_t rounds = (tiles * z + c.at_once - 1) / c.at_once;
+        const float sums = z > 1 ? 2.5f + (float)(z * m * cols) * 1.5e-6f : 0.0f;
+        return (float)rounds * ((float)((blocks + z - 1) / z) * c.step + c.tile) + sums;
+    };
+    float least = time(kDirectCosts[m <= 32 ? 1 : m <= 64 ? 2 : 3], 1);
+    for (int way = kRows64; way < kWays; ++way) {
+        const Cost &c = kCosts[dtype == GQ_IN_BF16][way];
+        if (!c.at_once)
+            continue;
+        for (int32_t z = 1; z <= 16 && z <= blocks; ++z) {
+            if (z > 1 && ((m + c.rows - 1) / c.rows) * ((cols + c.cols - 1) / c.cols) * z > c.at_once)
+                break;
+            const float us = time(c, z);
+            if (us < least) {
+                least = us;
+                best = {(Way)way, z, z > 1 ? 4 * z * m * cols : 0};
+            }
+        }
+    }
+    return best;
+}
+
+template <typename S, bool EXACT, typename O>
+int32_t launch_tile(const Product &a, O *y, hipStream_t st)
+{
+    const int64_t items = (int64_t)a.by_tiles.d * a.splits;
+    GQT_TRY(allow_lds(&k_product_tile<S, EXACT, O>, "k_product_tile", S::kLds));
+    k_product_tile<S, EXACT, O>
+        <<<(uint32_t)std::min<int64_t>(items, kCUs * S::kBlocksPerCu), 64 * S::kWaves, S::kLds,
+           st>>>(a, y);
     return check_launch("k_product_tile");
 }
 
+template <typename S, typename T>
+int32_t launch_tiles(Product a, T *y, hipStream_t st)
+{
+    constexpr bool kExact = sizeof(T) == 4;
+    const int64_t tiles_m = (a.m + S::kRows - 1) / S::kRows;
+    const int64_t tiles_n = (a.cols + S::kCols - 1) / S::kCols;
+    if (tiles_m * tiles_n >= ((int64_t)1 << 31) - 2 * kCUs)
+        return fail(GQ_ERR_UNSUPPORTED, "%lld tiles", (long long)(tiles_m * tiles_n));
+    a.tiles_m = (uint32_t)tiles_m;
+    a.by_tiles = fast_div((uint32_t)(tiles_m * tiles_n));
+    a.by_group = fast_div((uint32_t)(kGroup * tiles_n));
+    a.by_rest = fast_div((uint32_t)std::max<int64_t>(tiles_m % kGroup, 1));
+    a.steps = (a.blocks + a.splits - 1) / a.splits;
+    a.splits = (a.blocks + a.steps - 1) / a.steps; // none is empty
+    if (a.splits == 1)
+        return launch_tile<S, kExact, T>(a, y, st);
+    Product part = a;
+    part.bias = nullptr;
+    GQT_TRY((launch_tile<S, kExact, float>(part, a.parts, st)));
+    const uint32_t across = (uint32_t)((a.cols + kSumColumns * kThreads - 1) / (kSumColumns * kThreads));
+    k_sum_splits<T><<<dim3(across, (uint32_t)a.m), kThreads, 0, st>>>(a, y);
+    return check_launch("k_sum_splits");
+}
+
 template <typename T>
-int32_t launch_product(const Product &a, void *y, hipStream_t st)
+int32_t launch_product(const Product &a, Way way, void *y, hipStream_t st)
 {
     T *const out = (T *)y;
+    switch (way) {
+    case kRows64:
+        return launch_tiles<Rows64>(a, out, st);
+    case kSquare128:
+        return launch_tiles<Square128>(a, out, st);
+    case kSquare128x2:
+        if constexpr (sizeof(T) == 2)
+            return launch_tiles<Square128x2>(a, out, st);
+        break;
+    case kSquare256:
+        if constexpr (sizeof(T) == 2)
+            return launch_tiles<Square256>(a, out, st);
+        break;
+    case kWide256:
+        if constexpr (sizeof(T) == 4)
+            return launch_tiles<Wide256>(a, out, st);
+        break;
+    default:
+        break;
+    }
     if (a.m <= 16)
         return a.raw ? launch_split<T, 1, 1, true>(a, out, st)
                      : launch_split<T, 1, 1, false>(a, out, st);
     if (a.m <= 32)
         return launch_split<T, 2, 1, false>(a, out, st);
     if (a.m <= 64)
-        return launch_split<T, 4, 2, false>(a, out, st);
-    const int64_t squares = ((a.m + 127) / 128) * ((a.cols + 127) / 128);
-    if (squares >= 64) {
-        if constexpr (sizeof(T) == 2)
-            if (squares >= 1024)
-                return launch_tile<T, 4, 4>(a, out, st);
-        return launch_tile<T, 2, 2>(a, out, st);
-    }
-    return launch_split<T, 8, 2, false>(a, out, st);
+        return launch_split<T, 4, 1, false>(a, out, st);
+    return launch_split<T, 8, 1, false>(a, out, st);
 }
 
 int32_t check_product(int32_t dtype, int64_t m, int64_t cols, int64_t depth, const void *w_codes,
@@ -837,6 +1128,12 @@ Product product_of(int64_t m, const void *w_codes, const void *w_exps, int64_t c
 int64_t codes_bytes(int64_t m, int64_t depth) { return m * fp8_pitch(depth); }
 int64_t exps_bytes(int64_t m, int64_t depth) { return blocks_of(depth) * exp_pitch(m); }
 bool made_on_the_way(int64_t m) { return m <= 16; }
+int64_t plan_bytes(const Plan &p) { return (p.bytes + 15) / 16 * 16; }
+int64_t linear_bytes(const Plan &p, int64_t m, int64_t depth)
+{
+    return made_on_the_way(m) ? p.bytes
+                              : plan_bytes(p) + codes_bytes(m, depth) + exps_bytes(m, depth);
+}
 
 int32_t check_workspace(int64_t need, const void *workspace, int64_t workspace_bytes)
 {
@@ -849,9 +1146,14 @@ int32_t check_workspace(int64_t need, const void *workspace, int64_t workspace_b
                                      : fail(GQ_ERR_ALIGN, "workspace is not 16-byte aligned");
 }
 
-int32_t run_product(const Product &a, void *y, int32_t dtype, hipStream_t st)
+// Runs it by its plan, whose workspace comes first.
+int32_t run_product(Product a, const Plan &plan, void *y, int32_t dtype, void *workspace,
+                    hipStream_t st)
 {
-    return dtype == GQ_IN_F32 ? launch_product<float>(a, y, st) : launch_product<bf16>(a, y, st);
+    a.splits = plan.splits;
+    a.parts = (float *)workspace;
+    return dtype == GQ_IN_F32 ? launch_product<float>(a, plan.way, y, st)
+                              : launch_product<bf16>(a, plan.way, y, st);
 }
 
 } // namespace
@@ -924,7 +1226,8 @@ int32_t gqs_fp8_restore(const void *codes, const void *exps, int64_t rows, int64
     GQT_TRY(check_matrix("out", out, dtype, rows));
     if (rows == 0)
         return ok();
-    const uint32_t per_row = (uint32_t)((d + 7) / 8), chunks = (uint32_t)rows * per_row;
+    const FastDiv per_row = fast_div((uint32_t)((d + 7) / 8));
+    const uint32_t chunks = (uint32_t)rows * per_row.d;
     const uint32_t grid = (chunks + kThreads - 1) / kThreads;
     const int64_t epitch = squares ? blocks_of(d) : exp_pitch(rows);
     const uint8_t *c = (const uint8_t *)codes, *e = (const uint8_t *)exps;
@@ -942,7 +1245,7 @@ int64_t gqs_fp8_product_workspace_bytes(int64_t m, int64_t cols, int64_t depth, 
 {
     if (check_sides(dtype, m, depth) != GQ_OK || check_sides(dtype, m, cols) != GQ_OK)
         return -1;
-    return 0;
+    return plan_of(m, cols, depth, dtype).bytes;
 }
 
 int32_t gqs_fp8_product(const void *x_codes, const void *x_exps, int64_t m, const void *w_codes,
@@ -953,22 +1256,21 @@ int32_t gqs_fp8_product(const void *x_codes, const void *x_exps, int64_t m, cons
     GQT_TRY(check_product(dtype, m, cols, depth, w_codes, w_exps, bias, bias_dtype, y));
     GQT_TRY(check_codes("x_codes", x_codes, m > 0));
     GQT_TRY(check_codes("x_exps", x_exps, m > 0));
-    GQT_TRY(check_workspace(gqs_fp8_product_workspace_bytes(m, cols, depth, dtype), workspace,
-                            workspace_bytes));
+    const Plan plan = plan_of(m, cols, depth, dtype);
+    GQT_TRY(check_workspace(plan.bytes, workspace, workspace_bytes));
     if (m == 0)
         return ok();
     Product a = product_of(m, w_codes, w_exps, cols, depth, transposed, bias, bias_dtype);
     a.x = {(const uint8_t *)x_codes, (const uint8_t *)x_exps, fp8_pitch(depth)};
     a.epitch = exp_pitch(m);
-    return run_product(a, y, dtype, (hipStream_t)stream);
+    return run_product(a, plan, y, dtype, workspace, (hipStream_t)stream);
 }
 
 int64_t gqs_fp8_linear_workspace_bytes(int64_t m, int64_t cols, int64_t depth, int32_t dtype)
 {
-    const int64_t product = gqs_fp8_product_workspace_bytes(m, cols, depth, dtype);
-    if (product < 0 || made_on_the_way(m))
-        return product;
-    return product + codes_bytes(m, depth) + exps_bytes(m, depth);
+    if (check_sides(dtype, m, depth) != GQ_OK || check_sides(dtype, m, cols) != GQ_OK)
+        return -1;
+    return linear_bytes(plan_of(m, cols, depth, dtype), m, depth);
 }
 
 int32_t gqs_fp8_linear(const void *x, int32_t dtype, int64_t m, int64_t depth, int64_t ldx,
@@ -980,8 +1282,8 @@ int32_t gqs_fp8_linear(const void *x, int32_t dtype, int64_t m, int64_t depth, i
     GQT_TRY(check_matrix("x", x, dtype, m));
     GQT_TRY(check_ld("ldx", ldx, depth));
     GQT_TRY(check_rounding(rounding));
-    GQT_TRY(check_workspace(gqs_fp8_linear_workspace_bytes(m, cols, depth, dtype), workspace,
-                            workspace_bytes));
+    const Plan plan = plan_of(m, cols, depth, dtype);
+    GQT_TRY(check_workspace(linear_bytes(plan, m, depth), workspace, workspace_bytes));
     if (m == 0)
         return ok();
     const hipStream_t st = (hipStream_t)stream;
@@ -993,12 +1295,13 @@ int32_t gqs_fp8_linear(const void *x, int32_t dtype, int64_t m, int64_t depth, i
         a.k0 = (uint32_t)seed;
         a.k1 = (uint32_t)(seed >> 32);
     } else {
-        uint8_t *const codes = (uint8_t *)workspace, *const exps = codes + codes_bytes(m, depth);
+        uint8_t *const codes = (uint8_t *)workspace + plan_bytes(plan);
+        uint8_t *const exps = codes + codes_bytes(m, depth);
         GQT_TRY(launch_rows(x, dtype, m, depth, ldx, rounding, seed, codes, exps, st));
         a.x = {codes, exps, fp8_pitch(depth)};
         a.epitch = exp_pitch(m);
     }
-    return run_product(a, y, dtype, st);
+    return run_product(a, plan, y, dtype, workspace, st);
 }
 
 } // extern "C"

@@ -520,23 +520,6 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_sum_partials(
 // ---------------------------------------------------------------------------
 // Elementwise operators: one thread per 8 columns, rows padded to whole groups
 
-// Division of a 31-bit number by an invariant one: q = n m >> s.
-struct FastDiv {
-    uint32_t d, m, s;
-};
-inline FastDiv fast_div(uint32_t d)
-{
-    FastDiv f{d, 0, 31};
-    while (((uint64_t)1 << (f.s - 31)) < d)
-        ++f.s;
-    f.m = (uint32_t)((((uint64_t)1 << f.s) / d) + 1);
-    return f;
-}
-__device__ __forceinline__ uint32_t divide(uint32_t n, const FastDiv &f)
-{
-    return (uint32_t)(((uint64_t)n * f.m) >> f.s);
-}
-
 // The chunk of this thread; chunks = rows * (4 G).
 struct Chunk {
     int64_t row;

@@ -41,8 +41,26 @@ inline bool dtype_ok(int32_t dtype) { return dtype == GQ_IN_F32 || dtype == GQ_I
 inline bool aligned_to(const void *p, int64_t a) { return ((uintptr_t)p & (uintptr_t)(a - 1)) == 0; }
 inline int64_t groups_of(int64_t d) { return (d + 31) / 32; }
 
+// Division of a 31-bit number by an invariant one: q = n m >> s.
+struct FastDiv {
+    uint32_t d, m, s;
+};
+inline FastDiv fast_div(uint32_t d)
+{
+    FastDiv f{d, 0, 31};
+    while (((uint64_t)1 << (f.s - 31)) < d)
+        ++f.s;
+    f.m = (uint32_t)((((uint64_t)1 << f.s) / d) + 1);
+    return f;
+}
+
 // ---------------------------------------------------------------------------
 // Device
+
+__device__ __forceinline__ uint32_t divide(uint32_t n, const FastDiv &f)
+{
+    return (uint32_t)(((uint64_t)n * f.m) >> f.s);
+}
 
 using bf16 = __bf16;
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
