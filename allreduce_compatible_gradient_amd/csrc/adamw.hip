@@ -46,7 +46,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTensors = 64;                     // of a launch: 3.9 KB of arguments
-constexpr int64_t kChunk = 8 * kThreads * 4;     // elements of a block
+constexpr int64_t kStep = 8 * kThreads;          // elements of a block's step
+constexpr int64_t kFew = kStep * 2048;           // elements in all that take one step a block
 constexpr int64_t kMaxElements = (int64_t)1 << 35; // i / 8 is one word of the counter
 
 // Where a launch's tensors are; tensor j has the blocks from first[j] on.
@@ -55,6 +56,7 @@ struct Tensors {
     uint32_t first[kTensors + 1];
     int32_t count;
     uint32_t number; // of t[0] in the whole list
+    int32_t chunk;   // elements of a block
 };
 
 // The tensor of this block: the last whose first block is not behind it.
@@ -127,8 +129,8 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const Tensors a, Coefs by_va
     const gqs_tensor &t = a.t[j];
     const Coefs c = coefs ? *coefs : by_value;
     const float factor = scale ? *scale : 1.0f;
-    const int64_t base = (int64_t)(blockIdx.x - a.first[j]) * kChunk;
-    const int32_t n = (int32_t)min(t.n - base, kChunk);
+    const int64_t base = (int64_t)(blockIdx.x - a.first[j]) * a.chunk;
+    const int32_t n = (int32_t)min(t.n - base, (int64_t)a.chunk);
     // whole 128-element blocks, for the codes past n
     const int32_t end = BITS == 8 ? (n + 127) / 128 * 128 : n;
     P *const p = (P *)t.p + base;
@@ -153,7 +155,13 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const Tensors a, Coefs by_va
             const float gs = gv[k] * factor;
             m[k] = fmaf(r.beta1, m[k], r.other1 * gs);
             v[k] = fmaf(r.beta2, v[k], r.other2 * (gs * gs));
-            const float change = m[k] / fmaf(sqrtf(v[k]), c.root, r.eps);
+            // The 8-bit moments' roundings leave no time for a division and a
+            // root to the last bit: a unit in the last place each, and a v
+            // below 2^-126 counts as 0 here.
+            const float change =
+                BITS == 8 ? m[k] * __builtin_amdgcn_rcpf(
+                                       fmaf(__builtin_amdgcn_sqrtf(v[k]), c.root, r.eps))
+                          : m[k] / fmaf(sqrtf(v[k]), c.root, r.eps);
             pv[k] = fmaf(-c.size, change, pv[k] * c.decay);
         }
         const uint32_t eighth = (uint32_t)((base + i) >> 3);
@@ -212,7 +220,7 @@ __global__ __launch_bounds__(kThreads) void k_moment8_restore(const uint8_t *__r
 // ---------------------------------------------------------------------------
 // the norm
 
-constexpr int64_t kNormChunk = 8 * kThreads * 8;
+constexpr int64_t kNormChunk = kStep * 8;
 
 // The sum of v over the block, in thread 0.
 __device__ __forceinline__ double block_sum(double v)
@@ -240,12 +248,28 @@ __global__ __launch_bounds__(kThreads) void k_square_sums(const Tensors a,
     const int32_t n = (int32_t)min(a.t[j].n - base, kNormChunk);
     const G *const g = (const G *)a.t[j].g + base;
     double sum = 0.0;
-    for (int32_t i = 8 * threadIdx.x; i < n; i += 8 * kThreads) {
+    const auto add = [&](const Raw8<G> &r) {
         float v[8];
-        load8(g, i, n, v);
+        unpack(r, v);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             sum = fma((double)v[k], (double)v[k], sum);
+    };
+    if (n == kNormChunk) { // all loads at once
+        Raw8<G> r[kNormChunk / kStep];
+#pragma unroll
+        for (int k = 0; k < kNormChunk / kStep; ++k)
+            load_words(g + 8 * threadIdx.x + k * kStep, r[k]);
+#pragma unroll
+        for (int k = 0; k < kNormChunk / kStep; ++k)
+            add(r[k]);
+    } else {
+        for (int32_t i = 8 * threadIdx.x; i < n; i += kStep) {
+            Raw8<G> r;
+            load_ahead(g, i, n, r);
+            settle(g, i, n, r);
+            add(r);
+        }
     }
     sum = block_sum(sum);
     if (threadIdx.x == 0)
@@ -277,6 +301,7 @@ __global__ __launch_bounds__(kThreads) void k_norm(const double *__restrict__ pa
 int64_t gather(const gqs_tensor *tensors, int64_t count, int64_t from, int64_t chunk, Tensors &a,
                bool number_each)
 {
+    a.chunk = (int32_t)chunk;
     a.count = 0;
     a.first[0] = 0;
     a.number = (uint32_t)from;
@@ -348,9 +373,14 @@ template <typename P, typename G, int BITS>
 int32_t launch_adamw(const gqs_tensor *tensors, int64_t count, const Coefs &c, const Coefs *device,
                      const Rates &r, const float *scale, hipStream_t st)
 {
+    // Long chunks share the search for the tensor, short ones fill the card.
+    int64_t all = 0;
+    for (int64_t i = 0; i < count; ++i)
+        all += tensors[i].n;
+    const int64_t chunk = all < kFew ? kStep : 4 * kStep;
     Tensors a;
     for (int64_t at = 0; at < count;) {
-        at = gather(tensors, count, at, kChunk, a, true);
+        at = gather(tensors, count, at, chunk, a, true);
         if (a.count) {
             k_adamw<P, G, BITS><<<a.first[a.count], kThreads, 0, st>>>(a, c, device, r, scale);
             GQT_TRY(check_launch("k_adamw"));

@@ -76,29 +76,23 @@ __device__ __forceinline__ u32x2 e4m3_nearest8(const float (&v)[8], uint32_t e)
     return u32x2{e4m3_nearest4(t[0], t[1], t[2], t[3]), e4m3_nearest4(t[4], t[5], t[6], t[7])};
 }
 
-// One code of |t| in random rounding: scaled by 2^-120 the code is the float's
-// leading bits, subnormal or not, above 20 that are rounded off; u enters
-// above a half of its last place.
-__device__ __forceinline__ uint32_t e4m3_random(float t, uint32_t u)
+// Random rounding of x >= 0 whose code is the leading bits of x 2^scale, which
+// may be subnormal, above 20 that are rounded off: u enters above a half of
+// their last place.
+__device__ __forceinline__ uint32_t random_code(float x, int scale, uint32_t u)
 {
-    const uint32_t b = __float_as_uint(fabsf(t) * 0x1p-120f);
-    return (b + (u << 4 | 8u)) >> 20;
-}
-__device__ __forceinline__ uint32_t e5m3_random(float t, uint32_t u)
-{
-    const uint32_t b = __float_as_uint(t * 0x1p-111f);
-    return (b + (u << 4 | 8u)) >> 20;
+    return (__float_as_uint(ldexpf(x, scale)) + (u << 4 | 8u)) >> 20;
 }
 
 // The codes of eight values at random, with their signs.
 __device__ __forceinline__ u32x2 e4m3_random8(const float (&v)[8], uint32_t e, const uint4 &draw)
 {
-    const float inv = inverse_step(e);
+    const int scale = 7 - (int)e; // 2^-120 x 2^-E: the least normal number, 2^-6, becomes 2^-126
     const uint32_t top = e == kHighestE4m3 ? 0x77u : 0x7Eu;
     u32x2 w = {0, 0};
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const uint32_t c = min(e4m3_random(v[k] * inv, half16(draw, k)), top);
+        const uint32_t c = min(random_code(fabsf(v[k]), scale, half16(draw, k)), top);
         w[k >> 2] |= (c | (__float_as_uint(v[k]) >> 24 & 0x80u)) << (8 * (k & 3));
     }
     return w;
@@ -107,12 +101,12 @@ __device__ __forceinline__ u32x2 e4m3_random8(const float (&v)[8], uint32_t e, c
 // Those of eight second moments (v >= 0).
 __device__ __forceinline__ u32x2 e5m3_random8(const float (&v)[8], uint32_t e, const uint4 &draw)
 {
-    const float inv = inverse_step(e);
+    const int scale = 16 - (int)e; // 2^-111 x 2^-E: 2^-15 becomes 2^-126
     const uint32_t top = e == kHighestE5m3 ? 0xF7u : 0xFFu;
     u32x2 w = {0, 0};
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-        w[k >> 2] |= min(e5m3_random(v[k] * inv, half16(draw, k)), top) << (8 * (k & 3));
+        w[k >> 2] |= min(random_code(v[k], scale, half16(draw, k)), top) << (8 * (k & 3));
     return w;
 }
 

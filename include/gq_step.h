@@ -128,7 +128,9 @@ typedef struct gqs_adamw_args {
  *   g' = scale g, m = beta1 m + (1 - beta1) g', v = beta2 v + (1 - beta2) g'^2,
  *   p = p (1 - lr weight_decay)
  *       - lr m / (1 - beta1^step) / (sqrt(v / (1 - beta2^step)) + eps),
- * in fp32; the update takes the moments before their rounding.  A bf16 p is
+ * in fp32; the update takes the moments before their rounding (with 8-bit
+ * moments, root and quotient to a unit in their last place, and a v below
+ * 2^-126 as 0 under the root).  A bf16 p is
  * rounded once, to nearest, or, with `random`, at random: the 16 bits below
  * its last place get the half of draw 2 added.  lr >= 0, 0 <= beta < 1, eps
  * >= 0, step >= 1.  No two tensors may overlap.  The workspace (16 bytes) is
