@@ -72,12 +72,14 @@ class Fp8:
 class Fp8Weight:
     """The copy of a weight [n, k]: ``codes`` float8_e4m3fn [n, 128 Gk],
     ``exps`` uint8 [Gn, Gk] for the squares of 128 x 128, and ``codes_t``
-    [k, 128 Gn], the codes transposed (or None)."""
+    [k, 128 Gn], the codes transposed.  Either may be None where only the
+    product of the other is wanted (without codes, n has to be given)."""
 
-    __slots__ = ("codes", "exps", "k", "codes_t")
+    __slots__ = ("codes", "exps", "n", "k", "codes_t")
 
-    def __init__(self, codes: torch.Tensor, exps: torch.Tensor, k: int, codes_t=None):
+    def __init__(self, codes, exps: torch.Tensor, k: int, codes_t=None, n: int | None = None):
         self.codes, self.exps, self.k, self.codes_t = codes, exps, int(k), codes_t
+        self.n = int(codes.shape[0] if n is None else n)
 
     @classmethod
     def empty(cls, n: int, k: int, device, transposed: bool = True) -> "Fp8Weight":
@@ -88,13 +90,13 @@ class Fp8Weight:
 
     @property
     def shape(self):
-        return self.codes.shape[0], self.k
+        return self.n, self.k
 
     def _tensors(self):
         return self.codes, self.exps, self.codes_t
 
     def __repr__(self):
-        return f"Fp8Weight({self.shape[0]} x {self.k}, {self.codes.device})"
+        return f"Fp8Weight({self.n} x {self.k}, {self.exps.device})"
 
 
 def _blocks(d: int) -> int:
@@ -126,15 +128,15 @@ def _weight_copy(w, device, transposed: bool):
     """(codes, exps, cols, depth) of the product that reads a weight's copy."""
     if not isinstance(w, Fp8Weight):
         raise TypeError(f"w must be an Fp8Weight, got {type(w).__name__}")
-    if not isinstance(w.codes, torch.Tensor) or w.codes.dim() != 2 or w.codes.shape[0] < 1:
-        raise ValueError("w.codes must be [n, 128 Gk] with n >= 1")
     n, k = w.shape
+    if n < 1 or k < 1:
+        raise ValueError(f"w must be [n, k] with n, k >= 1, got {[n, k]}")
     exps = _part(w.exps, "w.exps", (_blocks(n), _blocks(k)), torch.uint8, device)
-    if not transposed:
-        return _part(w.codes, "w.codes", (n, 128 * _blocks(k)), _E4M3, device), exps, n, k
-    if w.codes_t is None:
-        raise ValueError("w has no transposed codes")
-    return _part(w.codes_t, "w.codes_t", (k, 128 * _blocks(n)), _E4M3, device), exps, k, n
+    if (w.codes_t if transposed else w.codes) is None:
+        raise ValueError(f"w has no {'transposed ' if transposed else ''}codes")
+    if transposed:
+        return _part(w.codes_t, "w.codes_t", (k, 128 * _blocks(n)), _E4M3, device), exps, k, n
+    return _part(w.codes, "w.codes", (n, 128 * _blocks(k)), _E4M3, device), exps, n, k
 
 
 def _rounding(seed):
@@ -170,7 +172,8 @@ def gqs_fp8_rows(x: torch.Tensor, *, seed=None, out: Fp8 | None = None, stream=N
 def gqs_fp8_weight(w: torch.Tensor, *, transposed: bool = True, out: Fp8Weight | None = None,
                    stream=None) -> Fp8Weight:
     """The copy of a weight [n, k], to nearest; with its transposed codes
-    unless they are not wanted (with `out`: if it has them)."""
+    unless they are not wanted (with `out`, which needs codes: if it has
+    them)."""
     dt, ldw = _matrix(w, "w")
     device = w.device
     if _elsewhere(device, stream):
@@ -191,11 +194,12 @@ def gqs_fp8_weight(w: torch.Tensor, *, transposed: bool = True, out: Fp8Weight |
 
 
 def gqs_fp8_restore(a, dtype=torch.bfloat16, *, stream=None) -> torch.Tensor:
-    """The values an Fp8 or Fp8Weight stands for (exact in either dtype)."""
+    """The values an Fp8 or Fp8Weight (with its codes) stands for, exact in
+    either dtype."""
     dt = _dtype(dtype, "dtype")
-    if not isinstance(a, (Fp8, Fp8Weight)) or not a.codes.is_cuda:
+    if not isinstance(a, (Fp8, Fp8Weight)) or not a.exps.is_cuda:
         raise ValueError("a must be an Fp8 or Fp8Weight on a device")
-    device = a.codes.device
+    device = a.exps.device
     if _elsewhere(device, stream):
         with _Elsewhere(device, stream, _tensors_of(a)):
             return gqs_fp8_restore(a, dtype)

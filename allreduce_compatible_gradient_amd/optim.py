@@ -11,7 +11,7 @@ updates below its last place count in expectation.
 
 ``gqs_*`` are the C entry points on lists of device tensors, in place, on
 torch's current stream or a given one, with no synchronization.  ``AdamW`` is
-the optimizer.
+the optimizer of torch's interface.
 """
 from __future__ import annotations
 
@@ -126,6 +126,7 @@ def gqs_adamw(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, betas=(0.9, 0.9
     otherwise.  Calls of one step with one seed share random numbers between
     tensors of the same number in their lists: give each list its own."""
     params, grads = list(params), list(grads)
+    exp_avgs, exp_avg_sqs = list(exp_avgs), list(exp_avg_sqs)
     if len(params) != len(grads):
         raise ValueError(f"{len(params)} params, {len(grads)} grads")
     if not params:
@@ -208,3 +209,185 @@ def gqs_grad_norm(grads, *, max_norm=None, stream=None):
                               None if scale is None else scale.data_ptr(), workspace.data_ptr(),
                               max(need, 0), _current(device)))
     return norm, scale
+
+
+# ---------------------------------------------------------------------------
+# the optimizer
+
+def _order(p):
+    """The order of p's dimensions in which its elements lie side by side
+    (None: in their own)."""
+    if p.is_contiguous():
+        return None
+    order = sorted(range(p.dim()), key=lambda k: (-p.stride(k), -p.shape[k]))
+    if not p.permute(order).is_contiguous():
+        raise ValueError(f"a parameter of strides {p.stride()} does not fill its memory")
+    return order
+
+
+def _on_device(p) -> bool:
+    return p.is_cuda
+
+
+class AdamW(torch.optim.Optimizer):
+    """AdamW (decoupled weight decay) on ROCm devices, all parameters of a
+    type in one launch.
+
+    bits=8 keeps both moments in 8 bits, 2 + 1/64 bytes a parameter in place of
+    8.  random rounds bf16 parameters at random (8-bit moments always are), so
+    that small updates count.  max_norm clips the gradients' norm over all
+    parameters (``last_norm`` is that of the last step, on the device).
+    Nothing waits for the device.
+
+    The random numbers come from `seed`, the step and the parameter's place: a
+    process group's ranks, which step with equal gradients, stay equal while
+    they have one seed.
+
+    capturable=True counts steps on the device, one count for a group, so that
+    a captured graph goes on counting (and draws new numbers) at each replay;
+    lr may then be a float32 tensor on the device.  Otherwise each parameter
+    counts the steps in which it had a gradient."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay: float = 1e-2, *, bits: int = 32, random: bool = True,
+                 seed: int = 0, max_norm: float | None = None, capturable: bool = False):
+        if bits not in (8, 32):
+            raise ValueError(f"bits must be 8 or 32, got {bits!r}")
+        if isinstance(lr, torch.Tensor):
+            if not capturable:
+                raise ValueError("lr may be a tensor with capturable=True")
+        elif not 0.0 <= lr < float("inf"):
+            raise ValueError(f"lr must be finite and not negative, got {lr}")
+        if len(betas) != 2 or not all(0.0 <= b < 1.0 for b in betas):
+            raise ValueError(f"betas must be two numbers from 0 to below 1, got {betas}")
+        if not 0.0 <= eps < float("inf") or not 0.0 <= weight_decay < float("inf"):
+            raise ValueError("eps and weight_decay must be finite and not negative")
+        if max_norm is not None and not 0.0 <= max_norm < float("inf"):
+            raise ValueError(f"max_norm must be finite and not negative, got {max_norm}")
+        super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps,
+                                      weight_decay=weight_decay))
+        self.bits, self.random, self.seed = bits, bool(random), int(seed)
+        self.max_norm, self.capturable, self.last_norm = max_norm, bool(capturable), None
+
+    def _new_state(self, p):
+        n, device = p.numel(), p.device
+        if self.bits == 32:
+            state = {"exp_avg": torch.zeros(n, device=device),
+                     "exp_avg_sq": torch.zeros(n, device=device)}
+        else:
+            m, v = Moment8.zeros(n, device, False), Moment8.zeros(n, device, True)
+            state = {"exp_avg": m.codes, "exp_avg_exps": m.exps,
+                     "exp_avg_sq": v.codes, "exp_avg_sq_exps": v.exps}
+        if not self.capturable:
+            state["step"] = 0
+        return state
+
+    def moments(self, p):
+        """p's (first, second) moment, flat in the order of its memory: fp32
+        tensors or Moment8."""
+        state = self.state[p]
+        if self.bits == 32:
+            return state["exp_avg"], state["exp_avg_sq"]
+        n = p.numel()
+        return (Moment8(state["exp_avg"], state["exp_avg_exps"], n),
+                Moment8(state["exp_avg_sq"], state["exp_avg_sq_exps"], n))
+
+    def _buckets(self):
+        """What one call takes: (group, step, place of its first parameter,
+        parameters, flat values, flat gradients), by group, device, types and
+        step."""
+        buckets, place = {}, 0
+        for k, group in enumerate(self.param_groups):
+            for p in group["params"]:
+                place += 1
+                if p.grad is None:
+                    continue
+                g = p.grad
+                if g.is_sparse:
+                    raise RuntimeError("AdamW takes no sparse gradients")
+                if not _on_device(p):
+                    raise ValueError(f"AdamW takes parameters on a device, one is on {p.device}")
+                state = self.state[p]
+                if not state:
+                    state.update(self._new_state(p))
+                order = _order(p)
+                value, g = p.detach(), g.detach()
+                if order is not None:
+                    value, g = value.permute(order), g.permute(order)
+                step = None if self.capturable else state["step"]
+                key = (k, p.device, p.dtype, g.dtype, step)
+                if key not in buckets:
+                    buckets[key] = (group, step, place, [], [], [])
+                buckets[key][3].append(p)
+                buckets[key][4].append(value)
+                buckets[key][5].append(g.contiguous())
+        return list(buckets.values())
+
+    def _clip(self, buckets):
+        """The gradients' common factor, on the device (None: no clipping)."""
+        if self.max_norm is None or not buckets:
+            return None
+        lists = {}
+        for b in buckets:
+            for g in b[5]:
+                lists.setdefault((g.device, g.dtype), []).append(g)
+        if len({device for device, _ in lists}) > 1:
+            raise ValueError("max_norm takes parameters on one device")
+        if len(lists) == 1:
+            self.last_norm, scale = gqs_grad_norm(*lists.values(), max_norm=self.max_norm)
+            return scale
+        norms = torch.stack([gqs_grad_norm(grads)[0] for grads in lists.values()])
+        self.last_norm = norms.double().square().sum().sqrt().float()
+        return (self.max_norm / (self.last_norm + 1e-6)).clamp(max=1.0)
+
+    def _count(self, group, device):
+        """The group's number of steps on the device, one more than before."""
+        count = group.get("step")
+        if count is None:
+            count = group["step"] = torch.zeros(1, dtype=torch.int64, device=device)
+        return count.add_(1)
+
+    @torch.no_grad()
+    def step(self, closure=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        buckets = self._buckets()
+        scale = self._clip(buckets)
+        counted = {}
+        for group, step, place, params, values, grads in buckets:
+            if self.capturable:
+                if id(group) not in counted:
+                    counted[id(group)] = self._count(group, params[0].device)
+                step = counted[id(group)]
+            else:
+                step += 1
+            m, v = zip(*(self.moments(p) for p in params))
+            drawn = self.bits == 8 or (self.random and params[0].dtype == torch.bfloat16)
+            gqs_adamw(values, grads, m, v, step=step, lr=group["lr"], betas=group["betas"],
+                      eps=group["eps"], weight_decay=group["weight_decay"], scale=scale,
+                      seed=_mix_seed(self.seed, place) if drawn else None)
+            if not self.capturable:
+                for p in params:
+                    self.state[p]["step"] = step
+        return loss
+
+    def load_state_dict(self, state_dict):
+        """As torch's, which would cast moments and codes to the parameters'
+        types: they come as they were saved."""
+        saved = [i for group in state_dict["param_groups"] for i in group["params"]]
+        for i in saved:
+            codes = state_dict["state"].get(i, {}).get("exp_avg")
+            if codes is not None and (codes.dtype == torch.float32) != (self.bits == 32):
+                raise ValueError(f"the state has other moments than those of bits={self.bits}")
+        super().load_state_dict(state_dict)
+        own = [p for group in self.param_groups for p in group["params"]]
+        for i, p in zip(saved, own):
+            for key, value in state_dict["state"].get(i, {}).items():
+                if isinstance(value, torch.Tensor):
+                    value = value.detach().clone().to(p.device)
+                self.state[p][key] = value
+        for group in self.param_groups:
+            if isinstance(group.get("step"), torch.Tensor) and group["params"]:
+                group["step"] = group["step"].clone().to(group["params"][0].device)

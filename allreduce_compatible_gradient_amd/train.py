@@ -461,6 +461,8 @@ def _rows(t: torch.Tensor, d: int) -> torch.Tensor:
     """t as [rows, d] with unit column stride (a copy where its strides do
     not allow it, such as a gradient expanded from a scalar)."""
     t = t.reshape(-1, d)
+    if t.shape[0] == 0:
+        return t.new_empty(t.shape)  # contiguous() leaves an empty tensor's strides
     if (d > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and 0 < t.stride(0) < d):
         t = t.contiguous()
     return t
@@ -580,12 +582,50 @@ def _parameter_grads(dy, x, dtypes, bias):
     return _cast(dw, dtypes[0]), _cast(db, dtypes[1])
 
 
+# The seeds of an fp8 product's gradient (the copies of a pass have 0 to 3).
+_DY_SEED = 4
+
+
+def _fp8_weight(weight, transposed: bool):
+    from .fp8 import gqs_fp8_weight
+    return gqs_fp8_weight(_rows(weight, weight.shape[-1]), transposed=transposed)
+
+
+def _fp8_parts(w):
+    """What the product for dx reads of a weight's copy, for
+    save_for_backward."""
+    return (None, None) if w is None else (w.codes_t, w.exps)
+
+
+def _forward_product(x, weight, bias, fp8: bool, need_dx: bool):
+    """(x w^T + bias, the weight's copy that the backward pass reads or
+    None): the library's product, or that of e4m3 copies, in x's dtype."""
+    if not fp8:
+        return torch.nn.functional.linear(x, weight, bias), None
+    from .fp8 import gqs_fp8_linear
+    w8 = _fp8_weight(weight, need_dx)
+    y = gqs_fp8_linear(_rows(x, x.shape[-1]), w8, None if bias is None else bias.contiguous())
+    return y.view(*x.shape[:-1], y.shape[-1]), w8
+
+
+def _backward_product(dy, weight, fp8_parts, shape, seed):
+    """dy w, dy [..., n]: of e4m3 copies where the forward pass made them, dy
+    rounded at random with a seed."""
+    if fp8_parts[0] is None:
+        return dy @ weight
+    from .fp8 import Fp8Weight, gqs_fp8_linear
+    w8 = Fp8Weight(None, fp8_parts[1], shape[1], fp8_parts[0], n=shape[0])
+    dx = gqs_fp8_linear(_rows(dy, shape[0]), w8, transposed=True, seed=seed)
+    return dx.view(*dy.shape[:-1], shape[1])
+
+
 class _Linear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, bias, seed, grad):
+    def forward(ctx, x, weight, bias, seed, grad, fp8):
         dtype = _product_dtype(x)
         need = ctx.needs_input_grad
         ctx.x_dtype, ctx.dtypes = x.dtype, _dtypes_of(weight, bias)
+        ctx.shape, ctx.seed = tuple(weight.shape), seed
         with _AS_IT_IS if dtype is None else _no_autocast(x):
             x, weight, bias = _cast(x, dtype), _cast(weight, dtype), _cast(bias, dtype)
             x2 = _rows(x, x.shape[-1])
@@ -595,29 +635,37 @@ class _Linear(torch.autograd.Function):
                 _matrix(x2, "x")  # refuses what the copy would
                 kept = None
             ctx.d = x2.shape[1]
-            ctx.save_for_backward(weight if need[0] else None, *_parts(kept))
-            return torch.nn.functional.linear(x, weight, bias)
+            y, w8 = _forward_product(x, weight, bias, fp8, need[0])
+            ctx.save_for_backward(weight if need[0] and not fp8 else None, *_parts(kept),
+                                  *_fp8_parts(w8))
+            return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        weight, codes, exps = ctx.saved_tensors
+        weight, codes, exps, *fp8_parts = ctx.saved_tensors
         dx = dw = db = None
         with _no_autocast(dy):
             if ctx.needs_input_grad[0]:
-                dx = _cast(dy @ weight, ctx.x_dtype)
+                seed = None if ctx.seed is None else _mix_seed(ctx.seed, _DY_SEED)
+                dx = _cast(_backward_product(dy, weight, fp8_parts, ctx.shape, seed), ctx.x_dtype)
             if ctx.needs_input_grad[1] or ctx.needs_input_grad[2]:
                 dw, db = _parameter_grads(_rows(dy, dy.shape[-1]), Act8(codes, exps, ctx.d),
                                           ctx.dtypes, ctx.needs_input_grad[2])
-        return dx, dw, db, None, None
+        return dx, dw, db, None, None, None
 
 
-def linear(x, weight, bias=None, *, seed=None):
+def linear(x, weight, bias=None, *, seed=None, fp8: bool = False):
     """x w^T + bias (the library's product), differentiable, with x kept for
     the weight's gradient, where there is one, in 8 bits.  Under autocast the
     product and the copy are those of the cast x, and the gradients have the
-    dtypes of x, weight and bias; autocast has to be to bf16."""
-    return _Linear.apply(x, weight, bias, seed, torch.is_grad_enabled())
+    dtypes of x, weight and bias; autocast has to be to bf16.
+
+    With fp8 the products for y and for x's gradient are those of e4m3 copies
+    with a scale for each block of 128 (``fp8``), made of x, the weight and
+    the gradient in each pass; the gradient's is rounded at random where a
+    seed is given."""
+    return _Linear.apply(x, weight, bias, seed, torch.is_grad_enabled(), bool(fp8))
 
 
 class _Mlp8(torch.autograd.Function):
@@ -627,7 +675,7 @@ class _Mlp8(torch.autograd.Function):
     a gradient reads them."""
 
     @staticmethod
-    def forward(ctx, x, nw, nb, w1, b1, w2, b2, eps, approximate, seed):
+    def forward(ctx, x, nw, nb, w1, b1, w2, b2, eps, approximate, seed, fp8):
         dtype = _product_dtype(x)
         x2 = _rows(x, x.shape[-1])
         rows, d = x2.shape
@@ -640,6 +688,7 @@ class _Mlp8(torch.autograd.Function):
         g8 = Act8.empty(rows, ff, x.device) if need[5] or need[6] else None
         ctx.d, ctx.ff, ctx.approximate, ctx.x_dtype = d, ff, approximate, x.dtype
         ctx.dtypes1, ctx.dtypes2 = _dtypes_of(w1, b1), _dtypes_of(w2, b2)
+        ctx.shapes, ctx.seed = (tuple(w1.shape), tuple(w2.shape)), seed
         with _AS_IT_IS if dtype is None else _no_autocast(x):
             w1, b1, w2, b2 = (_cast(t, dtype) for t in (w1, b1, w2, b2))
             cast = dtype is not None and dtype != x.dtype
@@ -649,12 +698,12 @@ class _Mlp8(torch.autograd.Function):
                 a = a.to(dtype)
                 if a8 is not None:
                     gqt_act8_save(a, seed=seeds[1], out=a8)
-            h = torch.nn.functional.linear(a, w1, b1)
+            h, w1_8 = _forward_product(a, w1, b1, fp8, any(need[:3]))
             g = gqt_gelu(h, approximate, save_h=h8, seed_h=seeds[2], save_y=g8, seed_y=seeds[3])
-            y = torch.nn.functional.linear(g, w2, b2)
-        ctx.save_for_backward(mean, rstd, nw, w1 if any(need[:3]) else None,
-                              w2 if any(need[:5]) else None, *_parts(x8), *_parts(a8),
-                              *_parts(h8), *_parts(g8))
+            y, w2_8 = _forward_product(g, w2, b2, fp8, any(need[:5]))
+        ctx.save_for_backward(mean, rstd, nw, w1 if any(need[:3]) and not fp8 else None,
+                              w2 if any(need[:5]) and not fp8 else None, *_parts(x8), *_parts(a8),
+                              *_parts(h8), *_parts(g8), *_fp8_parts(w1_8), *_fp8_parts(w2_8))
         return y.view(*x.shape[:-1], w2.shape[0])
 
     @staticmethod
@@ -663,6 +712,10 @@ class _Mlp8(torch.autograd.Function):
         mean, rstd, nw, w1, w2, *kept = ctx.saved_tensors
         d, ff = ctx.d, ctx.ff
         x8, a8, h8, g8 = (Act8(kept[2 * i], kept[2 * i + 1], (d, d, ff, ff)[i]) for i in range(4))
+        w1_8, w2_8 = kept[8:10], kept[10:]
+        seeds = [None, None]
+        if ctx.seed is not None:
+            seeds = [_mix_seed(ctx.seed, _DY_SEED + k) for k in range(2)]
         need = ctx.needs_input_grad
         dy2 = _rows(dy, dy.shape[-1])
         dx = dnw = dnb = dw1 = db1 = dw2 = db2 = None
@@ -670,15 +723,17 @@ class _Mlp8(torch.autograd.Function):
             if need[5] or need[6]:
                 dw2, db2 = _parameter_grads(dy2, g8, ctx.dtypes2, need[6])
             if any(need[:5]):
-                dh = gqt_gelu_backward(dy2 @ w2, h8, ctx.approximate)
+                dg = _backward_product(dy2, w2, w2_8, ctx.shapes[1], seeds[1])
+                dh = gqt_gelu_backward(dg, h8, ctx.approximate)
                 if need[3] or need[4]:
                     dw1, db1 = _parameter_grads(dh, a8, ctx.dtypes1, need[4])
                 if any(need[:3]):
                     dx, dnw, dnb = gqt_layer_norm_backward(
-                        _cast(dh @ w1, ctx.x_dtype), x8, mean, rstd, nw, weight_grad=need[1],
+                        _cast(_backward_product(dh, w1, w1_8, ctx.shapes[0], seeds[0]),
+                              ctx.x_dtype), x8, mean, rstd, nw, weight_grad=need[1],
                         bias_grad=need[2])
                     dx = dx.view(*dy.shape[:-1], d)
-        return dx, dnw, dnb, dw1, db1, dw2, db2, None, None, None
+        return dx, dnw, dnb, dw1, db1, dw2, db2, None, None, None, None
 
 
 def _is_plain(module, kind) -> bool:
@@ -717,11 +772,16 @@ class Mlp8(torch.nn.Module):
 
     norm, up and down run together as one operator.  One that was replaced or
     has hooks is called as it is instead, and keeps what it keeps; the others
-    keep the same copies as before."""
+    keep the same copies as before.
+
+    fp8=True takes the products of up and down (and those for the gradients
+    of their inputs) in e4m3 with a scale for each block of 128, as
+    ``linear(..., fp8=True)`` does.  Each pass makes its copies of the weights;
+    ``hold_fp8`` keeps them for the passes without gradients."""
 
     def __init__(self, d: int, hidden: int, *, eps: float = 1e-5, approximate: str = "tanh",
                  random: bool = True, seed: int | None = None, device=None,
-                 dtype=torch.bfloat16):
+                 dtype=torch.bfloat16, fp8: bool = False):
         super().__init__()
         _form(approximate)
         kw = {"device": device, "dtype": dtype}
@@ -730,6 +790,34 @@ class Mlp8(torch.nn.Module):
         self.down = torch.nn.Linear(hidden, d, **kw)
         self.approximate, self.random, self.seed, self.passes = approximate, random, seed, 0
         self._drawn = None  # the seed of a block that was given none
+        self.fp8 = bool(fp8)
+        self._held = None  # the weights' copies, for passes without gradients
+
+    def hold_fp8(self, hold: bool = True):
+        """Makes the e4m3 copies of up's and down's weights as they are now
+        and takes them, in passes without gradients, until it is called
+        again; hold=False drops them.  For serving: a pass then reads one
+        byte a weight.  They are not in the state dict, and weights changed
+        since are not seen."""
+        if hold and not self.fp8:
+            raise ValueError("hold_fp8 is for a block with fp8=True")
+        self._held = None
+        if hold:
+            self._held = tuple(_fp8_weight(m.weight.detach(), False) for m in (self.up, self.down))
+        return self
+
+    def _product(self, x, module, k: int):
+        """x through up (k = 0) or down (1), without gradients."""
+        if not self.fp8:
+            return module(x)
+        if self._held is None:
+            return linear(x, module.weight, module.bias, fp8=True)
+        from .fp8 import gqs_fp8_linear
+        dtype = _product_dtype(x)
+        with _no_autocast(x):
+            x = _cast(x, dtype)
+            y = gqs_fp8_linear(_rows(x, x.shape[-1]), self._held[k], _cast(module.bias, dtype))
+        return y.view(*x.shape[:-1], y.shape[-1])
 
     def _pass_seed(self) -> int:
         if self.seed is not None:
@@ -770,11 +858,13 @@ class Mlp8(torch.nn.Module):
             self.passes += 1
             if own_norm and own_up and own_down:
                 return x + _Mlp8.apply(x, norm.weight, norm.bias, up.weight, up.bias, down.weight,
-                                       down.bias, norm.eps, self.approximate, seed)
+                                       down.bias, norm.eps, self.approximate, seed,
+                                       self.fp8)
         seeds = _copy_seeds(seed)
         a = (layer_norm(x, norm.weight, norm.bias, norm.eps, bits=bits, seed=seeds[0]) if own_norm
              else norm(x))
-        h = linear(a, up.weight, up.bias, seed=seeds[1]) if bits and own_up else up(a)
+        h = (up(a) if not own_up else self._product(a, up, 0) if not bits
+             else linear(a, up.weight, up.bias, seed=seeds[1], fp8=self.fp8))
         g = gelu(h, self.approximate, bits=bits, seed=seeds[2])
-        return x + (linear(g, down.weight, down.bias, seed=seeds[3]) if bits and own_down
-                    else down(g))
+        return x + (down(g) if not own_down else self._product(g, down, 1) if not bits
+                    else linear(g, down.weight, down.bias, seed=seeds[3], fp8=self.fp8))

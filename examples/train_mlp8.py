@@ -8,7 +8,9 @@ the gradients reduced by Global-QSGD.
 The task is synthetic: the blocks learn the output of a fixed random stack of
 the same shape.  Layer norm, GELU, the 8-bit copies and the weight gradients
 are the operators of `allreduce_compatible_gradient_amd.train`; what the backward pass
-leaves in DDP's buckets goes through `global_qsgd_hook`.  Each rank draws
+leaves in DDP's buckets goes through `global_qsgd_hook`.  With --fp8 the blocks'
+products are taken from e4m3 copies, and with --adamw the update is that of
+`allreduce_compatible_gradient_amd.optim`.  Each rank draws
 its own data and rounds its activations with its own seed, so that the ranks'
 rounding errors are independent and average out with their gradients.
 """
@@ -21,7 +23,7 @@ import torch
 import torch.distributed as dist
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
-from allreduce_compatible_gradient_amd import train  # noqa: E402
+from allreduce_compatible_gradient_amd import optim, train  # noqa: E402
 from allreduce_compatible_gradient_amd.ddp import GlobalQSGDState, global_qsgd_hook  # noqa: E402
 
 
@@ -29,8 +31,17 @@ def stack(args, rank: int, seed: int, device) -> torch.nn.Sequential:
     torch.manual_seed(seed)  # the same weights on every rank
     return torch.nn.Sequential(*[
         train.Mlp8(args.d, args.hidden, random=not args.nearest, seed=rank * args.blocks + i,
-                   device=device, dtype=torch.float32)
+                   device=device, dtype=torch.float32, fp8=args.fp8)
         for i in range(args.blocks)])
+
+
+def optimizer_of(args, parameters):
+    """torch's Adam, or AdamW of this package, which goes on from the reduced
+    gradients: clipped, with moments in 32 or 8 bits (of one seed on every
+    rank, so that the ranks stay equal)."""
+    if not args.adamw:
+        return torch.optim.Adam(parameters, lr=args.lr)
+    return optim.AdamW(parameters, lr=args.lr, weight_decay=0.0, bits=args.adamw, max_norm=args.clip)
 
 
 def run(args) -> list:
@@ -40,7 +51,7 @@ def run(args) -> list:
     model = torch.nn.parallel.DistributedDataParallel(
         stack(args, rank, 2, device), device_ids=[device.index])
     model.register_comm_hook(GlobalQSGDState(scheme="L", s=args.levels, seed=5), global_qsgd_hook)
-    optimizer = torch.optim.Adam(model.parameters(), lr=args.lr)
+    optimizer = optimizer_of(args, model.parameters())
     data = torch.Generator(device=device).manual_seed(100 + rank)
     losses = []
     for _ in range(args.steps):
@@ -65,6 +76,11 @@ def arguments(argv=None):
     p.add_argument("--lr", type=float, default=1e-3)
     p.add_argument("--levels", type=int, default=127, help="Global-L_s of the gradients")
     p.add_argument("--nearest", action="store_true", help="round the copies to nearest")
+    p.add_argument("--fp8", action="store_true",
+                   help="the blocks' products in e4m3 with a scale for each block of 128")
+    p.add_argument("--adamw", type=int, choices=(32, 8), default=0, metavar="BITS",
+                   help="this package's AdamW with moments in 32 or 8 bits")
+    p.add_argument("--clip", type=float, default=None, help="with --adamw: the gradients' norm")
     return p.parse_args(argv)
 
 

@@ -92,7 +92,7 @@ def rows(x: np.ndarray, seed=None):
         c[:, :, 2] = np.arange(n)[:, None]
         u = halves(c.reshape(-1, 4), seed).reshape(-1, 128)
     codes, exps = _blocks(v.reshape(-1, 128), u)
-    return codes.reshape(n, -1), exps.reshape(n, g).T
+    return codes.reshape(n, 128 * g), exps.reshape(n, g).T
 
 
 def rows_values(codes, exps, d):
