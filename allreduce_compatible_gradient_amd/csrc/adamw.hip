@@ -345,22 +345,26 @@ struct Range {
 };
 
 // Whether what the step writes overlaps: two lanes would update one element.
+// The ranges mostly come in order, as they were allocated, and sort at once.
 int32_t check_overlap(const gqs_tensor *tensors, int64_t count, int64_t p_bytes, int bits)
 {
     Range few[3 * kTensors], *all = few;
     if (count > kTensors && !(all = new (std::nothrow) Range[3 * count]))
         return fail(GQ_ERR_UNSUPPORTED, "%lld tensors", (long long)count);
     int64_t used = 0;
-    for (int64_t i = 0; i < count; ++i) {
-        const gqs_tensor &t = tensors[i];
-        if (t.n == 0)
-            continue;
-        const int64_t state = bits == 8 ? fp8_pitch(t.n) : 4 * t.n;
-        all[used++] = {(uintptr_t)t.p, (uintptr_t)t.p + (uintptr_t)(p_bytes * t.n)};
-        all[used++] = {(uintptr_t)t.m, (uintptr_t)t.m + (uintptr_t)state};
-        all[used++] = {(uintptr_t)t.v, (uintptr_t)t.v + (uintptr_t)state};
-    }
-    std::sort(all, all + used, [](const Range &a, const Range &b) { return a.begin < b.begin; });
+    const auto add = [&](const void *p, int64_t bytes) {
+        all[used++] = {(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes};
+    };
+    for (int which = 0; which < 3; ++which)
+        for (int64_t i = 0; i < count; ++i) {
+            const gqs_tensor &t = tensors[i];
+            const int64_t state = bits == 8 ? fp8_pitch(t.n) : 4 * t.n;
+            if (t.n > 0)
+                add(which == 0 ? t.p : which == 1 ? t.m : t.v, which == 0 ? p_bytes * t.n : state);
+        }
+    const auto before = [](const Range &a, const Range &b) { return a.begin < b.begin; };
+    if (!std::is_sorted(all, all + used, before))
+        std::sort(all, all + used, before);
     bool overlap = false;
     for (int64_t i = 1; i < used; ++i)
         overlap |= all[i].begin < all[i - 1].end;

@@ -15,7 +15,9 @@ the optimizer of torch's interface.
 """
 from __future__ import annotations
 
-import ctypes
+import itertools
+import operator
+import struct
 
 import torch
 
@@ -51,42 +53,55 @@ class Moment8:
         return f"Moment8({self.n}, {'second' if self.second else 'first'}, {self.codes.device})"
 
 
+# Lists of a hundred tensors and more are looked over in a few microseconds:
+# by maps of C functions, not tensor by tensor.
+_dtype_of, _index = operator.attrgetter("dtype"), torch.Tensor.get_device
+_numel, _data_ptr = torch.Tensor.numel, torch.Tensor.data_ptr
+_codes, _exps, _count = map(operator.attrgetter, ("codes", "exps", "n"))
+
+
 def _arrays(tensors, name: str, device, dtype=None):
     """(dtype, sizes, addresses) of contiguous device tensors of one dtype."""
-    for t in tensors:
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError(f"{name} must be device tensors")
-        if t.device != device:
-            raise ValueError(f"{name}: a tensor is on {t.device}, expected {device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    types = {t.dtype for t in tensors}
+    if not all(issubclass(kind, torch.Tensor) for kind in set(map(type, tensors))):
+        raise ValueError(f"{name} must be device tensors")
+    if set(map(_index, tensors)) != {device.index}:
+        raise ValueError(f"{name} must be on {device}, got {sorted({str(t.device) for t in tensors})}")
+    if not all(map(torch.Tensor.is_contiguous, tensors)):
+        raise ValueError(f"{name} must be contiguous")
+    types = set(map(_dtype_of, tensors))
     if len(types) > 1 or (dtype is not None and types != {dtype}):
         want = "one dtype" if dtype is None else str(dtype)
         raise TypeError(f"{name} must have {want}, got {sorted(map(str, types))}")
-    return types.pop(), [t.numel() for t in tensors], [t.data_ptr() for t in tensors]
+    return types.pop(), list(map(_numel, tensors)), list(map(_data_ptr, tensors))
 
 
 def _moments(moments, name: str, sizes, device, second: bool):
     """(bits, codes or values, exps) of a list of moments."""
     if len(moments) != len(sizes):
         raise ValueError(f"{len(moments)} {name}, {len(sizes)} tensors")
-    if not any(isinstance(m, Moment8) for m in moments):
+    kinds = set(map(type, moments))
+    if Moment8 not in kinds:
         _, counts, at = _arrays(moments, name, device, torch.float32)
         if counts != sizes:
             raise ValueError(f"{name} must have their parameters' sizes")
-        return 32, at, [0] * len(at)
-    if not all(isinstance(m, Moment8) for m in moments):
+        return 32, at, itertools.repeat(0)
+    if len(kinds) > 1:
         raise TypeError(f"{name} must be all Moment8 or all tensors")
-    if [m.n for m in moments] != sizes:
+    if list(map(_count, moments)) != sizes:
         raise ValueError(f"{name} must have their parameters' sizes")
     kind = torch.uint8 if second else _E4M3
-    _, counts, codes = _arrays([m.codes for m in moments], f"{name}' codes", device, kind)
-    _, groups, exps = _arrays([m.exps for m in moments], f"{name}' exps", device, torch.uint8)
-    blocks = [(n + 127) // 128 for n in sizes]
-    if groups != blocks or counts != [128 * b for b in blocks]:
+    _, counts, codes = _arrays(list(map(_codes, moments)), f"{name}' codes", device, kind)
+    _, groups, exps = _arrays(list(map(_exps, moments)), f"{name}' exps", device, torch.uint8)
+    blocks = [(n + 127) >> 7 for n in sizes]
+    if groups != blocks or counts != [b << 7 for b in blocks]:
         raise ValueError(f"{name} must hold a code for each of 128 G elements and G exps")
     return 8, codes, exps
+
+
+def _list(*columns) -> bytes:
+    """The C array of tensors whose seven columns these are."""
+    words = list(itertools.chain.from_iterable(zip(*columns)))
+    return struct.pack(f"{len(words)}Q", *words)
 
 
 def _scalar(t, name: str, dtype, device):
@@ -161,8 +176,7 @@ def gqs_adamw(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, betas=(0.9, 0.9
         args.step = step
     if args.lr_device or args.step_device:
         workspace = torch.empty(16, dtype=torch.uint8, device=device)
-    words = [w for t in zip(p_at, g_at, m_at, v_at, m_exps, v_exps, sizes) for w in t]
-    check(lib().gqs_adamw((ctypes.c_uint64 * len(words))(*words), len(sizes),
+    check(lib().gqs_adamw(_list(p_at, g_at, m_at, v_at, m_exps, v_exps, sizes), len(sizes),
                           _dtype(p_type, "params"), _dtype(g_type, "grads"), args,
                           None if workspace is None else workspace.data_ptr(), 16,
                           _current(device)))
@@ -198,8 +212,8 @@ def gqs_grad_norm(grads, *, max_norm=None, stream=None):
         with _Elsewhere(device, stream, grads):
             return gqs_grad_norm(grads, max_norm=max_norm)
     kind, sizes, at = _arrays(grads, "grads", device)
-    words = [w for g, n in zip(at, sizes) for w in (0, g, 0, 0, 0, 0, n)]
-    tensors = (ctypes.c_uint64 * len(words))(*words)
+    none = itertools.repeat(0)
+    tensors = _list(none, at, none, none, none, none, sizes)
     need = lib().gqs_grad_norm_workspace_bytes(tensors, len(sizes))
     workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
     out = torch.empty(2, dtype=torch.float32, device=device)
