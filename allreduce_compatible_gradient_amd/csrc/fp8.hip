@@ -195,19 +195,6 @@ struct Squares {
     }
 };
 
-__device__ __forceinline__ i32x8 load_fragment(const uint8_t *p)
-{
-    const u32x4 a = *reinterpret_cast<const u32x4 *>(p);
-    const u32x4 b = *reinterpret_cast<const u32x4 *>(p + 16);
-    i32x8 f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        f[k] = (int)a[k];
-        f[4 + k] = (int)b[k];
-    }
-    return f;
-}
-
 // Eight of a fragment's values times their step in bf16, where they are exact.
 __device__ __forceinline__ bf16x8 widen(const i32x8 &f, int part, float step)
 {
@@ -253,42 +240,92 @@ struct Bytes<8> {
     }
 };
 
-// Row `row`'s 32 columns from `col` on of x as its copy holds them, made of
-// what load_ahead read: lanes r, r + 16, r + 32 and r + 48 have the block's
-// four parts.
-template <typename T>
-__device__ __forceinline__ i32x8 make_fragment(Raw8<T> (&raw)[4], const T *p, int32_t row,
-                                               int32_t col, int32_t d, int32_t random, uint32_t k0,
-                                               uint32_t k1, uint32_t &e)
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+
+// Loads from memory to LDS: `to` and what follows it for the other lanes.  In
+// assembly, for the compiler makes every read of LDS wait for such loads,
+// wherever they go, and does not count others behind them: a wait of ours has
+// to come before the reads.
+// Lanes past the descriptor's end give zeros.
+__device__ __forceinline__ void load_lds16(uint32_t to, const u32x4 &from, uint32_t at, uint32_t base)
 {
-    float v[4][8];
-    uint32_t m = 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        settle(p, col + 8 * q, d, raw[q]);
-        unpack(raw[q], v[q]);
-        m = max(m, abs_bits(v[q]));
-    }
-    m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-    m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-    e = e4m3_exponent(m);
-    i32x8 f = {};
-    if (e == 255u)
-        return f;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        u32x2 w;
-        if (random)
-            w = e4m3_random8(v[q], e,
-                             philox10(make_uint4(((uint32_t)col >> 3) + q, 0u, (uint32_t)row, 0u),
-                                      k0, k1));
-        else
-            w = e4m3_nearest8(v[q], e);
-        f[2 * q] = (int)w[0];
-        f[2 * q + 1] = (int)w[1];
-    }
-    return f;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(to), "v"(at), "s"(from), "s"(base) : "memory");
 }
+__device__ __forceinline__ void load_lds4(uint32_t to, const u32x4 &from, uint32_t at, uint32_t base)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                 :: "s"(to), "v"(at), "s"(from), "s"(base) : "memory");
+}
+__device__ __forceinline__ void load_lds1(uint32_t to, const u32x4 &from, uint32_t at, uint32_t base)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, %3 offen lds"
+                 :: "s"(to), "v"(at), "s"(from), "s"(base) : "memory");
+}
+
+__device__ __forceinline__ u32x4 descriptor(const uint8_t *p, uint32_t bytes)
+{
+    const uint64_t at = (uint64_t)p;
+    return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32)),
+                 (uint32_t)__builtin_amdgcn_readfirstlane(bytes), 0x00020000u};
+}
+
+// How rows of 128 bytes lie in LDS.  It gives 256 bytes a cycle, sixteen lanes
+// their sixteen bytes.  A lane's F rows lie in F lines of 128 bytes, for the
+// second eight of sixteen lanes with neighbours changed about, and a row's
+// sixteen-byte pieces at their number xor the lane's, so that the lanes of a
+// fragment's read, F rows apart, find all banks.
+template <int F>
+struct Order { // what the lane of rows F r on does to its lines' and pieces' numbers
+    static __device__ __forceinline__ int change(int r) { return F > 1 ? r >> 3 & 1 : 0; }
+    static __device__ __forceinline__ int turn(int r) { return F > 1 ? r & 7 : r >> 1 & 7; }
+};
+
+// A block of 16 F rows of an operand, in a wave's own part of LDS.
+template <int F>
+struct Strip {
+    static constexpr int kBytes = 16 * F * 128, kLoads = 2 * F;
+
+    // Where the lane's pieces lie, from the first row on; rows from `rows` on
+    // are the last.
+    static __device__ __forceinline__ void offsets(uint32_t (&at)[kLoads], int lane, int32_t rows,
+                                                   int64_t pitch)
+    {
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) {
+            const int line = 8 * q + lane / 8;
+            const int row = line ^ Order<F>::change(line / F);
+            const int piece = (lane & 7) ^ Order<F>::turn(line / F);
+            at[q] = (uint32_t)(min(row, rows - 1) * pitch) + 16 * piece;
+        }
+    }
+    static __device__ __forceinline__ void load(uint32_t to, const u32x4 &from,
+                                                const uint32_t (&at)[kLoads], int32_t step)
+    {
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q)
+            load_lds16(to + 1024 * q, from, at[q], 128 * step);
+    }
+    static __device__ __forceinline__ i32x8 fragment(uint32_t strip, int i, int lane)
+    {
+        const int r = lane & 15;
+        const uint32_t at = strip + r * F * 128 + 128 * Order<F>::change(r) +
+                            16 * (Order<F>::turn(r) ^ (lane >> 4 << 1));
+        const uint32_t of = 128 * (i & 1), beyond = 128 * (i & ~1);
+        const u32x4 a = *(const lds_u32x4 *)(uintptr_t)((at ^ of) + beyond);
+        const u32x4 b = *(const lds_u32x4 *)(uintptr_t)((at ^ (of + 16)) + beyond);
+        i32x8 f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            f[k] = (int)a[k];
+            f[4 + k] = (int)b[k];
+        }
+        return f;
+    }
+};
 
 template <typename O>
 __device__ __forceinline__ void store_one(O *p, float v) { *p = (O)v; }
@@ -320,128 +357,147 @@ struct Product {
     uint32_t k0, k1;
 };
 
-// A block has 16 FM rows and 16 FN columns of y; its waves take the depth's
-// blocks in turn and add their sums in LDS.  Fragments come straight from
-// memory.  MADE: x's copy is made on the way (FM = 1).
-template <typename T, int FM, int FN, bool MADE>
-__global__ __launch_bounds__(FM * FN >= 8 ? 512 : 1024) void k_product_split(const Product a, T *__restrict__ y)
+// Few rows: a block has 16 F rows and 16 columns of y; its waves take the
+// depth's blocks in turn, STEPS at once, each through LDS of its own, where
+// loads of whole lines put them (lanes that load fragments straight from
+// memory, sixteen rows at once, take four times as long), and add their sums
+// at the end.  MADE: x's copy is made on the way, sixteen lanes a row (F = 1).
+template <typename T, int F, int STEPS, bool MADE>
+__global__ __launch_bounds__(F > 2 ? 512 : 1024) void k_product_direct(const Product a,
+                                                                       T *__restrict__ y)
 {
     constexpr bool kExact = sizeof(T) == 4;
-    extern __shared__ __align__(16) float sums[];
+    using X = Strip<F>;
+    using W = Strip<1>;
+    constexpr int kStep = X::kBytes + W::kBytes;
+    extern __shared__ __align__(1024) uint8_t lds[];
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const uint32_t tm = divide(blockIdx.x, a.by_tiles);
-    const int32_t col0 = (int32_t)(blockIdx.x - tm * a.by_tiles.d) * 16 * FN;
-    const int64_t row0 = (int64_t)tm * 16 * FM;
-    const uint8_t *xp[FM], *wp[FN];
+    const int32_t col0 = (int32_t)(blockIdx.x - tm * a.by_tiles.d) * 16;
+    const int64_t row0 = (int64_t)tm * 16 * F;
+    const int32_t rows = (int32_t)min(a.m - row0, (int64_t)16 * F), cols = min(a.cols - col0, 16);
+    const uint32_t own = (uint32_t)(uintptr_t)(lds_u8 *)lds + wave * STEPS * kStep;
+
+    uint32_t w_at[W::kLoads], x_at[X::kLoads];
+    W::offsets(w_at, lane, cols, a.w.pitch);
+    const u32x4 w_from =
+        descriptor(a.w.codes + col0 * a.w.pitch, (uint32_t)cols * (uint32_t)a.w.pitch);
+    u32x4 x_from{};
+    const uint8_t *ep = nullptr;
+    if constexpr (!MADE) {
+        X::offsets(x_at, lane, rows, a.x.pitch);
+        x_from = descriptor(a.x.codes + row0 * a.x.pitch, (uint32_t)rows * (uint32_t)a.x.pitch);
+        // a tile's last rows may have no bytes: they are not stored
+        ep = a.x.exps + min(row0 + F * r, a.epitch - F);
+    }
+    f32x4 acc[F] = {};
+    for (int32_t s0 = wave * STEPS; s0 < a.blocks; s0 += waves * STEPS) {
+        const int32_t steps = min(STEPS, a.blocks - s0);
+        Bytes<F> ex[STEPS];
+        uint32_t ew[STEPS];
+        Raw8<T> raw[STEPS][4];
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); // what lay there has been read
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
-        xp[i] = MADE ? nullptr : a.x.codes + min(row0 + FM * r + i, a.m - 1) * a.x.pitch + 32 * g;
+        for (int p = 0; p < STEPS; ++p) {
+            if (p >= steps)
+                break;
+            const uint32_t to = own + p * kStep;
+            W::load(to, w_from, w_at, s0 + p);
+            if constexpr (MADE) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-        wp[j] = a.w.codes + (int64_t)min(col0 + FN * r + j, a.cols - 1) * a.w.pitch + 32 * g;
-    const int64_t made_row = min(row0 + r, a.m - 1);
-    const T *const raw = MADE ? (const T *)a.raw + made_row * a.ldx : nullptr;
-    // a tile's last rows may have no bytes: they are not stored, and read others'
-    const uint8_t *const ep = MADE ? nullptr : a.x.exps + min(row0 + FM * r, a.epitch - FM);
-    f32x4 acc[FM][FN] = {};
-    struct Step {
-        i32x8 fx[FM], fw[FN];
-        Raw8<T> raw[4];
-        Bytes<FM> ex;
-        uint32_t ew;
-    };
-    const auto fetch = [&](Step &k, int32_t s) GQT_INLINE {
+                for (int i = 0; i < 4; ++i) // row 4 i + g
+                    if (4 * i < rows)
+                        load_ahead((const T *)a.raw + min(row0 + 4 * i + g, a.m - 1) * a.ldx,
+                                   128 * (s0 + p) + 8 * r, a.depth, raw[p][i]);
+            } else {
+                X::load(to + W::kBytes, x_from, x_at, s0 + p);
+                ex[p] = *reinterpret_cast<const Bytes<F> *>(ep + (s0 + p) * a.epitch);
+            }
+            ew[p] = a.squares.at(col0 >> 7, s0 + p);
+        }
         if constexpr (MADE) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                load_ahead(raw, 128 * s + 32 * g + 8 * q, a.depth, k.raw[q]);
-        } else {
+            for (int p = 0; p < STEPS; ++p) {
+                if (p >= steps)
+                    break;
+                uint32_t of_row = 0; // lane r: the exponent of row r
 #pragma unroll
-            for (int i = 0; i < FM; ++i)
-                k.fx[i] = load_fragment(xp[i] + 128 * (int64_t)s);
-            k.ex = *reinterpret_cast<const Bytes<FM> *>(ep + s * a.epitch);
+                for (int i = 0; i < 4; ++i) {
+                    if (4 * i >= rows)
+                        break;
+                    const int32_t row = 4 * i + g, col = 128 * (s0 + p) + 8 * r;
+                    float v[8];
+                    settle((const T *)a.raw + min(row0 + row, a.m - 1) * a.ldx, col, a.depth,
+                           raw[p][i]);
+                    unpack(raw[p][i], v);
+                    const uint32_t e = e4m3_exponent(row16_max(abs_bits(v)));
+                    u32x2 w = {0, 0};
+                    if (e != 255u)
+                        w = a.random
+                                ? e4m3_random8(v, e,
+                                               philox10(make_uint4((uint32_t)col >> 3, 0u,
+                                                                   (uint32_t)(row0 + row), 0u),
+                                                        a.k0, a.k1))
+                                : e4m3_nearest8(v, e);
+                    const uint32_t at = own + p * kStep + W::kBytes + row * 128 +
+                                        16 * ((r >> 1) ^ Order<1>::turn(row)) + 8 * (r & 1);
+                    *(lds_u32x2 *)(uintptr_t)at = w;
+                    const uint32_t other = (uint32_t)__shfl((int)e, 16 * (r & 3));
+                    of_row = r >> 2 == i ? other : of_row;
+                }
+                ex[p].b = (uint8_t)of_row;
+            }
         }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-            k.fw[j] = load_fragment(wp[j] + 128 * (int64_t)s);
-        k.ew = a.squares.at(col0 >> 7, s);
-    };
-    const auto multiply = [&](Step &k, int32_t s) GQT_INLINE {
-        uint32_t ex[FM];
-        if constexpr (MADE) {
-            k.fx[0] = make_fragment(k.raw, raw, (int32_t)made_row, 128 * s + 32 * g, a.depth,
-                                    a.random, a.k0, a.k1, ex[0]);
-        } else {
+        for (int p = 0; p < STEPS; ++p) {
+            if (p >= steps)
+                break;
+            const uint32_t at = own + p * kStep;
+            const i32x8 fw = W::fragment(at, 0, lane);
+            bf16x8 wide[4];
+            if constexpr (kExact) {
 #pragma unroll
-            for (int i = 0; i < FM; ++i)
-                ex[i] = k.ex.byte(i);
-        }
-        if constexpr (kExact) {
+                for (int part = 0; part < 4; ++part)
+                    wide[part] = widen(fw, part, step_of(ew[p]));
+            }
 #pragma unroll
-            for (int part = 0; part < 4; ++part) {
-                bf16x8 bw[FN];
+            for (int i = 0; i < F; ++i) {
+                const i32x8 fx = X::fragment(at + W::kBytes, i, lane);
+                if constexpr (kExact) {
 #pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    bw[j] = widen(k.fw[j], part, step_of(k.ew));
-#pragma unroll
-                for (int i = 0; i < FM; ++i) {
-                    const bf16x8 bx = widen(k.fx[i], part, step_of(ex[i]));
-#pragma unroll
-                    for (int j = 0; j < FN; ++j)
-                        acc[i][j] =
-                            __builtin_amdgcn_mfma_f32_16x16x32_bf16(bx, bw[j], acc[i][j], 0, 0, 0);
+                    for (int part = 0; part < 4; ++part)
+                        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            widen(fx, part, step_of(ex[p].byte(i))), wide[part], acc[i], 0, 0, 0);
+                } else {
+                    acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        fx, fw, acc[i], 0, 0, 0, (int)ex[p].byte(i), 0, (int)ew[p]);
                 }
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        k.fx[i], k.fw[j], acc[i][j], 0, 0, 0, (int)ex[i], 0, (int)k.ew);
-        }
-    };
-    // The next of the wave's blocks is on its way while one is multiplied.
-    Step one, two;
-    if (wave < a.blocks)
-        fetch(one, wave);
-    for (int32_t s = wave; s < a.blocks; s += 2 * waves) {
-        if (s + waves < a.blocks)
-            fetch(two, s + waves);
-        multiply(one, s);
-        if (s + waves < a.blocks) {
-            if (s + 2 * waves < a.blocks)
-                fetch(one, s + 2 * waves);
-            multiply(two, s + waves);
         }
     }
-    // sums[wave][i][q][lane][j]
+    // sums[wave][i][q][lane], where the blocks were
+    float *const sums = reinterpret_cast<float *>(lds);
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < F; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-                sums[((wave * FM + i) * 4 + q) * 64 * FN + lane * FN + j] = acc[i][j][q];
+            sums[((wave * F + i) * 4 + q) * 64 + lane] = acc[i][q];
     __syncthreads();
-    for (int at = threadIdx.x; at < FM * 4 * 64; at += blockDim.x) {
+    for (int at = threadIdx.x; at < F * 4 * 64; at += blockDim.x) {
         const int l = at & 63, q = at >> 6 & 3, i = at >> 8;
-        const int64_t row = row0 + FM * (4 * (l >> 4) + q) + i;
-        const int32_t col = col0 + FN * (l & 15);
-        if (row >= a.m)
+        const int64_t row = row0 + F * (4 * (l >> 4) + q) + i;
+        const int32_t col = col0 + (l & 15);
+        if (row >= a.m || col >= a.cols)
             continue;
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            float v = 0.0f;
-            for (int w = 0; w < waves; ++w)
-                v += sums[((w * FM + i) * 4 + q) * 64 * FN + l * FN + j];
-            if (col + j < a.cols) {
-                if (a.bias)
-                    v += bias_at(a.bias, a.bias_dtype, col + j);
-                store_one(y + row * a.cols + col + j, v);
-            }
-        }
+        float v = 0.0f;
+        for (int w = 0; w < waves; ++w)
+            v += sums[((w * F + i) * 4 + q) * 64 + l];
+        if (a.bias)
+            v += bias_at(a.bias, a.bias_dtype, col);
+        store_one(y + row * a.cols + col, v);
     }
 }
 
@@ -453,34 +509,8 @@ __global__ __launch_bounds__(FM * FN >= 8 ? 512 : 1024) void k_product_split(con
 // lane).  A block goes from tile to tile without a pause in its loads.
 //
 // With F fragments, row F (l % 32) + i of a wave's rows belongs to fragment i.
-// LDS gives 256 bytes a cycle, sixteen lanes their sixteen bytes.  A lane's F
-// rows lie in F lines of 128 bytes, for the second eight of sixteen lanes with
-// neighbours changed about, and a row's sixteen-byte pieces at their number xor
-// the lane's modulo 8, so that the lanes of a fragment's read find all banks.
 
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
-typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-// Loads from memory to LDS: `to` and what follows it for the other lanes.  In
-// assembly, for the compiler makes every read of LDS wait for such loads,
-// wherever they go, and does not count others behind them; land() waits.
-// Lanes past the descriptor's end give zeros.
-__device__ __forceinline__ void load_lds16(uint32_t to, const u32x4 &from, uint32_t at, uint32_t base)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(to), "v"(at), "s"(from), "s"(base) : "memory");
-}
-__device__ __forceinline__ void load_lds4(uint32_t to, const u32x4 &from, uint32_t at, uint32_t base)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-                 :: "s"(to), "v"(at), "s"(from), "s"(base) : "memory");
-}
-__device__ __forceinline__ void load_lds1(uint32_t to, const u32x4 &from, uint32_t at, uint32_t base)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, %3 offen lds"
-                 :: "s"(to), "v"(at), "s"(from), "s"(base) : "memory");
-}
 
 // Until all but the last LEFT of this wave's loads have landed, and all waves
 // are here with their reads of LDS done.
@@ -490,21 +520,9 @@ __device__ __forceinline__ void land()
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
 }
 
-__device__ __forceinline__ u32x4 descriptor(const uint8_t *p, uint32_t bytes)
-{
-    const uint64_t at = (uint64_t)p;
-    return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at),
-                 (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32)),
-                 (uint32_t)__builtin_amdgcn_readfirstlane(bytes), 0x00020000u};
-}
-
 template <int F, int ROWS, int WAVES>
 struct Panel { // an operand's step
     static constexpr int kBytes = ROWS * 128, kLoads = ROWS / 8 / WAVES;
-
-    // What the lane of rows F r on does to its lines' and pieces' numbers.
-    static __device__ __forceinline__ int change(int r) { return F > 1 ? r >> 3 & 1 : 0; }
-    static __device__ __forceinline__ int turn(int r) { return F > 1 ? r & 7 : r >> 1 & 7; }
 
     // Where this lane's pieces of the wave's loads lie, from the first row on.
     static __device__ __forceinline__ void offsets(uint32_t (&at)[kLoads], int wave, int lane,
@@ -513,7 +531,8 @@ struct Panel { // an operand's step
 #pragma unroll
         for (int q = 0; q < kLoads; ++q) {
             const int line = 8 * (kLoads * wave + q) + lane / 8;
-            const int row = line ^ change(line / F), piece = (lane & 7) ^ turn(line / F);
+            const int row = line ^ Order<F>::change(line / F);
+            const int piece = (lane & 7) ^ Order<F>::turn(line / F);
             at[q] = (uint32_t)(row * pitch) + 16 * piece;
         }
     }
@@ -522,7 +541,8 @@ struct Panel { // an operand's step
     static __device__ __forceinline__ uint32_t lines(int half, int lane)
     {
         const int r = lane & 31;
-        return (32 * half + r) * F * 128 + 128 * change(r) + 16 * (turn(r) ^ (lane >> 5 << 1));
+        return (32 * half + r) * F * 128 + 128 * Order<F>::change(r) +
+               16 * (Order<F>::turn(r) ^ (lane >> 5 << 1));
     }
 
     // Half u of fragment i.
@@ -937,18 +957,18 @@ int32_t allow_lds(K *kernel, const char *name, uint32_t bytes)
     return e == hipSuccess ? GQ_OK : fail(GQ_ERR_DEVICE, "%s: %s", name, hipGetErrorString(e));
 }
 
-template <typename T, int FM, int FN, bool MADE>
-int32_t launch_split(Product a, T *y, hipStream_t st)
+template <typename T, int F, int STEPS, bool MADE>
+int32_t launch_direct(Product a, T *y, hipStream_t st)
 {
-    a.by_tiles = fast_div((uint32_t)((a.cols + 16 * FN - 1) / (16 * FN))); // of a row of them
-    const int64_t grid = (a.m + 16 * FM - 1) / (16 * FM) * a.by_tiles.d;
-    const int waves = std::min(FM * FN >= 8 ? 8 : 16, std::max(1, (int)a.blocks));
-    const uint32_t lds = (uint32_t)waves * FM * FN * 1024;
+    a.by_tiles = fast_div((uint32_t)((a.cols + 15) / 16)); // of a row of them
+    const int64_t grid = (a.m + 16 * F - 1) / (16 * F) * a.by_tiles.d;
+    const int waves = std::min(F > 2 ? 8 : 16, std::max(1, (a.blocks + STEPS - 1) / STEPS));
+    const uint32_t lds = (uint32_t)(waves * STEPS * (Strip<F>::kBytes + Strip<1>::kBytes));
     if (grid >= ((int64_t)1 << 31) / (64 * 16))
         return fail(GQ_ERR_UNSUPPORTED, "%lld tiles", (long long)grid);
-    GQT_TRY(allow_lds(&k_product_split<T, FM, FN, MADE>, "k_product_split", lds));
-    k_product_split<T, FM, FN, MADE><<<(uint32_t)grid, 64 * waves, lds, st>>>(a, y);
-    return check_launch("k_product_split");
+    GQT_TRY(allow_lds(&k_product_direct<T, F, STEPS, MADE>, "k_product_direct", lds));
+    k_product_direct<T, F, STEPS, MADE><<<(uint32_t)grid, 64 * waves, lds, st>>>(a, y);
+    return check_launch("k_product_direct");
 }
 
 constexpr int kCUs = 256;
@@ -982,39 +1002,43 @@ constexpr Cost kCosts[2][kWays] = {
     {{}, {64, 128, kCUs, 0.34f, 1.4f}, {128, 128, kCUs, 0.55f, 1.8f},
      {128, 128, 2 * kCUs, 0.9f, 4.4f}, {256, 256, kCUs, 1.6f, 5.8f}, {}},
 };
-constexpr Cost kDirectCosts[4] = { // of 16, 32, 64 and 128 rows: one block of loads a wave
-    {16, 16, kCUs, 0.1f, 0.2f}, {32, 16, kCUs, 0.16f, 0.2f}, {64, 16, kCUs, 0.26f, 0.2f},
-    {128, 16, kCUs, 0.43f, 0.3f}};
+constexpr Cost kDirectCosts[3] = { // of 32, 64 and 128 rows
+    {32, 16, kCUs, 0.08f, 0.2f}, {64, 16, kCUs, 0.13f, 0.2f}, {128, 16, kCUs, 0.24f, 1.7f}};
 
 // What costs least: rounds of tiles, and, where the depth is split, a second
 // kernel that adds up the parts.  Microseconds in a graph, the ways forced: bf16
 // 4096 x 1024 x 1024 Rows64 11.3, Square128 9.2, Square128x2 10.7, Square256
 // 17.7; 2048 x 4096 x 4096 53, 40, 36, 51; 8192 x 4096 x 1024 71, 51, 50, 40;
-// 512 x 4096 x 4096 15.6, 20.9, 24.7, 29; 96 x 1024 x 4096 10.1, 11.7, 13.9,
-// 16.7, directly 17; 96 x 1024 x 1024 6.2, 9.7, 10.3, 12.5, 6.7.  fp32 8192 x
-// 4096 x 1024 Rows64 110, Square128 83, Wide256 70; 1024 x 4096 x 4096 46, 36,
-// 42; 96 x 1024 x 1024 9.5, 10.2, 11.4, directly 7.1.
+// 512 x 4096 x 4096 15.6, 20.9, 24.7, 29.  fp32 8192 x 4096 x 1024 Rows64 110,
+// Square128 83, Wide256 70; 1024 x 4096 x 4096 46, 36, 42.  Directly and by the
+// best tiles: bf16 64 x 4096 x 4096 7.0, 10.9; 128 x 4096 x 4096 12.0, 13.7;
+// 256 x 4096 x 4096 20.3, 13.9; 64 x 8192 x 8192 19.1, 17.5.
 Plan plan_of(int64_t m, int64_t cols, int64_t depth, int32_t dtype)
 {
     const int64_t blocks = blocks_of(depth);
     Plan best{kDirect, 1, 0};
     if (m <= 16)
         return best;
-    const auto time = [&](const Cost &c, int64_t z) {
-        const int64_t tiles = ((m + c.rows - 1) / c.rows) * ((cols + c.cols - 1) / c.cols);
-        const int64_t rounds = (tiles * z + c.at_once - 1) / c.at_once;
-        const float sums = z > 1 ? 2.5f + (float)(z * m * cols) * 1.5e-6f : 0.0f;
-        return (float)rounds * ((float)((blocks + z - 1) / z) * c.step + c.tile) + sums;
+    const auto tiles_of = [&](const Cost &c) {
+        return ((m + c.rows - 1) / c.rows) * ((cols + c.cols - 1) / c.cols);
     };
-    float least = time(kDirectCosts[m <= 32 ? 1 : m <= 64 ? 2 : 3], 1);
+    const auto time = [&](const Cost &c, int64_t z, float step) {
+        const int64_t rounds = (tiles_of(c) * z + c.at_once - 1) / c.at_once;
+        const float sums = z > 1 ? 3.5f + (float)(z * m * cols) * 1.5e-6f : 0.0f;
+        return (float)rounds * ((float)((blocks + z - 1) / z) * step + c.tile) + sums;
+    };
+    // few blocks of direct loads have more of the L2 each
+    const Cost &direct = kDirectCosts[m <= 32 ? 0 : m <= 64 ? 1 : 2];
+    const float full = std::min(1.0f, (float)tiles_of(direct) / (float)kCUs);
+    float least = time(direct, 1, direct.step * (0.55f + 0.45f * full));
     for (int way = kRows64; way < kWays; ++way) {
         const Cost &c = kCosts[dtype == GQ_IN_BF16][way];
         if (!c.at_once)
             continue;
         for (int32_t z = 1; z <= 16 && z <= blocks; ++z) {
-            if (z > 1 && ((m + c.rows - 1) / c.rows) * ((cols + c.cols - 1) / c.cols) * z > c.at_once)
+            if (z > 1 && tiles_of(c) * z > c.at_once)
                 break;
-            const float us = time(c, z);
+            const float us = time(c, z, c.step);
             if (us < least) {
                 least = us;
                 best = {(Way)way, z, z > 1 ? 4 * z * m * cols : 0};
@@ -1083,14 +1107,15 @@ int32_t launch_product(const Product &a, Way way, void *y, hipStream_t st)
     default:
         break;
     }
+    constexpr int kSteps = sizeof(T) == 4 ? 1 : 2; // fp32 rows leave no registers for two
     if (a.m <= 16)
-        return a.raw ? launch_split<T, 1, 1, true>(a, out, st)
-                     : launch_split<T, 1, 1, false>(a, out, st);
+        return a.raw ? launch_direct<T, 1, kSteps, true>(a, out, st)
+                     : launch_direct<T, 1, kSteps, false>(a, out, st);
     if (a.m <= 32)
-        return launch_split<T, 2, 1, false>(a, out, st);
+        return launch_direct<T, 2, 1, false>(a, out, st);
     if (a.m <= 64)
-        return launch_split<T, 4, 1, false>(a, out, st);
-    return launch_split<T, 8, 1, false>(a, out, st);
+        return launch_direct<T, 4, 1, false>(a, out, st);
+    return launch_direct<T, 8, 1, false>(a, out, st);
 }
 
 int32_t check_product(int32_t dtype, int64_t m, int64_t cols, int64_t depth, const void *w_codes,

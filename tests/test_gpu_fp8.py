@@ -362,3 +362,39 @@ def test_offsets_past_32_bits():
     want = x[at].float().sum(dim=1)
     assert torch.equal(y[at].float(), want[:, None].expand(-1, n))
     assert not y[m - 129:m - 1].any() and not y[6:1000].any()
+
+
+# sizes that reach every way of the product, and the depth's split, at one
+# fragment more and less than whole tiles
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(4097, 4100, 130), (4095, 8191, 70), (2049, 4097, 400),
+                                   (1023, 1025, 1100), (300, 2050, 3000), (129, 129, 5000),
+                                   (65, 300, 4100), (20, 60, 9000), (8200, 260, 256)])
+def test_every_way(m, n, k, dtype):
+    """Whole numbers, whose sums are exact in any order: y and dx against
+    plain products."""
+    g = torch.Generator(device=DEV).manual_seed(m + n + k)
+
+    def draw_whole(rows, cols):
+        x = torch.randint(-2, 3, (rows, cols), device=DEV, generator=g).float()
+        return x * (torch.rand(rows, cols, device=DEV, generator=g) < 0.2)
+    x, w, dy = draw_whole(m, k), draw_whole(n, k), draw_whole(m, n)
+    w8 = fp8.gqs_fp8_weight(w.to(DT[dtype]))
+    for got, want in ((fp8.gqs_fp8_linear(x.to(DT[dtype]), w8), x @ w.t()),
+                      (fp8.gqs_fp8_linear(dy.to(DT[dtype]), w8, transposed=True), dy @ w)):
+        # products are at most 4, so no sum of eight is cut off; bf16 holds
+        # whole numbers up to 256
+        assert torch.equal(got.float(), want.to(DT[dtype]).float())
+        assert want.abs().max() > 8
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 1, 20000), (40, 1, 20000), (300, 1, 6000), (1, 20000, 1),
+                                   (20000, 1, 1), (3000, 3, 3)])
+def test_narrow_products(m, n, k):
+    x = torch.ones(m, k, device=DEV, dtype=torch.bfloat16)
+    x[-1] = 2
+    w8 = fp8.gqs_fp8_weight(torch.ones(n, k, device=DEV, dtype=torch.bfloat16))
+    y = fp8.gqs_fp8_linear(x, w8).float()
+    want = torch.full((m, n), float(k), device=DEV)
+    want[-1] *= 2
+    assert torch.equal(y, want.bfloat16().float())
