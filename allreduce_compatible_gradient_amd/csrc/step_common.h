@@ -13,6 +13,7 @@ namespace gqt {
 
 constexpr int64_t kMaxSide = (int64_t)1 << 22;
 constexpr int64_t kMaxRows = (int64_t)1 << 31;
+constexpr int64_t kMaxBlocks = (int64_t)1 << 27; // of 128: a launch has fewer than 2^32 threads
 
 inline int64_t blocks_of(int64_t d) { return (d + 127) / 128; }
 inline int64_t fp8_pitch(int64_t d) { return 128 * blocks_of(d); }
@@ -78,22 +79,48 @@ __device__ __forceinline__ u32x2 e4m3_nearest8(const float (&v)[8], uint32_t e)
 
 // Random rounding of x >= 0 whose code is the leading bits of x 2^scale, which
 // may be subnormal, above 20 that are rounded off: u enters above a half of
-// their last place.
+// their last place.  The code is byte 2 of the result.
 __device__ __forceinline__ uint32_t random_code(float x, int scale, uint32_t u)
 {
-    return (__float_as_uint(ldexpf(x, scale)) + (u << 4 | 8u)) >> 20;
+    return ((__float_as_uint(ldexpf(x, scale)) + 8u) >> 4) + u;
+}
+
+// Byte 2 of each of four, in their order.
+__device__ __forceinline__ uint32_t third_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    return perm(perm(d, c, 0x0C0C0602u), perm(b, a, 0x0C0C0602u), 0x05040100u);
+}
+
+// Bytes above `top` become it.  For the exponents whose upper numbers have no
+// float, so hardly ever.
+__device__ __forceinline__ uint32_t cap_bytes(uint32_t w, uint32_t top)
+{
+    uint32_t r = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        r |= min(w >> (8 * k) & 0xFFu, top) << (8 * k);
+    return r;
 }
 
 // The codes of eight values at random, with their signs.
 __device__ __forceinline__ u32x2 e4m3_random8(const float (&v)[8], uint32_t e, const uint4 &draw)
 {
     const int scale = 7 - (int)e; // 2^-120 x 2^-E: the least normal number, 2^-6, becomes 2^-126
-    const uint32_t top = e == kHighestE4m3 ? 0x77u : 0x7Eu;
-    u32x2 w = {0, 0};
+    u32x2 w;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const uint32_t c = min(random_code(fabsf(v[k]), scale, half16(draw, k)), top);
-        w[k >> 2] |= (c | (__float_as_uint(v[k]) >> 24 & 0x80u)) << (8 * (k & 3));
+    for (int h = 0; h < 2; ++h) {
+        uint32_t t[4], b[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            t[k] = random_code(fabsf(v[4 * h + k]), scale, half16(draw, 4 * h + k));
+            b[k] = __float_as_uint(v[4 * h + k]);
+        }
+        w[h] = third_bytes(t[0], t[1], t[2], t[3]);
+        if (e == kHighestE4m3)
+            w[h] = cap_bytes(w[h], 0x77u);
+        const uint32_t top = perm(perm(b[3], b[2], 0x0C0C0703u), perm(b[1], b[0], 0x0C0C0703u),
+                                  0x05040100u);
+        w[h] |= top & 0x80808080u;
     }
     return w;
 }
@@ -102,11 +129,17 @@ __device__ __forceinline__ u32x2 e4m3_random8(const float (&v)[8], uint32_t e, c
 __device__ __forceinline__ u32x2 e5m3_random8(const float (&v)[8], uint32_t e, const uint4 &draw)
 {
     const int scale = 16 - (int)e; // 2^-111 x 2^-E: 2^-15 becomes 2^-126
-    const uint32_t top = e == kHighestE5m3 ? 0xF7u : 0xFFu;
-    u32x2 w = {0, 0};
+    u32x2 w;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-        w[k >> 2] |= min(random_code(v[k], scale, half16(draw, k)), top) << (8 * (k & 3));
+    for (int h = 0; h < 2; ++h) {
+        uint32_t t[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            t[k] = random_code(v[4 * h + k], scale, half16(draw, 4 * h + k));
+        w[h] = third_bytes(t[0], t[1], t[2], t[3]);
+        if (e == kHighestE5m3)
+            w[h] = cap_bytes(w[h], 0xF7u);
+    }
     return w;
 }
 
@@ -123,13 +156,17 @@ __device__ __forceinline__ void e4m3_values(const u32x2 w, float step, float (&v
         v[4 * h + 3] = hi[1] * step;
     }
 }
+// A second moment's code as a float 2^111 times smaller than its number: the
+// leading bits, subnormal below c = 8.
+__device__ __forceinline__ float e5m3_small(const u32x2 w, int k)
+{
+    return bits_f32((w[k >> 2] >> (8 * (k & 3)) & 0xFFu) << 20);
+}
 __device__ __forceinline__ void e5m3_values(const u32x2 w, float step, float (&v)[8])
 {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const uint32_t c = w[k >> 2] >> (8 * (k & 3)) & 0xFFu;
-        v[k] = bits_f32(c << 20) * 0x1p111f * step;
-    }
+    for (int k = 0; k < 8; ++k)
+        v[k] = e5m3_small(w, k) * 0x1p111f * step;
 }
 
 } // namespace gqt

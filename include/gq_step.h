@@ -18,9 +18,11 @@
  *     its values stand for NaN.
  *   - GQS_ROUND_NEAREST: ties to even.  GQS_ROUND_RANDOM: with f the fraction
  *     of the way from the lower neighbour of |x| 2^-E to the upper, up where
- *     u + floor(f 2^16 + 1/2) >= 2^16: unbiased, up to 2^-17 of a step.  u is
- *     16-bit half c % 8 of the Philox4x32-10 block at counter (c / 8, 0, row,
- *     0) under the key `seed`, c the column.
+ *     u + floor(f 2^16 + 1/2) >= 2^16: unbiased, up to 2^-17 of a step
+ *     (between the format's numbers below its least normal one, f is first
+ *     rounded to a multiple of 2^-20).  u is 16-bit half c % 8 of the
+ *     Philox4x32-10 block at counter (c / 8, 0, row, 0) under the key `seed`,
+ *     c the column.
  *   - Rows: a block is 128 columns of a row; codes [rows][128 G] with G =
  *     ceil(d / 128) (columns past d hold 0), exps [G][16 ceil(rows / 16)].
  *   - Weights: w[n][k] has a block for each square of 128 x 128; codes
@@ -43,7 +45,7 @@
  *   - Matrices, dtypes, strides, memory, streams, errors and status values as
  *     in gq_train.h; codes and exps are 16-byte aligned.
  *   - Sizes: rows >= 0 and < 2^31, matrix sides in [1, 2^22], rows times
- *     blocks < 2^31.
+ *     blocks < 2^27.
  *   - No atomics: the same call gives the same bits.
  */
 #ifndef GQ_STEP_H
@@ -110,7 +112,7 @@ typedef struct gqs_tensor {
     void *v;
     void *m_exps;
     void *v_exps;
-    int64_t n; /* >= 0, < 2^35 */
+    int64_t n; /* >= 0, < 2^34 */
 } gqs_tensor;
 
 typedef struct gqs_adamw_args {

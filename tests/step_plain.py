@@ -51,6 +51,7 @@ def block(v: np.ndarray, table: np.ndarray, u=None):
     if u is None:
         up = (f > 0.5) | ((f == 0.5) & (lo % 2 == 1))
     else:
+        f = np.where(lo < 8, np.rint(f * 2.0**20) / 2.0**20, f)
         up = u + np.floor(f * 65536 + 0.5) >= 65536
     q = lo + up
     # values from 2^128 on have no float
