@@ -243,6 +243,16 @@ def _on_device(p) -> bool:
     return p.is_cuda
 
 
+def _capturing(device) -> bool:
+    return device.type == "cuda" and torch.cuda.is_current_stream_capturing()
+
+
+def _refuse_capture(device) -> None:
+    """Moments and counts that a graph zeroes would begin anew at each replay."""
+    if _capturing(device):
+        raise RuntimeError("a parameter's first step cannot be captured: take it before")
+
+
 class AdamW(torch.optim.Optimizer):
     """AdamW (decoupled weight decay) on ROCm devices, all parameters of a
     type in one launch.
@@ -259,7 +269,8 @@ class AdamW(torch.optim.Optimizer):
 
     capturable=True counts steps on the device, one count for a group, so that
     a captured graph goes on counting (and draws new numbers) at each replay;
-    lr may then be a float32 tensor on the device.  Otherwise each parameter
+    lr may then be a float32 tensor on the device.  A parameter's first step
+    makes its moments and is taken before a capture.  Otherwise each parameter
     counts the steps in which it had a gradient."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
@@ -285,6 +296,7 @@ class AdamW(torch.optim.Optimizer):
 
     def _new_state(self, p):
         n, device = p.numel(), p.device
+        _refuse_capture(device)
         if self.bits == 32:
             state = {"exp_avg": torch.zeros(n, device=device),
                      "exp_avg_sq": torch.zeros(n, device=device)}
@@ -358,6 +370,7 @@ class AdamW(torch.optim.Optimizer):
         """The group's number of steps on the device, one more than before."""
         count = group.get("step")
         if count is None:
+            _refuse_capture(device)
             count = group["step"] = torch.zeros(1, dtype=torch.int64, device=device)
         return count.add_(1)
 
@@ -368,6 +381,9 @@ class AdamW(torch.optim.Optimizer):
             with torch.enable_grad():
                 loss = closure()
         buckets = self._buckets()
+        if not self.capturable and buckets and _capturing(buckets[0][3][0].device):
+            raise RuntimeError("a captured step needs capturable=True: the graph would keep "
+                               "the number of this one")
         scale = self._clip(buckets)
         counted = {}
         for group, step, place, params, values, grads in buckets:

@@ -372,6 +372,28 @@ def test_optimizer_refusals(device):
         optim.AdamW([p]).step()
 
 
+def test_optimizer_refuses_captures_that_would_go_wrong(device, monkeypatch):
+    """A graph would zero what a first step makes at each replay, and keep the
+    number of a step that the host counts."""
+    p, q = (torch.nn.Parameter(torch.ones(4, device=device)) for _ in range(2))
+    p.grad = torch.ones(4, device=device)
+    ready, fixed = optim.AdamW([p, q], capturable=True), optim.AdamW([p])
+    ready.step()
+    fixed.step()
+    before = p.detach().clone()
+    with monkeypatch.context() as m:
+        m.setattr(optim, "_capturing", lambda device: True)
+        for opt in (fixed, optim.AdamW([p], capturable=True), optim.AdamW([p], bits=8)):
+            with pytest.raises(RuntimeError):
+                opt.step()
+        ready.step()
+        q.grad = torch.ones(4, device=device)
+        with pytest.raises(RuntimeError):
+            ready.step()
+    assert (q == 1).all() and not torch.equal(p, before)
+    assert int(ready.param_groups[0]["step"]) == 2
+
+
 def test_optimizer_refuses_host_parameters():
     p = torch.nn.Parameter(torch.ones(4))
     p.grad = torch.ones(4)
