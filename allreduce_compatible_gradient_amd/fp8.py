@@ -18,6 +18,8 @@ are the same under autograd.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from ._step import check, lib
@@ -215,6 +217,12 @@ def gqs_fp8_restore(a, dtype=torch.bfloat16, *, stream=None) -> torch.Tensor:
     return out
 
 
+@functools.lru_cache(maxsize=1024)
+def _need(entry: str, m: int, cols: int, depth: int, dt: int) -> int:
+    """A workspace's bytes, which depend on nothing else."""
+    return int(getattr(lib(), entry)(m, cols, depth, dt))
+
+
 def _workspace(workspace, need: int, device):
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
@@ -253,7 +261,7 @@ def gqs_fp8_product(x: Fp8, w: Fp8Weight, bias=None, *, transposed: bool = False
     x_codes, x_exps = _row_copy(x, "x", m, depth, device)
     bdt = _bias(bias, cols, device)
     y = torch.empty((m, cols), dtype=dtype, device=device)
-    need = lib().gqs_fp8_product_workspace_bytes(m, cols, depth, dt)
+    need = _need("gqs_fp8_product_workspace_bytes", m, cols, depth, dt)
     workspace = _workspace(workspace, need, device)
     check(lib().gqs_fp8_product(x_codes, x_exps, m, codes, exps, cols, depth, transposed,
                                 _ptr(bias), bdt, y.data_ptr(), dt, _ptr(workspace), max(need, 0),
@@ -282,7 +290,7 @@ def gqs_fp8_linear(x: torch.Tensor, w: Fp8Weight, bias=None, *, transposed: bool
         raise ValueError(f"x is {list(x.shape)}, expected {depth} columns")
     bdt = _bias(bias, cols, device)
     y = torch.empty((m, cols), dtype=x.dtype, device=device)
-    need = lib().gqs_fp8_linear_workspace_bytes(m, cols, depth, dt)
+    need = _need("gqs_fp8_linear_workspace_bytes", m, cols, depth, dt)
     workspace = _workspace(workspace, need, device)
     check(lib().gqs_fp8_linear(x.data_ptr(), dt, m, depth, ldx, *_rounding(seed), codes, exps,
                                cols, transposed, _ptr(bias), bdt, y.data_ptr(), _ptr(workspace),

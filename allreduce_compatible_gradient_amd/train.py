@@ -18,7 +18,8 @@ Two layers:
   is no fallback: without the built library or a GPU they raise.
 - ``layer_norm``, ``gelu``, ``linear`` and ``Mlp8``: the same operators under
   autograd, and a transformer's MLP block that keeps everything it needs for
-  its backward pass in 8 bits.
+  its backward pass in 8 bits.  ``linear`` and ``Mlp8`` are the library's
+  products, or with ``fp8=True`` those of e4m3 copies (``fp8``).
 """
 from __future__ import annotations
 
