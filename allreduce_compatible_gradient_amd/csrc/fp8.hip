@@ -251,6 +251,13 @@ struct Bytes<8> {
     }
 };
 
+// N of them, PART at once.
+template <int N, int PART>
+struct Parts {
+    Bytes<PART> part[N / PART];
+    __device__ __forceinline__ uint32_t byte(int i) const { return part[i / PART].byte(i % PART); }
+};
+
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
@@ -378,7 +385,8 @@ struct Product {
 // than a kernel of its own, about 2 us.  From bf16 rows 1 x 4096 x 1024 (rows,
 // columns, depth) 4.0 us, 1 x 4096 x 4096 5.6, 16 x 1024 x 4096 8.3; from
 // their copy 32 x 4096 x 4096 5.7, 64 x 4096 x 4096 7.0 (a weight of 17 MB,
-// 2.4 to 3 TB/s: latency, more than its bytes).
+// 2.4 to 3 TB/s: latency, more than its bytes), 96 x 4096 x 4096 10.4, bound
+// by the rows, which every block of columns takes from the L2 again.
 template <typename T, int F, int STEPS, bool MADE>
 __global__ __launch_bounds__(F > 2 ? 512 : 1024) void k_product_direct(const Product a,
                                                                        T *__restrict__ y)
@@ -401,17 +409,21 @@ __global__ __launch_bounds__(F > 2 ? 512 : 1024) void k_product_direct(const Pro
     const u32x4 w_from =
         descriptor(a.w.codes + col0 * a.w.pitch, (uint32_t)cols * (uint32_t)a.w.pitch);
     u32x4 x_from{};
-    const uint8_t *ep = nullptr;
+    // Where the lane's exponents are, kPart together (a row copy has bytes for
+    // whole 16s of rows, which kPart divides); rows past them are not stored.
+    constexpr int kPart = F == 6 ? 2 : F;
+    int32_t e_at[F / kPart];
     if constexpr (!MADE) {
         X::offsets(x_at, lane, rows, a.x.pitch);
         x_from = descriptor(a.x.codes + row0 * a.x.pitch, (uint32_t)rows * (uint32_t)a.x.pitch);
-        // a tile's last rows may have no bytes: they are not stored
-        ep = a.x.exps + min(row0 + F * r, a.epitch - F);
+#pragma unroll
+        for (int i = 0; i < F; i += kPart)
+            e_at[i / kPart] = (int32_t)min(row0 + F * r + i, a.epitch - kPart);
     }
     f32x4 acc[F] = {};
     for (int32_t s0 = wave * STEPS; s0 < a.blocks; s0 += waves * STEPS) {
         const int32_t steps = min(STEPS, a.blocks - s0);
-        Bytes<F> ex[STEPS];
+        Parts<F, kPart> ex[STEPS];
         uint32_t ew[STEPS];
         Raw8<T> raw[STEPS][4];
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); // what lay there has been read
@@ -429,7 +441,10 @@ __global__ __launch_bounds__(F > 2 ? 512 : 1024) void k_product_direct(const Pro
                                    128 * (s0 + p) + 8 * r, a.depth, raw[p][i]);
             } else {
                 X::load(to + W::kBytes, x_from, x_at, s0 + p);
-                ex[p] = *reinterpret_cast<const Bytes<F> *>(ep + (s0 + p) * a.epitch);
+                const uint8_t *const e = a.x.exps + (s0 + p) * a.epitch;
+#pragma unroll
+                for (int i = 0; i < F / kPart; ++i)
+                    ex[p].part[i] = *reinterpret_cast<const Bytes<kPart> *>(e + e_at[i]);
             }
             ew[p] = a.squares.at(col0 >> 7, s0 + p);
         }
@@ -463,7 +478,7 @@ __global__ __launch_bounds__(F > 2 ? 512 : 1024) void k_product_direct(const Pro
                     const uint32_t other = (uint32_t)__shfl((int)e, 16 * (r & 3));
                     of_row = r >> 2 == i ? other : of_row;
                 }
-                ex[p].b = (uint8_t)of_row;
+                ex[p].part[0].b = (uint8_t)of_row;
             }
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -1026,8 +1041,11 @@ constexpr Cost kCosts[2][kWays] = {
     {{}, {64, 128, kCUs, 0.34f, 1.4f}, {128, 128, kCUs, 0.55f, 1.8f},
      {128, 128, 2 * kCUs, 0.9f, 4.4f}, {256, 256, kCUs, 1.6f, 5.8f}, {}},
 };
-constexpr Cost kDirectCosts[3] = { // of 32, 64 and 128 rows
-    {32, 16, kCUs, 0.08f, 0.2f}, {64, 16, kCUs, 0.13f, 0.2f}, {128, 16, kCUs, 0.24f, 1.7f}};
+constexpr Cost kDirectCosts[4] = { // of 32, 64, 96 and 128 rows
+    {32, 16, kCUs, 0.08f, 0.2f},
+    {64, 16, kCUs, 0.13f, 0.2f},
+    {96, 16, kCUs, 0.2f, 0.9f},
+    {128, 16, kCUs, 0.24f, 1.7f}};
 
 // What costs least: rounds of tiles, and, where the depth is split, a second
 // kernel that adds up the parts.  Microseconds in a graph, the ways forced: bf16
@@ -1035,7 +1053,8 @@ constexpr Cost kDirectCosts[3] = { // of 32, 64 and 128 rows
 // 17.7; 2048 x 4096 x 4096 53, 40, 36, 51; 8192 x 4096 x 1024 71, 51, 50, 40;
 // 512 x 4096 x 4096 15.6, 20.9, 24.7, 29.  fp32 8192 x 4096 x 1024 Rows64 110,
 // Square128 83, Wide256 70; 1024 x 4096 x 4096 46, 36, 42.  Directly and by the
-// best tiles: bf16 64 x 4096 x 4096 7.0, 10.9; 128 x 4096 x 4096 12.0, 13.7;
+// best tiles: bf16 64 x 4096 x 4096 7.0, 10.9; 128 x 4096 x 4096 12.0, 13.7
+// (96 rows in a kernel for 96 10.4, for 128 11.2; fp32 9.7, 11.7);
 // 256 x 4096 x 4096 20.3, 13.9; 64 x 8192 x 8192 19.1, 17.5.
 Plan plan_of(int64_t m, int64_t cols, int64_t depth, int32_t dtype)
 {
@@ -1052,7 +1071,7 @@ Plan plan_of(int64_t m, int64_t cols, int64_t depth, int32_t dtype)
         return (float)rounds * ((float)((blocks + z - 1) / z) * step + c.tile) + sums;
     };
     // few blocks of direct loads have more of the L2 each
-    const Cost &direct = kDirectCosts[m <= 32 ? 0 : m <= 64 ? 1 : 2];
+    const Cost &direct = kDirectCosts[std::min<int64_t>((m - 1) / 32, 3)];
     const float full = std::min(1.0f, (float)tiles_of(direct) / (float)kCUs);
     float least = time(direct, 1, direct.step * (0.55f + 0.45f * full));
     for (int way = kRows64; way < kWays; ++way) {
@@ -1139,6 +1158,8 @@ int32_t launch_product(const Product &a, Way way, void *y, hipStream_t st)
         return launch_direct<T, 2, 1, false>(a, out, st);
     if (a.m <= 64)
         return launch_direct<T, 4, 1, false>(a, out, st);
+    if (a.m <= 96)
+        return launch_direct<T, 6, 1, false>(a, out, st);
     return launch_direct<T, 8, 1, false>(a, out, st);
 }
 

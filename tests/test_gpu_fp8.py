@@ -388,6 +388,26 @@ def test_every_way(m, n, k, dtype):
         assert want.abs().max() > 8
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("first", [1, 17, 33, 65, 97, 129, 257])
+def test_rows_have_their_own_steps(first, dtype):
+    """Every number of rows of a way for few of them, each row of another
+    power of two."""
+    n, k = 37, 300
+    g = torch.Generator(device=DEV).manual_seed(first)
+
+    def draw_whole(rows, cols):
+        x = torch.randint(-2, 3, (rows, cols), device=DEV, generator=g).float()
+        return x * (torch.rand(rows, cols, device=DEV, generator=g) < 0.2)
+    w = draw_whole(n, k)
+    w8 = fp8.gqs_fp8_weight(w.to(DT[dtype]))
+    for m in range(first, first + 32):
+        x = draw_whole(m, k)
+        steps = torch.exp2((torch.arange(m, device=DEV) * 5 % 23 - 11).float())[:, None]
+        got = fp8.gqs_fp8_linear((x * steps).to(DT[dtype]), w8)
+        assert torch.equal(got.float() / steps, (x @ w.t()).to(DT[dtype]).float()), m
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 1, 20000), (40, 1, 20000), (300, 1, 6000), (1, 20000, 1),
                                    (20000, 1, 1), (3000, 3, 3)])
 def test_narrow_products(m, n, k):
