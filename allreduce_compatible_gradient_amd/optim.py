@@ -294,6 +294,10 @@ class AdamW(torch.optim.Optimizer):
         self.bits, self.random, self.seed = bits, bool(random), int(seed)
         self.max_norm, self.capturable, self.last_norm = max_norm, bool(capturable), None
 
+    def __getstate__(self):  # torch's holds the groups and states alone
+        own = ("bits", "random", "seed", "max_norm", "capturable", "last_norm")
+        return {**super().__getstate__(), **{name: getattr(self, name) for name in own}}
+
     def _new_state(self, p):
         n, device = p.numel(), p.device
         _refuse_capture(device)
@@ -405,13 +409,18 @@ class AdamW(torch.optim.Optimizer):
 
     def load_state_dict(self, state_dict):
         """As torch's, which would cast moments and codes to the parameters'
-        types: they come as they were saved."""
-        saved = [i for group in state_dict["param_groups"] for i in group["params"]]
-        for i in saved:
-            codes = state_dict["state"].get(i, {}).get("exp_avg")
-            if codes is not None and (codes.dtype == torch.float32) != (self.bits == 32):
-                raise ValueError(f"the state has other moments than those of bits={self.bits}")
+        types: they come as they were saved.  Steps counted on the host and
+        on the device are taken for each other."""
+        for group in state_dict["param_groups"]:
+            states = [state_dict["state"].get(i, {}) for i in group["params"]]
+            for state in states:
+                codes = state.get("exp_avg")
+                if codes is not None and (codes.dtype == torch.float32) != (self.bits == 32):
+                    raise ValueError(f"the state has other moments than those of bits={self.bits}")
+            if self.capturable and len({state["step"] for state in states if "step" in state}) > 1:
+                raise ValueError("capturable=True has one count for a group, the state's differ")
         super().load_state_dict(state_dict)
+        saved = [i for group in state_dict["param_groups"] for i in group["params"]]
         own = [p for group in self.param_groups for p in group["params"]]
         for i, p in zip(saved, own):
             for key, value in state_dict["state"].get(i, {}).items():
@@ -419,5 +428,13 @@ class AdamW(torch.optim.Optimizer):
                     value = value.detach().clone().to(p.device)
                 self.state[p][key] = value
         for group in self.param_groups:
-            if isinstance(group.get("step"), torch.Tensor) and group["params"]:
-                group["step"] = group["step"].clone().to(group["params"][0].device)
+            states = [self.state[p] for p in group["params"] if self.state.get(p)]
+            count = group.pop("step", None)
+            if self.capturable:
+                for state in states:
+                    count = state.pop("step", count)
+                if count is not None:
+                    group["step"] = torch.tensor([int(count)], device=group["params"][0].device)
+            elif count is not None:
+                for state in states:
+                    state["step"] = int(count)

@@ -241,6 +241,27 @@ def test_held_weights(device):
         train.Mlp8(8, 16, device=device).hold_fp8()
 
 
+def test_held_copies_are_dropped_with_their_weights(device):
+    """By a state that is loaded and by a cast; a layer that is no plain
+    Linear is not held."""
+    make = lambda: train.Mlp8(40, 150, device=device, dtype=torch.float32, fp8=True)  # noqa: E731
+    block, other = make(), make()
+    x = leaf(device, 4, 40, seed=1).detach()
+    with torch.no_grad():
+        y = other(x)
+        block.hold_fp8()
+        assert not torch.equal(block(x), y)
+        block.load_state_dict(other.state_dict())
+        assert torch.equal(block(x), y)
+        block.hold_fp8().double().float().up.weight.zero_()
+        assert not torch.equal(block(x), y)
+        block.load_state_dict(other.state_dict())
+        block.up = torch.nn.Sequential(other.up)
+        assert torch.allclose(block.hold_fp8()(x), y, atol=0.1)
+        del block.__dict__["fp8"], block.__dict__["_held"]  # as an older pickle
+        assert torch.isfinite(block(x)).all()
+
+
 # ---------------------------------------------------------------------------
 # the optimizer
 
@@ -334,6 +355,52 @@ def test_optimizer_goes_on_from_its_state(device, bits):
     assert twin["state"][0]["step"] == 2
     with pytest.raises(ValueError):
         optim.AdamW(parameters(device), bits=40 - bits).load_state_dict(opt.state_dict())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_optimizer_copies_and_pickles(device, bits):
+    ps = parameters(device)
+    opt = optim.AdamW(ps, lr=1e-2, bits=bits, seed=4, max_norm=1.0)
+    give(ps, 1)
+    opt.step()
+    file = io.BytesIO()
+    torch.save(opt, file)
+    file.seek(0)
+    for twin in (copy.deepcopy(opt), torch.load(file, weights_only=False)):
+        assert (twin.bits, twin.seed, twin.max_norm, twin.capturable) == (bits, 4, 1.0, False)
+        qs = twin.param_groups[0]["params"]
+        twin_of = [p.detach().clone() for p in ps]
+        for p, q, r in zip(ps, qs, twin_of):
+            assert torch.equal(p, q) and q is not p
+            q.grad = p.grad.clone()
+        twin.step()
+        assert all(not torch.equal(q, r) for q, r in zip(qs, twin_of))
+
+
+@pytest.mark.parametrize("first", [False, True])
+def test_optimizer_counts_go_over(device, first):
+    """Steps counted on the host go on on the device, and the other way."""
+    ps = parameters(device)
+    opt = optim.AdamW(ps, lr=1e-2, bits=8, seed=4, capturable=first)
+    for step in (1, 2):
+        give(ps, step)
+        opt.step()
+    qs = [torch.nn.Parameter(p.detach().clone(memory_format=torch.preserve_format)) for p in ps]
+    other = optim.AdamW(qs, lr=1e-2, bits=8, seed=4, capturable=not first)
+    other.load_state_dict(opt.state_dict())
+    give(ps, 3)
+    give(qs, 3)
+    opt.step()
+    other.step()
+    for p, q in zip(ps, qs):
+        assert torch.equal(p, q)
+    assert ("step" in other.param_groups[0]) == (not first)
+    assert all(("step" in other.state[q]) == first for q in qs)
+    if not first:
+        ps[0].grad = None
+        opt.step()
+        with pytest.raises(ValueError):
+            other.load_state_dict(opt.state_dict())
 
 
 def test_optimizer_groups(device):
