@@ -780,6 +780,8 @@ class Mlp8(torch.nn.Module):
     ``linear(..., fp8=True)`` does.  Each pass makes its copies of the weights;
     ``hold_fp8`` keeps them for the passes without gradients."""
 
+    fp8, _held = False, None  # of a block pickled before it had them
+
     def __init__(self, d: int, hidden: int, *, eps: float = 1e-5, approximate: str = "tanh",
                  random: bool = True, seed: int | None = None, device=None,
                  dtype=torch.bfloat16, fp8: bool = False):
@@ -797,27 +799,32 @@ class Mlp8(torch.nn.Module):
     def hold_fp8(self, hold: bool = True):
         """Makes the e4m3 copies of up's and down's weights as they are now
         and takes them, in passes without gradients, until it is called
-        again; hold=False drops them.  For serving: a pass then reads one
-        byte a weight.  They are not in the state dict, and weights changed
-        since are not seen."""
+        again; hold=False drops them, and so do loading a state and moving
+        or casting the block.  For serving: a pass then reads one byte a
+        weight.  They are made of the weights as they are stored (without
+        them, autocast casts first) and are not in the state dict; weights
+        changed since are not seen."""
         if hold and not self.fp8:
             raise ValueError("hold_fp8 is for a block with fp8=True")
         self._held = None
         if hold:
-            self._held = tuple(_fp8_weight(m.weight.detach(), False) for m in (self.up, self.down))
+            self._held = tuple(
+                _fp8_weight(m.weight.detach(), False) if _is_plain(m, torch.nn.Linear) else None
+                for m in (self.up, self.down))
         return self
 
     def _product(self, x, module, k: int):
         """x through up (k = 0) or down (1), without gradients."""
         if not self.fp8:
             return module(x)
-        if self._held is None:
+        held = None if self._held is None else self._held[k]
+        if held is None:
             return linear(x, module.weight, module.bias, fp8=True)
         from .fp8 import gqs_fp8_linear
         dtype = _product_dtype(x)
         with _no_autocast(x):
             x = _cast(x, dtype)
-            y = gqs_fp8_linear(_rows(x, x.shape[-1]), self._held[k], _cast(module.bias, dtype))
+            y = gqs_fp8_linear(_rows(x, x.shape[-1]), held, _cast(module.bias, dtype))
         return y.view(*x.shape[:-1], y.shape[-1])
 
     def _pass_seed(self) -> int:
@@ -842,7 +849,12 @@ class Mlp8(torch.nn.Module):
         if drew:
             self._drawn = drawn & 0xFFFFFFFFFFFFFFFF
 
+    def _apply(self, *args, **kwargs):
+        self._held = None
+        return super()._apply(*args, **kwargs)
+
     def _load_from_state_dict(self, state_dict, prefix, *args):
+        self._held = None
         # a state without them leaves them as they are
         state_dict.setdefault(prefix + "_extra_state", self.get_extra_state())
         super()._load_from_state_dict(state_dict, prefix, *args)

@@ -81,7 +81,10 @@ def arguments(argv=None):
     p.add_argument("--adamw", type=int, choices=(32, 8), default=0, metavar="BITS",
                    help="this package's AdamW with moments in 32 or 8 bits")
     p.add_argument("--clip", type=float, default=None, help="with --adamw: the gradients' norm")
-    return p.parse_args(argv)
+    args = p.parse_args(argv)
+    if args.clip is not None and not args.adamw:
+        p.error("--clip goes with --adamw")
+    return args
 
 
 def main():
