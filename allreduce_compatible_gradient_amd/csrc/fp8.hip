@@ -186,8 +186,6 @@ __global__ __launch_bounds__(kThreads) void k_fp8_restore(const uint8_t *__restr
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef u32x2 u32x2_e2 __attribute__((aligned(2)));
-typedef u32x2 u32x2_e4 __attribute__((aligned(4)));
-typedef uint32_t u32_e2 __attribute__((aligned(2)));
 typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 struct Operand {
@@ -546,8 +544,8 @@ __global__ __launch_bounds__(F > 2 ? 512 : 1024) void k_product_direct(const Pro
 // there, and a 256 x 256 tile's step of 64 KB its MFMAs' time over again, so
 // that smaller tiles are bound by their loads.  bf16 8192 x 8192 x 8192: 413 us,
 // 2660 TFLOP/s (without the loads 3250, the MFMAs alone 4190); 8192 x 4096 x
-// 4096 110 us, 2500, where they are busy 62% of the time and 5.8 us go to a
-// tile's end.  fp32 results: 214 us, 1285 TFLOP/s.
+// 4096 110 us, 2500, where they are busy 62% of the time and 4.6 us go to a
+// tile's beginning and end.  fp32 results: 214 us, 1285 TFLOP/s.
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -625,44 +623,37 @@ __device__ __forceinline__ Item item_of(uint32_t number, const Product &a)
     return w;
 }
 
-// N consecutive results of a row, of which `left` exist.
-template <int N>
-__device__ __forceinline__ void store_row(bf16 *p, const float (&v)[N], int32_t left)
+// N consecutive results at a byte of a buffer; those past its end are dropped.
+constexpr uint32_t kNowhere = 0x80000000u; // past 64 rows of 2^24 bytes
+template <typename O, int N>
+__device__ __forceinline__ void store_buffer(__amdgpu_buffer_rsrc_t to, uint32_t at,
+                                             const float (&v)[N])
 {
-    if (N > 1 && left >= N) {
-        uint32_t w[(N + 1) / 2];
+    if constexpr (sizeof(O) == 4) {
+        if constexpr (N == 4)
+            __builtin_amdgcn_raw_buffer_store_b128(
+                u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3])}, to, (int)at, 0, 0);
+        else if constexpr (N == 2)
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(v[0]), __float_as_uint(v[1])},
+                                                  to, (int)at, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), to, (int)at, 0, 0);
+    } else if constexpr (N == 1) {
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (bf16)v[0]), to, (int)at,
+                                              0, 0);
+    } else {
+        uint32_t w[N / 2];
 #pragma unroll
         for (int k = 0; k < N / 2; ++k) {
             const bf16x2 h = {(bf16)v[2 * k], (bf16)v[2 * k + 1]};
             w[k] = __builtin_bit_cast(uint32_t, h);
         }
         if constexpr (N == 4)
-            *reinterpret_cast<u32x2_e2 *>(p) = u32x2{w[0], w[1]};
-        else if constexpr (N == 2)
-            *reinterpret_cast<u32_e2 *>(p) = w[0];
-        return;
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{w[0], w[1]}, to, (int)at, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b32(w[0], to, (int)at, 0, 0);
     }
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-        if (k < left)
-            p[k] = (bf16)v[k];
-}
-template <int N>
-__device__ __forceinline__ void store_row(float *p, const float (&v)[N], int32_t left)
-{
-    if (N > 1 && left >= N) {
-        if constexpr (N == 4)
-            *reinterpret_cast<u32x4_e4 *>(p) =
-                u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                      __float_as_uint(v[3])};
-        else if constexpr (N == 2)
-            *reinterpret_cast<u32x2_e4 *>(p) = u32x2{__float_as_uint(v[0]), __float_as_uint(v[1])};
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-        if (k < left)
-            p[k] = v[k];
 }
 
 // What a tile's kernel needs of LDS: STAGES of both panels and of the exponent
@@ -788,7 +779,6 @@ __global__ __launch_bounds__(64 * S::kWaves, S::kWaves *S::kBlocksPerCu / 4) voi
     ex = *reinterpret_cast<const Bytes<FM> *>(xe);
     ew = *reinterpret_cast<const uint32_t *>(we);
     uint32_t now = 0; // the stage
-
     for (int32_t number = blockIdx.x; number < total; number += gridDim.x) {
         const Item w = item_of(number, a);
         f32x16 acc[FM][FN] = {};
@@ -869,19 +859,40 @@ __global__ __launch_bounds__(64 * S::kWaves, S::kWaves *S::kBlocksPerCu / 4) voi
 #pragma unroll
         for (int j = 0; j < FN; ++j)
             asm volatile("" : "+v"(bias[j]));
+        // The wave's rows by a descriptor that ends with the last: what lies
+        // past it, or is put there, is not stored.
+        const int64_t row0 = (int64_t)w.tm * S::kRows + 32 * FM * wm;
+        const uint32_t pitch = (uint32_t)a.cols * sizeof(O);
+        const auto rows = __builtin_amdgcn_make_buffer_rsrc(
+            out + row0 * a.cols, 0, (int)(max(min(a.m - row0, (int64_t)32 * FM), (int64_t)0) * pitch),
+            0x00020000);
+        const int32_t left = a.cols - col;
+        const auto store = [&](auto to_row) GQT_INLINE {
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
+            for (int i = 0; i < FM; ++i)
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
-                const int of = 8 * (q / 4) + 4 * (lane >> 5) + q % 4;
-                const int64_t row = (int64_t)w.tm * S::kRows + 32 * FM * wm + FM * of + i;
-                float v[FN];
+                for (int q = 0; q < 16; ++q) {
+                    float v[FN];
 #pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    v[j] = acc[i][j][q] + bias[j];
-                if (row < a.m)
-                    store_row<FN>(out + row * a.cols + col, v, a.cols - col);
-            }
+                    for (int j = 0; j < FN; ++j)
+                        v[j] = acc[i][j][q] + bias[j];
+                    to_row((FM * (8 * (q / 4) + q % 4) + i) * pitch, v);
+                }
+        };
+        const uint32_t lane_at = FM * 4 * (lane >> 5) * pitch + (uint32_t)col * sizeof(O);
+        const uint32_t whole = left >= FN ? lane_at : kNowhere;
+        store([&](uint32_t row_at, const float (&v)[FN]) GQT_INLINE {
+            store_buffer<O>(rows, whole + row_at, v);
+        });
+        if (FN > 1 && (w.tn + 1) * S::kCols > a.cols && a.cols % FN) // the last columns' rest
+            store([&](uint32_t row_at, const float (&v)[FN]) GQT_INLINE {
+#pragma unroll
+                for (int j = 0; j < FN - 1; ++j) {
+                    const float one[1] = {v[j]};
+                    const uint32_t at = lane_at + j * (uint32_t)sizeof(O);
+                    store_buffer<O>(rows, (left < FN && j < left ? at : kNowhere) + row_at, one);
+                }
+            });
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); // nothing may land in LDS after the end
 }
@@ -889,6 +900,17 @@ __global__ __launch_bounds__(64 * S::kWaves, S::kWaves *S::kBlocksPerCu / 4) voi
 // Adds the parts' sums of a row, in their order, and the bias: 2 to 4 us where
 // the depth is split.
 constexpr int kSumColumns = 4;
+__device__ __forceinline__ void store_sums(bf16 *p, const float (&v)[kSumColumns])
+{
+    const bf16x2 lo = {(bf16)v[0], (bf16)v[1]}, hi = {(bf16)v[2], (bf16)v[3]};
+    *reinterpret_cast<u32x2_e2 *>(p) =
+        u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+}
+__device__ __forceinline__ void store_sums(float *p, const float (&v)[kSumColumns])
+{
+    *reinterpret_cast<u32x4_e4 *>(p) = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                             __float_as_uint(v[2]), __float_as_uint(v[3])};
+}
 template <typename O>
 __global__ __launch_bounds__(kThreads) void k_sum_splits(const Product a, O *__restrict__ y)
 {
@@ -916,7 +938,15 @@ __global__ __launch_bounds__(kThreads) void k_sum_splits(const Product a, O *__r
     for (int k = 0; k < kSumColumns; ++k)
         if (a.bias && col + k < a.cols)
             v[k] += bias_at(a.bias, a.bias_dtype, col + k);
-    store_row<kSumColumns>(y + row * a.cols + col, v, a.cols - col);
+    O *const out = y + row * a.cols + col;
+    if (col + kSumColumns <= a.cols) {
+        store_sums(out, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < kSumColumns; ++k)
+            if (col + k < a.cols)
+                store_one(out + k, v[k]);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -1038,8 +1068,8 @@ constexpr Cost kCosts[2][kWays] = {
     {{}, {64, 128, kCUs, 0.62f, 1.5f}, {128, 128, kCUs, 0.95f, 2.6f}, {}, {},
      {256, 128, kCUs, 1.57f, 4.1f}},
     // 8-bit products of bf16 ones
-    {{}, {64, 128, kCUs, 0.34f, 1.4f}, {128, 128, kCUs, 0.55f, 1.8f},
-     {128, 128, 2 * kCUs, 0.9f, 4.4f}, {256, 256, kCUs, 1.6f, 5.8f}, {}},
+    {{}, {64, 128, kCUs, 0.34f, 1.1f}, {128, 128, kCUs, 0.55f, 1.2f},
+     {128, 128, 2 * kCUs, 0.9f, 3.6f}, {256, 256, kCUs, 1.6f, 4.6f}, {}},
 };
 constexpr Cost kDirectCosts[4] = { // of 32, 64, 96 and 128 rows
     {32, 16, kCUs, 0.08f, 0.2f},
@@ -1050,7 +1080,7 @@ constexpr Cost kDirectCosts[4] = { // of 32, 64, 96 and 128 rows
 // What costs least: rounds of tiles, and, where the depth is split, a second
 // kernel that adds up the parts.  Microseconds in a graph, the ways forced: bf16
 // 4096 x 1024 x 1024 Rows64 11.3, Square128 9.2, Square128x2 10.7, Square256
-// 17.7; 2048 x 4096 x 4096 53, 40, 36, 51; 8192 x 4096 x 1024 71, 51, 50, 40;
+// 17.7; 2048 x 4096 x 4096 53, 40, 36, 51; 8192 x 4096 x 1024 71, 51, 50, 38;
 // 512 x 4096 x 4096 15.6, 20.9, 24.7, 29.  fp32 8192 x 4096 x 1024 Rows64 110,
 // Square128 83, Wide256 70; 1024 x 4096 x 4096 46, 36, 42.  Directly and by the
 // best tiles: bf16 64 x 4096 x 4096 7.0, 10.9; 128 x 4096 x 4096 12.0, 13.7
