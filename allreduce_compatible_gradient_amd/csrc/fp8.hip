@@ -373,9 +373,9 @@ struct Product {
     uint32_t k0, k1;
 };
 
-// Few rows: the weight's bytes bound it, so all blocks of the card read them,
-// none twice in a row of blocks.  A block has 16 F rows and 16 columns of y;
-// its waves take the depth's blocks in turn, STEPS at once, each through LDS
+// Few rows: a block has 16 F rows and 16 columns of y, so that a weight of
+// thousands of columns is read by all of the card, once for each 16 F rows.
+// Its waves take the depth's blocks in turn, STEPS at once, each through LDS
 // of its own, where loads of whole lines put them (lanes that load fragments
 // straight from memory, sixteen rows at once, take four times as long), and
 // add their sums at the end.  MADE: x's copy is made on the way, sixteen lanes
@@ -383,8 +383,8 @@ struct Product {
 // than a kernel of its own, about 2 us.  From bf16 rows 1 x 4096 x 1024 (rows,
 // columns, depth) 4.0 us, 1 x 4096 x 4096 5.6, 16 x 1024 x 4096 8.3; from
 // their copy 32 x 4096 x 4096 5.7, 64 x 4096 x 4096 7.0 (a weight of 17 MB,
-// 2.4 to 3 TB/s: latency, more than its bytes), 96 x 4096 x 4096 10.4, bound
-// by the rows, which every block of columns takes from the L2 again.
+// 2.4 to 3 TB/s: bound by latency, more than by its bytes), 96 x 4096 x 4096
+// 10.4, bound by the rows, which every block takes from the L2 again.
 template <typename T, int F, int STEPS, bool MADE>
 __global__ __launch_bounds__(F > 2 ? 512 : 1024) void k_product_direct(const Product a,
                                                                        T *__restrict__ y)
