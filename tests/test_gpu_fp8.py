@@ -408,6 +408,29 @@ def test_rows_have_their_own_steps(first, dtype):
         assert torch.equal(got.float() / steps, (x @ w.t()).to(DT[dtype]).float()), m
 
 
+# each way, with one to three columns and some rows more than whole tiles
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(4097, 4101, 130), (2049, 4098, 400), (1023, 1027, 1100),
+                                   (300, 2050, 3000), (129, 129, 5000), (90, 301, 700),
+                                   (20, 62, 9000), (8201, 259, 256), (5, 35, 300)])
+@pytest.mark.parametrize("before", [64, 65])
+def test_results_end_where_they_end(m, n, k, before, dtype):
+    """Nothing is stored around a result, wherever it begins, and what is
+    stored is what another call stores."""
+    x = torch.randn(m, k, device=DEV).to(DT[dtype])
+    w8 = fp8.gqs_fp8_weight(torch.randn(n, k, device=DEV).to(DT[dtype]))
+    L, code = _step.lib(), 0 if dtype == "f32" else 1
+    need = L.gqs_fp8_linear_workspace_bytes(m, n, k, code)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+    held = torch.full((before + m * n + 64,), 5.0, device=DEV, dtype=DT[dtype])
+    y = held[before:before + m * n]
+    _step.check(L.gqs_fp8_linear(x.data_ptr(), code, m, k, k, 0, 0, w8.codes.data_ptr(),
+                                 w8.exps.data_ptr(), n, 0, None, 0, y.data_ptr(), ws.data_ptr(),
+                                 need, torch.cuda.current_stream().cuda_stream))
+    assert (held[:before] == 5.0).all() and (held[before + m * n:] == 5.0).all()
+    assert torch.equal(y.view(m, n), fp8.gqs_fp8_linear(x, w8))
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 1, 20000), (40, 1, 20000), (300, 1, 6000), (1, 20000, 1),
                                    (20000, 1, 1), (3000, 3, 3)])
 def test_narrow_products(m, n, k):
