@@ -20,6 +20,7 @@ import operator
 import struct
 
 import torch
+from torch.autograd.graph import increment_version
 
 from ._step import CAdamWArgs, check, lib
 from .train import _current, _dtype, _Elsewhere, _elsewhere, _mix_seed
@@ -139,7 +140,9 @@ def gqs_adamw(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, betas=(0.9, 0.9
     captured graph reads at every replay.  A `seed` is needed with Moment8; a
     bf16 parameter is rounded at random where one is given, to nearest
     otherwise.  Calls of one step with one seed share random numbers between
-    tensors of the same number in their lists: give each list its own."""
+    tensors of the same number in their lists: give each list its own.
+
+    To autograd the params are changed in place, as by torch's own operations."""
     params, grads = list(params), list(grads)
     exp_avgs, exp_avg_sqs = list(exp_avgs), list(exp_avg_sqs)
     if len(params) != len(grads):
@@ -180,6 +183,7 @@ def gqs_adamw(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, betas=(0.9, 0.9
                           _dtype(p_type, "params"), _dtype(g_type, "grads"), args,
                           None if workspace is None else workspace.data_ptr(), 16,
                           _current(device)))
+    increment_version(params)  # a graph that saved one is refused its backward pass
 
 
 def gqs_moment8_restore(moment: Moment8, dtype=torch.bfloat16, *, stream=None) -> torch.Tensor:
