@@ -1,0 +1,118 @@
+"""AdamW with 8-bit moments where a block's gradients are of very different
+sizes: the smallest elements' second moments are below their block's lowest
+code, mostly kept as 0, while their first moments are now and then rounded up
+to a whole code.  Their steps stay bounded."""
+import numpy as np
+import pytest
+
+import step_plain as plain
+
+U = plain.U
+HYPER = dict(lr=1.0, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0)
+
+
+def least_of(exps, n):
+    """Half the lowest step of each element's block, 2^(E - 19), at least 2^-126."""
+    E = np.asarray(exps, dtype=np.float64) - 127
+    return np.repeat(np.maximum(np.exp2(E - 19), 2.0**-126), 128)[:n]
+
+
+def update(p, g, m, v, least, t):
+    """(p, m, v, bound on a kernel's fp32 p) of a step, v + least under the root."""
+    lr, (b1, b2), eps = HYPER["lr"], HYPER["betas"], HYPER["eps"]
+    m, mm = b1 * m + (1 - b1) * g, b1 * np.abs(m) + (1 - b1) * np.abs(g)
+    v = b2 * v + (1 - b2) * g * g
+    root = np.sqrt((v + least) / (1 - b2**t)) + eps
+    new = p - lr * (m / (1 - b1**t)) / root
+    # m's roundings 5 U; v's 7 U and its sum with the least 1, halved by the
+    # root; constants, root and reciprocal to a unit in the last place, sum and
+    # products: 12 U in all; the result 2 U
+    size = lr * mm / (1 - b1**t) / root
+    return new, m, v, size * (5 + 4 + 12) * U * 1.02 + 2 * U * (np.abs(p) + size) + 2.0**-148
+
+
+def gradients(blocks, ratio, a, t):
+    """[blocks, 128] of one size but for their signs, the first of each block
+    1 / ratio times the others'."""
+    signs = np.random.default_rng(1000 * t + 1).choice([-1.0, 1.0], (blocks, 128))
+    sizes = np.full(128, float(np.float32(a * ratio)))
+    sizes[0] = a
+    return (signs * sizes).ravel()
+
+
+# With gradients of one size s_i for element i, exact moments have steps of at
+# most lr.  Those in 8 bits: the largest element has |m| <= 1.07 a c1 (c1 = 1 -
+# b1^t, and a rounding of 1/16) and v >= a^2 c2 / 2 (roundings of 1/8 at
+# random, whose drift stays far from a half).  Its block's first moments have
+# a lowest code of 2^-9 2^Em < 2^-9 1.07 a c1 / 224, and an element with s_i
+# below it keeps at most one such code, as 0.9 of it and 0.1 s_i are less; its
+# root is at least that of 2^-19 2^Ev >= 2^-19 a^2 c2 / 2 / 61440.  So its step
+# is at most lr 1.07 2^-9 / 224 / sqrt(2^-19 / 122880) = 2.4 lr.  Elements with
+# s_i of some codes: m is below s_i c1 and one code, so (1 + 2.4) lr with the
+# root of their own v or the least alone.
+MOST = 3.4
+
+
+@pytest.mark.parametrize("a,ratio", [(0.125, 2.0**-14), (0.125, 2.0**-17), (1.0, 2.0**-18),
+                                     (1.0, 2.0**-20)])
+def test_steps_of_the_definition(a, ratio):
+    n, blocks = 4 * 128, 4
+    p, m8, v8 = np.zeros(n), plain.moment(np.zeros(n), False), plain.moment(np.zeros(n), True)
+    largest = 0.0
+    for t in range(1, 41):
+        g = gradients(blocks, ratio, a, t)
+        m = plain.moment_values(*m8, n, False)
+        v = plain.moment_values(*v8, n, True)
+        new, m, v, _ = update(p, g, m, v, least_of(v8[1], n), t)
+        largest = max(largest, np.abs(new - p).max())
+        p, m8, v8 = new, plain.moment(m, False, t, 0, 5), plain.moment(v, True, t, 0, 5)
+    assert largest <= MOST
+
+
+torch = pytest.importorskip("torch")
+gpu = pytest.mark.gpu
+
+
+def on_device(x):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.from_numpy(np.asarray(x)).to("cuda")
+
+
+@gpu
+@pytest.mark.parametrize("a,ratio", [(0.125, 2.0**-14), (0.125, 2.0**-17), (1.0, 2.0**-18),
+                                     (1.0, 2.0**-20), (1e-3, 2.0**-18)])
+def test_steps_of_the_kernel(a, ratio):
+    """From zero, step after step: each is what the definition makes of the
+    moments before it, and none is larger than it may be."""
+    from allreduce_compatible_gradient_amd import optim
+    n, blocks = 8 * 128, 8
+    p = on_device(np.zeros(n, dtype=np.float32))
+    m8, v8 = optim.Moment8.zeros(n, "cuda", False), optim.Moment8.zeros(n, "cuda", True)
+    largest = 0.0
+    for t in range(1, 61):
+        g = gradients(blocks, ratio, a, t)
+        old = p.double().cpu().numpy()
+        m, v = (optim.gqs_moment8_restore(x, torch.float32).double().cpu().numpy()
+                for x in (m8, v8))
+        want, _, _, bound = update(old, g, m, v, least_of(v8.exps.cpu().numpy(), n), t)
+        optim.gqs_adamw([p], [on_device(g).float()], [m8], [v8], step=t, seed=7, **HYPER)
+        got = p.double().cpu().numpy()
+        off = np.abs(got - want) / bound
+        assert off.max() <= 1, (t, int(off.argmax()), float(off.max()))
+        largest = max(largest, np.abs(got - old).max())
+    assert largest <= MOST, largest
+
+
+@gpu
+def test_no_step_is_infinite():
+    """eps 0 and second moments whose root is below the least normal float."""
+    from allreduce_compatible_gradient_amd import optim
+    n = 300
+    for g in (1e-22, 3e-39, 0.0):
+        p = on_device(np.ones(n, dtype=np.float32))
+        m8, v8 = optim.Moment8.zeros(n, "cuda", False), optim.Moment8.zeros(n, "cuda", True)
+        for t in (1, 2, 3):
+            optim.gqs_adamw([p], [torch.full_like(p, g)], [m8], [v8], step=t, seed=7,
+                            **{**HYPER, "eps": 0.0})
+            assert torch.isfinite(p).all(), (g, t)
