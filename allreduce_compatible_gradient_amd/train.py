@@ -746,6 +746,22 @@ def _is_plain(module, kind) -> bool:
                      or torch.nn.modules.module._has_any_global_hook()))
 
 
+class _Held:
+    """A plain layer's e4m3 weight and its bias as they were, and what they
+    were made of."""
+
+    def __init__(self, layer):
+        self.weight, self.bias = layer.weight, layer.bias
+        self.memory = layer.weight.detach()  # lives on, so that no other weight gets its address
+        self.copy = _fp8_weight(self.memory, False)
+        self.bias_copy = None if layer.bias is None else layer.bias.detach().clone()
+
+    def is_of(self, layer) -> bool:
+        return (layer.weight is self.weight and layer.bias is self.bias
+                and layer.weight.dtype == self.memory.dtype
+                and layer.weight.data_ptr() == self.memory.data_ptr())
+
+
 _modules = itertools.count()  # numbers the blocks whose seed was not given
 
 
@@ -780,7 +796,7 @@ class Mlp8(torch.nn.Module):
     ``linear(..., fp8=True)`` does.  Each pass makes its copies of the weights;
     ``hold_fp8`` keeps them for the passes without gradients."""
 
-    fp8, _held = False, None  # of a block pickled before it had them
+    fp8, _held, _holding, _handles = False, None, False, ()  # of a block pickled before them
 
     def __init__(self, d: int, hidden: int, *, eps: float = 1e-5, approximate: str = "tanh",
                  random: bool = True, seed: int | None = None, device=None,
@@ -794,37 +810,56 @@ class Mlp8(torch.nn.Module):
         self.approximate, self.random, self.seed, self.passes = approximate, random, seed, 0
         self._drawn = None  # the seed of a block that was given none
         self.fp8 = bool(fp8)
-        self._held = None  # the weights' copies, for passes without gradients
+        self._held = None  # up and down for passes without gradients
+        self._holding = False  # whether those take them
+        self._handles = ()  # of what up and down call where a state is loaded
 
     def hold_fp8(self, hold: bool = True):
-        """Makes the e4m3 copies of up's and down's weights as they are now
-        and takes them, in passes without gradients, until it is called
-        again; hold=False drops them, and so do loading a state and moving
-        or casting the block.  For serving: a pass then reads one byte a
-        weight.  They are made of the weights as they are stored (without
-        them, autocast casts first) and are not in the state dict; weights
-        changed since are not seen."""
+        """Makes e4m3 copies of up's and down's weights, and copies of their
+        biases, as they are now and takes them in passes without gradients.
+        For serving: a pass then reads one byte a weight.
+
+        They are taken until a pass with gradients runs (an update may
+        follow), a state is loaded into the block, up or down, one of them or
+        its weight is replaced, moved or cast, or it is called again;
+        hold=False drops them.  Other changes of a weight or bias in place are
+        not seen.  They are made of the weights as they are stored (without
+        them, autocast casts first) and go into no state dict, copy or pickle.
+        A graph captured with them reads their memory, which stays as it is
+        until the block is moved or cast or this is called again."""
         if hold and not self.fp8:
             raise ValueError("hold_fp8 is for a block with fp8=True")
-        self._held = None
+        for handle in self._handles:
+            handle.remove()
+        self._held, self._holding, self._handles = None, False, ()
         if hold:
-            self._held = tuple(
-                _fp8_weight(m.weight.detach(), False) if _is_plain(m, torch.nn.Linear) else None
-                for m in (self.up, self.down))
+            layers = [m if _is_plain(m, torch.nn.Linear) else None for m in (self.up, self.down)]
+            self._held = tuple(m and _Held(m) for m in layers)
+            self._handles = tuple(m.register_load_state_dict_pre_hook(self._let_go)
+                                  for m in layers if m)
+            self._holding = True
         return self
+
+    def _let_go(self, *args):
+        self._holding = False
+
+    def __getstate__(self):
+        return {**self.__dict__, "_held": None, "_holding": False, "_handles": ()}
 
     def _product(self, x, module, k: int):
         """x through up (k = 0) or down (1), without gradients."""
         if not self.fp8:
             return module(x)
-        held = None if self._held is None else self._held[k]
+        held = self._held[k] if self._holding else None
+        if held is not None and not held.is_of(module):
+            held, self._holding = None, False
         if held is None:
             return linear(x, module.weight, module.bias, fp8=True)
         from .fp8 import gqs_fp8_linear
         dtype = _product_dtype(x)
         with _no_autocast(x):
             x = _cast(x, dtype)
-            y = gqs_fp8_linear(_rows(x, x.shape[-1]), held, _cast(module.bias, dtype))
+            y = gqs_fp8_linear(_rows(x, x.shape[-1]), held.copy, _cast(held.bias_copy, dtype))
         return y.view(*x.shape[:-1], y.shape[-1])
 
     def _pass_seed(self) -> int:
@@ -850,11 +885,11 @@ class Mlp8(torch.nn.Module):
             self._drawn = drawn & 0xFFFFFFFFFFFFFFFF
 
     def _apply(self, *args, **kwargs):
-        self._held = None
+        self._held, self._holding = None, False
         return super()._apply(*args, **kwargs)
 
     def _load_from_state_dict(self, state_dict, prefix, *args):
-        self._held = None
+        self._let_go()
         # a state without them leaves them as they are
         state_dict.setdefault(prefix + "_extra_state", self.get_extra_state())
         super()._load_from_state_dict(state_dict, prefix, *args)
@@ -866,6 +901,7 @@ class Mlp8(torch.nn.Module):
         seed, bits = None, None
         if torch.is_grad_enabled():
             bits = 8
+            self._let_go()
             if self.random:
                 seed = self._pass_seed()
             self.passes += 1
