@@ -130,7 +130,7 @@ def _device_of(tensors, name: str):
 
 def gqs_adamw(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, betas=(0.9, 0.999),
               eps: float = 1e-8, weight_decay: float = 1e-2, scale=None, seed=None,
-              stream=None) -> None:
+              random=None, stream=None) -> None:
     """One AdamW step, in place, over lists of tensors: params of one dtype
     and grads of one dtype (fp32 or bf16 each), moments as fp32 tensors or
     Moment8, all contiguous on one device, no two overlapping.
@@ -138,8 +138,8 @@ def gqs_adamw(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, betas=(0.9, 0.9
     scale: a device float, the gradients' factor.  step counts from 1; it and
     lr may be device tensors (int64 and float32, one element), which a
     captured graph reads at every replay.  A `seed` is needed with Moment8; a
-    bf16 parameter is rounded at random where one is given, to nearest
-    otherwise.  Calls of one step with one seed share random numbers between
+    bf16 parameter is rounded at random where one is given, unless `random` is
+    False, and to nearest otherwise.  Calls of one step with one seed share random numbers between
     tensors of the same number in their lists: give each list its own.
 
     To autograd the params are changed in place, as by torch's own operations."""
@@ -154,7 +154,8 @@ def gqs_adamw(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, betas=(0.9, 0.9
         with _Elsewhere(device, stream, _tensors_of(params, grads, exp_avgs, exp_avg_sqs, scale,
                                                     step, lr)):
             return gqs_adamw(params, grads, exp_avgs, exp_avg_sqs, step=step, lr=lr, betas=betas,
-                             eps=eps, weight_decay=weight_decay, scale=scale, seed=seed)
+                             eps=eps, weight_decay=weight_decay, scale=scale, seed=seed,
+                             random=random)
     p_type, sizes, p_at = _arrays(params, "params", device)
     g_type, g_sizes, g_at = _arrays(grads, "grads", device)
     if g_sizes != sizes:
@@ -165,9 +166,12 @@ def gqs_adamw(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, betas=(0.9, 0.9
         raise TypeError("exp_avgs and exp_avg_sqs must be both Moment8 or both tensors")
     if bits == 8 and seed is None:
         raise ValueError("moments in 8 bits are rounded at random: a seed is needed")
+    if random and seed is None:
+        raise ValueError("random rounding needs a seed")
     args = CAdamWArgs(0.0, betas[0], betas[1], eps, weight_decay, 0,
                       _scalar(scale, "scale", torch.float32, device), None, None,
-                      0 if seed is None else int(seed) & 0xFFFFFFFFFFFFFFFF, seed is not None, bits)
+                      0 if seed is None else int(seed) & 0xFFFFFFFFFFFFFFFF,
+                      seed is not None if random is None else bool(random), bits)
     workspace = None
     if isinstance(lr, torch.Tensor):
         args.lr_device = _scalar(lr, "lr", torch.float32, device)
@@ -405,10 +409,12 @@ class AdamW(torch.optim.Optimizer):
             else:
                 step += 1
             m, v = zip(*(self.moments(p) for p in params))
-            drawn = self.bits == 8 or (self.random and params[0].dtype == torch.bfloat16)
+            bf16 = params[0].dtype == torch.bfloat16
+            drawn = self.bits == 8 or (self.random and bf16)
+            nearest = {"random": False} if drawn and bf16 and not self.random else {}
             gqs_adamw(values, grads, m, v, step=step, lr=group["lr"], betas=group["betas"],
                       eps=group["eps"], weight_decay=group["weight_decay"], scale=scale,
-                      seed=_mix_seed(self.seed, place) if drawn else None)
+                      seed=_mix_seed(self.seed, place) if drawn else None, **nearest)
             if not self.capturable:
                 for p in params:
                     self.state[p]["step"] = step

@@ -74,3 +74,45 @@ def test_a_graph_from_before_a_step_is_refused_on_the_gpu():
     optim.gqs_adamw([p], [p.clone()], [torch.zeros_like(p)], [torch.zeros_like(p)], step=1,
                     lr=1e-3, stream=torch.cuda.Stream())
     assert p._version > 0
+
+
+# ---------------------------------------------------------------------------
+# bf16 parameters to nearest, whatever the moments are
+
+def test_rounding_of_parameters_is_its_own_choice(launches):
+    p, g = torch.ones(3, dtype=torch.bfloat16), torch.ones(3)
+    eights = [optim.Moment8.zeros(3, "cpu", k) for k in (False, True)]
+    wide = [torch.zeros(3) for _ in range(2)]
+    for moments, kw, want in ((eights, dict(seed=1), 1), (eights, dict(seed=1, random=False), 0),
+                              (eights, dict(seed=1, random=True), 1), (wide, dict(), 0),
+                              (wide, dict(seed=1), 1), (wide, dict(seed=1, random=False), 0)):
+        optim.gqs_adamw([p], [g], [moments[0]], [moments[1]], step=1, lr=1e-3, **kw)
+        assert launches.args[-1]["random"] == want, kw
+    with pytest.raises(ValueError):
+        optim.gqs_adamw([p], [g], [wide[0]], [wide[1]], step=1, lr=1e-3, random=True)
+    for bits in (8, 32):
+        for random in (False, True):
+            q = torch.nn.Parameter(p.clone())
+            q.grad = torch.ones_like(q)
+            optim.AdamW([q], bits=bits, random=random).step()
+            assert launches.args[-1]["random"] == random, (bits, random)
+            assert launches.args[-1]["bits"] == bits
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [8, 32])
+def test_parameters_to_nearest_on_the_gpu(bits):
+    """The first step has exact moments, and its change is that of 64 bits: p
+    lies within half a last place of it and fp32's few."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    p = torch.nn.Parameter(torch.randn(5000, device="cuda").bfloat16())
+    p.grad = torch.randn(5000, device="cuda").bfloat16()
+    old, g = p.detach().double(), p.grad.double()
+    optim.AdamW([p], lr=1e-2, bits=bits, random=False, seed=3).step()
+    want = old * (1 - 1e-4) - 1e-2 * g / (g.abs() + 1e-8)
+    half = torch.exp2(torch.floor(torch.log2(want.abs())) - 8)
+    # constants, moments, root, quotient and sums: below 2^-18 of the change
+    # and 2^-22 of p
+    slack = 2.0**-18 * 1e-2 + 2.0**-22 * old.abs()
+    assert ((p.double() - want).abs() <= half + slack).all()
