@@ -311,6 +311,7 @@ class AdamW(torch.optim.Optimizer):
 
     def _new_state(self, p):
         n, device = p.numel(), p.device
+        order = _order(p)
         _refuse_capture(device)
         if self.bits == 32:
             state = {"exp_avg": torch.zeros(n, device=device),
@@ -319,13 +320,16 @@ class AdamW(torch.optim.Optimizer):
             m, v = Moment8.zeros(n, device, False), Moment8.zeros(n, device, True)
             state = {"exp_avg": m.codes, "exp_avg_exps": m.exps,
                      "exp_avg_sq": v.codes, "exp_avg_sq_exps": v.exps}
+        # p's sizes, and the order of its dimensions in which the moments lie
+        state["shape"], state["order"] = list(p.shape), order
         if not self.capturable:
             state["step"] = 0
         return state
 
     def moments(self, p):
-        """p's (first, second) moment, flat in the order of its memory: fp32
-        tensors or Moment8."""
+        """p's (first, second) moment, flat in the order that p's memory had
+        in its first step (``state[p]["order"]`` of its dimensions; None:
+        their own): fp32 tensors or Moment8."""
         state = self.state[p]
         if self.bits == 32:
             return state["exp_avg"], state["exp_avg_sq"]
@@ -335,8 +339,9 @@ class AdamW(torch.optim.Optimizer):
 
     def _buckets(self):
         """What one call takes: (group, step, place of its first parameter,
-        parameters, flat values, flat gradients), by group, device, types and
-        step."""
+        parameters, values and gradients in the moments' order, and those
+        values that are copies with where they belong), by group, device,
+        types and step."""
         buckets, place = {}, 0
         for k, group in enumerate(self.param_groups):
             for p in group["params"]:
@@ -351,14 +356,19 @@ class AdamW(torch.optim.Optimizer):
                 state = self.state[p]
                 if not state:
                     state.update(self._new_state(p))
-                order = _order(p)
+                if "order" not in state:  # saved without it
+                    state["order"] = _order(p)
+                order = state["order"]
                 value, g = p.detach(), g.detach()
                 if order is not None:
                     value, g = value.permute(order), g.permute(order)
                 step = None if self.capturable else state["step"]
                 key = (k, p.device, p.dtype, g.dtype, step)
                 if key not in buckets:
-                    buckets[key] = (group, step, place, [], [], [])
+                    buckets[key] = (group, step, place, [], [], [], [])
+                if not value.is_contiguous():  # p lies in another order since
+                    buckets[key][6].append((value, value.contiguous()))
+                    value = buckets[key][6][-1][1]
                 buckets[key][3].append(p)
                 buckets[key][4].append(value)
                 buckets[key][5].append(g.contiguous())
@@ -401,7 +411,7 @@ class AdamW(torch.optim.Optimizer):
                                "the number of this one")
         scale = self._clip(buckets)
         counted = {}
-        for group, step, place, params, values, grads in buckets:
+        for group, step, place, params, values, grads, copies in buckets:
             if self.capturable:
                 if id(group) not in counted:
                     counted[id(group)] = self._count(group, params[0].device)
@@ -415,15 +425,36 @@ class AdamW(torch.optim.Optimizer):
             gqs_adamw(values, grads, m, v, step=step, lr=group["lr"], betas=group["betas"],
                       eps=group["eps"], weight_decay=group["weight_decay"], scale=scale,
                       seed=_mix_seed(self.seed, place) if drawn else None, **nearest)
+            for view, value in copies:
+                view.copy_(value)
             if not self.capturable:
                 for p in params:
                     self.state[p]["step"] = step
         return loss
 
+    def _check_sizes(self, i, state, p):
+        """Whether saved moments are those of a parameter like p."""
+        if state.get("shape", list(p.shape)) != list(p.shape):
+            raise ValueError(f"the state of parameter {i} is of {state['shape']}, its parameter "
+                             f"{list(p.shape)}")
+        blocks = (p.numel() + 127) // 128
+        sizes = {"exp_avg": p.numel()} if self.bits == 32 else {"exp_avg": 128 * blocks,
+                                                                "exp_avg_exps": blocks}
+        for key, n in sizes.items():
+            for name in (key, key.replace("avg", "avg_sq")):
+                if name in state and state[name].numel() != n:
+                    raise ValueError(f"the state of parameter {i} has {state[name].numel()} "
+                                     f"elements of {name}, its parameter takes {n}")
+
     def load_state_dict(self, state_dict):
         """As torch's, which would cast moments and codes to the parameters'
-        types: they come as they were saved.  Steps counted on the host and
-        on the device are taken for each other."""
+        types: they come as they were saved, for parameters of the same shapes
+        in any memory order.  Steps counted on the host and on the device are
+        taken for each other."""
+        saved = [i for group in state_dict["param_groups"] for i in group["params"]]
+        own = [p for group in self.param_groups for p in group["params"]]
+        for i, p in zip(saved, own):
+            self._check_sizes(i, state_dict["state"].get(i, {}), p)
         for group in state_dict["param_groups"]:
             states = [state_dict["state"].get(i, {}) for i in group["params"]]
             for state in states:
@@ -433,12 +464,13 @@ class AdamW(torch.optim.Optimizer):
             if self.capturable and len({state["step"] for state in states if "step" in state}) > 1:
                 raise ValueError("capturable=True has one count for a group, the state's differ")
         super().load_state_dict(state_dict)
-        saved = [i for group in state_dict["param_groups"] for i in group["params"]]
         own = [p for group in self.param_groups for p in group["params"]]
         for i, p in zip(saved, own):
             for key, value in state_dict["state"].get(i, {}).items():
                 if isinstance(value, torch.Tensor):
                     value = value.detach().clone().to(p.device)
+                elif isinstance(value, list):
+                    value = list(value)
                 self.state[p][key] = value
         for group in self.param_groups:
             states = [self.state[p] for p in group["params"] if self.state.get(p)]

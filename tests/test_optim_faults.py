@@ -116,3 +116,86 @@ def test_parameters_to_nearest_on_the_gpu(bits):
     # and 2^-22 of p
     slack = 2.0**-18 * 1e-2 + 2.0**-22 * old.abs()
     assert ((p.double() - want).abs() <= half + slack).all()
+
+
+# ---------------------------------------------------------------------------
+# moments lie in the order of the parameter that they were made for
+
+def relaid(p):
+    """p's values in other memory orders."""
+    orders = [p.detach().contiguous(), p.detach().transpose(0, -1).contiguous().transpose(0, -1)]
+    if p.dim() == 4:
+        orders.append(p.detach().contiguous(memory_format=torch.channels_last))
+    return orders
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_state_goes_to_a_parameter_of_another_order(device, bits):  # noqa: F811
+    ps = parameters(device)
+    opt = optim.AdamW(ps, lr=1e-2, bits=bits, seed=4)
+    for step in (1, 2):
+        give(ps, step)
+        opt.step()
+    saved = opt.state_dict()
+    twins = []
+    for k in range(3):
+        qs = [torch.nn.Parameter(relaid(p)[min(k, p.dim() // 2)].clone(
+            memory_format=torch.preserve_format)) for p in ps]
+        again = optim.AdamW(qs, lr=1e-2, bits=bits, seed=4)
+        again.load_state_dict(saved)
+        for step in (3, 4):
+            give(qs, step, same_layout=step == 3)
+            again.step()
+        twins.append((again, qs))
+    for step in (3, 4):
+        give(ps, step)
+        opt.step()
+    for again, qs in twins:
+        for p, q in zip(ps, qs):
+            assert torch.equal(p, q), (p.stride(), q.stride())
+            for a, b in zip(opt.moments(p), again.moments(q)):
+                same = (torch.equal(a, b) if bits == 32 else
+                        torch.equal(a.codes.view(torch.uint8), b.codes.view(torch.uint8)))
+                assert same
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_parameter_that_is_laid_out_anew(device, bits):  # noqa: F811
+    ps, qs = parameters(device), parameters(device)
+    one, other = (optim.AdamW(x, lr=1e-2, bits=bits, seed=4) for x in (ps, qs))
+    for step in range(1, 5):
+        give(ps, step)
+        give(qs, step)
+        one.step()
+        other.step()
+        for q in qs:
+            q.data = relaid(q)[step % len(relaid(q))].clone(memory_format=torch.preserve_format)
+    for p, q in zip(ps, qs):
+        assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_state_of_other_sizes_is_refused(device, bits):  # noqa: F811
+    ps = parameters(device)
+    opt = optim.AdamW(ps, bits=bits)
+    give(ps, 1)
+    opt.step()
+    for shape in ((7, 6), (5, 7), (35, 40), (35,)):
+        qs = parameters(device)
+        qs[0] = torch.nn.Parameter(leaf(device, *shape, seed=1).detach())
+        again = optim.AdamW(qs, bits=bits)
+        with pytest.raises(ValueError):
+            again.load_state_dict(opt.state_dict())
+        assert not again.state
+    # a state without shapes, as older ones: by the numbers of elements
+    old = opt.state_dict()
+    for state in old["state"].values():
+        del state["shape"], state["order"]
+    with pytest.raises(ValueError):
+        again = optim.AdamW([torch.nn.Parameter(leaf(device, 300, seed=1).detach())]
+                            + parameters(device)[1:], bits=bits)
+        again.load_state_dict(old)
+    same = optim.AdamW(parameters(device), bits=bits)
+    same.load_state_dict(old)
+    give(same.param_groups[0]["params"], 2)
+    same.step()
