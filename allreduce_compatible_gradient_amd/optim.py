@@ -58,6 +58,7 @@ class Moment8:
 # by maps of C functions, not tensor by tensor.
 _dtype_of, _index = operator.attrgetter("dtype"), torch.Tensor.get_device
 _numel, _data_ptr = torch.Tensor.numel, torch.Tensor.data_ptr
+_device, _sparse = operator.attrgetter("device"), operator.attrgetter("is_sparse")
 _codes, _exps, _count = map(operator.attrgetter, ("codes", "exps", "n"))
 
 
@@ -261,6 +262,21 @@ def _refuse_capture(device) -> None:
         raise RuntimeError("a parameter's first step cannot be captured: take it before")
 
 
+_MOST = 1 << 34  # a tensor has fewer elements
+
+
+def _check_settings(lr, betas, eps, weight_decay, capturable: bool) -> None:
+    if isinstance(lr, torch.Tensor):
+        if not capturable:
+            raise ValueError("lr may be a tensor with capturable=True")
+    elif not 0.0 <= lr < float("inf"):
+        raise ValueError(f"lr must be finite and not negative, got {lr}")
+    if len(betas) != 2 or not all(0.0 <= b < 1.0 for b in betas):
+        raise ValueError(f"betas must be two numbers from 0 to below 1, got {betas}")
+    if not 0.0 <= eps < float("inf") or not 0.0 <= weight_decay < float("inf"):
+        raise ValueError("eps and weight_decay must be finite and not negative")
+
+
 class AdamW(torch.optim.Optimizer):
     """AdamW (decoupled weight decay) on ROCm devices, all parameters of a
     type in one launch.
@@ -289,15 +305,7 @@ class AdamW(torch.optim.Optimizer):
                  seed: int = 0, max_norm: float | None = None, capturable: bool = False):
         if bits not in (8, 32):
             raise ValueError(f"bits must be 8 or 32, got {bits!r}")
-        if isinstance(lr, torch.Tensor):
-            if not capturable:
-                raise ValueError("lr may be a tensor with capturable=True")
-        elif not 0.0 <= lr < float("inf"):
-            raise ValueError(f"lr must be finite and not negative, got {lr}")
-        if len(betas) != 2 or not all(0.0 <= b < 1.0 for b in betas):
-            raise ValueError(f"betas must be two numbers from 0 to below 1, got {betas}")
-        if not 0.0 <= eps < float("inf") or not 0.0 <= weight_decay < float("inf"):
-            raise ValueError("eps and weight_decay must be finite and not negative")
+        _check_settings(lr, betas, eps, weight_decay, capturable)
         if max_norm is not None and not 0.0 <= max_norm < float("inf"):
             raise ValueError(f"max_norm must be finite and not negative, got {max_norm}")
         super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps,
@@ -337,6 +345,30 @@ class AdamW(torch.optim.Optimizer):
         return (Moment8(state["exp_avg"], state["exp_avg_exps"], n),
                 Moment8(state["exp_avg_sq"], state["exp_avg_sq_exps"], n))
 
+    def _check(self):
+        """Refuses what a step would, before it has changed anything."""
+        for group in self.param_groups:
+            _check_settings(group["lr"], group["betas"], group["eps"], group["weight_decay"],
+                            self.capturable)
+            params = [p for p in group["params"] if p.grad is not None]
+            grads = [p.grad for p in params]
+            if any(map(_sparse, grads)):
+                raise RuntimeError("AdamW takes no sparse gradients")
+            devices = dict(zip(map(_device, params), params))
+            for device, p in devices.items():
+                if not _on_device(p):
+                    raise ValueError(f"AdamW takes parameters on a device, one is on {device}")
+            for name, tensors in (("a parameter", params), ("a gradient", grads)):
+                for dtype in set(map(_dtype_of, tensors)):
+                    _dtype(dtype, name)
+            if max(map(_numel, params), default=0) >= _MOST:
+                raise ValueError("a parameter has 2^34 elements or more")
+            if self.capturable and len(devices) > 1:
+                raise ValueError("capturable=True takes a group's parameters on one device, got "
+                                 f"{sorted(map(str, devices))}")
+            if isinstance(group["lr"], torch.Tensor) and devices:
+                _scalar(group["lr"], "lr", torch.float32, *devices)
+
     def _buckets(self):
         """What one call takes: (group, step, place of its first parameter,
         parameters, values and gradients in the moments' order, and those
@@ -349,10 +381,6 @@ class AdamW(torch.optim.Optimizer):
                 if p.grad is None:
                     continue
                 g = p.grad
-                if g.is_sparse:
-                    raise RuntimeError("AdamW takes no sparse gradients")
-                if not _on_device(p):
-                    raise ValueError(f"AdamW takes parameters on a device, one is on {p.device}")
                 state = self.state[p]
                 if not state:
                     state.update(self._new_state(p))
@@ -405,6 +433,7 @@ class AdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        self._check()
         buckets = self._buckets()
         if not self.capturable and buckets and _capturing(buckets[0][3][0].device):
             raise RuntimeError("a captured step needs capturable=True: the graph would keep "

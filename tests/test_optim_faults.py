@@ -199,3 +199,38 @@ def test_a_state_of_other_sizes_is_refused(device, bits):  # noqa: F811
     same.load_state_dict(old)
     give(same.param_groups[0]["params"], 2)
     same.step()
+
+
+# ---------------------------------------------------------------------------
+# a step is taken as a whole or not at all
+
+def test_a_step_that_is_refused_changes_nothing(device):  # noqa: F811
+    """Whatever comes last: another type, another device, a setting."""
+    def param(dtype=torch.float32, on=device):
+        p = torch.nn.Parameter(torch.ones(5, device=on, dtype=dtype))
+        p.grad = torch.ones_like(p)
+        return p
+
+    def sparse():
+        p = param()
+        p.grad = torch.sparse_coo_tensor([[0]], [1.0], (5,), device=device)
+        return p
+    rate = torch.tensor(1e-3, device=device, dtype=torch.float64)
+    for bad, kw, setting in ((param(torch.float16), {}, {}), (param(torch.float64), {}, {}),
+                             (param(on="meta"), dict(capturable=True), {}), (sparse(), {}, {}),
+                             (param(), {}, dict(lr=-1.0)), (param(), {}, dict(lr=rate)),
+                             (param(), dict(capturable=True), dict(lr=rate)),
+                             (param(), {}, dict(betas=(0.9, 1.0))),
+                             (param(), {}, dict(weight_decay=float("nan")))):
+        for apart in (False, True):
+            if setting and not apart:
+                continue
+            p = param()
+            groups = [{"params": [p]}, {"params": [bad]}] if apart else [p, bad]
+            if apart and bad.device.type == "meta" and device == "cpu":
+                continue  # a group each: no fault
+            opt = optim.AdamW(groups, **kw)
+            opt.param_groups[-1].update(setting)
+            with pytest.raises((TypeError, ValueError, RuntimeError)):
+                opt.step()
+            assert (p == 1).all() and not opt.state and "step" not in opt.param_groups[0]
