@@ -294,11 +294,13 @@ class AdamW(torch.optim.Optimizer):
     process group's ranks, which step with equal gradients, stay equal while
     they have one seed.
 
-    capturable=True counts steps on the device, one count for a group, so that
-    a captured graph goes on counting (and draws new numbers) at each replay;
-    lr may then be a float32 tensor on the device.  A parameter's first step
-    makes its moments and is taken before a capture.  Otherwise each parameter
-    counts the steps in which it had a gradient."""
+    Each parameter counts the steps in which it had a gradient.
+    capturable=True counts on the device, so that a captured graph goes on
+    counting (and draws new numbers) at each replay; lr may then be a float32
+    tensor on the device.  A group's parameters share a count
+    (``param_groups[k]["step"]``) while they have gradients in the same steps;
+    the others get one of their own, in their state.  That, like a parameter's
+    first step, which makes its moments, is done before a capture."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 1e-2, *, bits: int = 32, random: bool = True,
@@ -373,9 +375,12 @@ class AdamW(torch.optim.Optimizer):
         """What one call takes: (group, step, place of its first parameter,
         parameters, values and gradients in the moments' order, and those
         values that are copies with where they belong), by group, device,
-        types and step."""
+        types and step (with capturable: its count, None for the group's)."""
         buckets, place = {}, 0
         for k, group in enumerate(self.param_groups):
+            first = None  # the count of parameters that begin behind their group
+            if self.capturable:
+                self._part_counts(group)
             for p in group["params"]:
                 place += 1
                 if p.grad is None:
@@ -384,14 +389,18 @@ class AdamW(torch.optim.Optimizer):
                 state = self.state[p]
                 if not state:
                     state.update(self._new_state(p))
+                    if self.capturable and "step" in group:
+                        if first is None:
+                            first = torch.zeros(1, dtype=torch.int64, device=p.device)
+                        state["step"] = first
                 if "order" not in state:  # saved without it
                     state["order"] = _order(p)
                 order = state["order"]
                 value, g = p.detach(), g.detach()
                 if order is not None:
                     value, g = value.permute(order), g.permute(order)
-                step = None if self.capturable else state["step"]
-                key = (k, p.device, p.dtype, g.dtype, step)
+                step = state.get("step")
+                key = (k, p.device, p.dtype, g.dtype, id(step) if self.capturable else step)
                 if key not in buckets:
                     buckets[key] = (group, step, place, [], [], [], [])
                 if not value.is_contiguous():  # p lies in another order since
@@ -419,13 +428,30 @@ class AdamW(torch.optim.Optimizer):
         self.last_norm = norms.double().square().sum().sqrt().float()
         return (self.max_norm / (self.last_norm + 1e-6)).clamp(max=1.0)
 
+    def _part_counts(self, group):
+        """Gives those of a count's parameters that have no gradient now a
+        count of their own where others have one."""
+        counts = {}
+        for p in group["params"]:
+            state = self.state.get(p)
+            if state:
+                count = state.get("step", group.get("step"))
+                counts.setdefault(id(count), (count, [], []))[1 if p.grad is None else 2].append(p)
+        for count, still, stepping in counts.values():
+            if still and stepping and count is not None:
+                if _capturing(count.device):
+                    raise RuntimeError("a captured step takes gradients of the parameters that "
+                                       "had them before: take one with these before")
+                own = count.clone()
+                for p in still:
+                    self.state[p]["step"] = own
+
     def _count(self, group, device):
-        """The group's number of steps on the device, one more than before."""
-        count = group.get("step")
-        if count is None:
+        """The group's number of steps on the device."""
+        if group.get("step") is None:
             _refuse_capture(device)
-            count = group["step"] = torch.zeros(1, dtype=torch.int64, device=device)
-        return count.add_(1)
+            group["step"] = torch.zeros(1, dtype=torch.int64, device=device)
+        return group["step"]
 
     @torch.no_grad()
     def step(self, closure=None):
@@ -442,9 +468,10 @@ class AdamW(torch.optim.Optimizer):
         counted = {}
         for group, step, place, params, values, grads, copies in buckets:
             if self.capturable:
-                if id(group) not in counted:
-                    counted[id(group)] = self._count(group, params[0].device)
-                step = counted[id(group)]
+                if step is None:
+                    step = self._count(group, params[0].device)
+                if id(step) not in counted:
+                    counted[id(step)] = step.add_(1)
             else:
                 step += 1
             m, v = zip(*(self.moments(p) for p in params))
@@ -490,8 +517,11 @@ class AdamW(torch.optim.Optimizer):
                 codes = state.get("exp_avg")
                 if codes is not None and (codes.dtype == torch.float32) != (self.bits == 32):
                     raise ValueError(f"the state has other moments than those of bits={self.bits}")
-            if self.capturable and len({state["step"] for state in states if "step" in state}) > 1:
-                raise ValueError("capturable=True has one count for a group, the state's differ")
+            counts = {state["step"] for state in states
+                      if not isinstance(state.get("step"), (type(None), torch.Tensor))}
+            if self.capturable and len(counts) > 1:
+                raise ValueError("capturable=True takes one count for a group over from the "
+                                 f"host's, the state's are {sorted(counts)}")
         super().load_state_dict(state_dict)
         own = [p for group in self.param_groups for p in group["params"]]
         for i, p in zip(saved, own):
@@ -503,12 +533,17 @@ class AdamW(torch.optim.Optimizer):
                 self.state[p][key] = value
         for group in self.param_groups:
             states = [self.state[p] for p in group["params"] if self.state.get(p)]
-            count = group.pop("step", None)
-            if self.capturable:
-                for state in states:
-                    count = state.pop("step", count)
-                if count is not None:
-                    group["step"] = torch.tensor([int(count)], device=group["params"][0].device)
-            elif count is not None:
-                for state in states:
-                    state["step"] = int(count)
+            common = group.pop("step", None)
+            steps = [state.pop("step", common) for state in states]
+            steps = [0 if n is None else int(n) for n in steps]
+            if not self.capturable:
+                for state, n in zip(states, steps):
+                    state["step"] = n
+            elif steps:
+                common = steps[0] if common is None else int(common)
+                counts = {n: torch.tensor([n], device=states[0]["exp_avg"].device)
+                          for n in {common, *steps}}
+                group["step"] = counts[common]
+                for state, n in zip(states, steps):
+                    if n != common:
+                        state["step"] = counts[n]

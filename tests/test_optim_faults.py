@@ -234,3 +234,78 @@ def test_a_step_that_is_refused_changes_nothing(device):  # noqa: F811
             with pytest.raises((TypeError, ValueError, RuntimeError)):
                 opt.step()
             assert (p == 1).all() and not opt.state and "step" not in opt.param_groups[0]
+
+
+# ---------------------------------------------------------------------------
+# steps counted on the device: each parameter's own
+
+def _run_with_gaps(device, capturable, bits, present):
+    ps = parameters(device)
+    opt = optim.AdamW([{"params": ps[:3]}, {"params": ps[3:]}], lr=1e-2, bits=bits, seed=4,
+                      capturable=capturable)
+    for step, these in enumerate(present, 1):
+        give(ps, step)
+        for k, p in enumerate(ps):
+            if k not in these:
+                p.grad = None
+        opt.step()
+    return ps, opt
+
+
+def count_of(opt, p):
+    group = next(g for g in opt.param_groups if any(q is p for q in g["params"]))
+    return int(opt.state[p].get("step", group.get("step")))
+
+
+GAPS = [[(0, 3), (0, 1, 3), (0, 1, 2, 3)],            # first gradients that come late
+        [(0, 1, 2, 3), (0, 1), (0, 1), (0, 1, 2, 3)],  # and that stay away
+        [(0,), (1,), (0,), (1, 2), (0, 1, 2, 3)]]
+
+
+@pytest.mark.parametrize("present", GAPS)
+def test_counts_on_the_device_are_those_on_the_host(device, present):  # noqa: F811
+    ps, opt = _run_with_gaps(device, False, 32, present)
+    qs, other = _run_with_gaps(device, True, 32, present)
+    for k, (p, q) in enumerate(zip(ps, qs)):
+        assert count_of(opt, p) == count_of(other, q) == sum(k in these for these in present)
+        # powers on the device and on the host may differ in a factor's last bit
+        assert ((p - q).abs() <= 2.0**-21 * (q.abs() + 1e-2)).all()
+    for kind in (False, True):  # a state goes over, and goes on
+        rs = [torch.nn.Parameter(q.detach().clone(memory_format=torch.preserve_format))
+              for q in qs]
+        again = optim.AdamW([{"params": rs[:3]}, {"params": rs[3:]}], lr=1e-2, seed=4,
+                            capturable=kind)
+        again.load_state_dict(other.state_dict())
+        give(rs, 9)
+        again.step()
+        assert [count_of(again, r) for r in rs] == [count_of(other, q) + 1 for q in qs]
+
+
+def test_counts_do_not_part_in_a_capture(device, monkeypatch):  # noqa: F811
+    ps, opt = _run_with_gaps(device, True, 32, GAPS[1])
+    before = [p.detach().clone() for p in ps]
+    ps[0].grad = None
+    with monkeypatch.context() as m:
+        m.setattr(optim, "_capturing", lambda device: True)
+        with pytest.raises(RuntimeError):
+            opt.step()
+    assert all(torch.equal(p, q) for p, q in zip(ps, before))
+
+
+@pytest.mark.gpu
+def test_captured_steps_count_for_each():
+    """A graph goes on with counts that have parted."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    ps, opt = _run_with_gaps("cuda", True, 32, GAPS[0])
+    qs, other = _run_with_gaps("cuda", True, 32, GAPS[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.step()
+    for _ in range(3):
+        graph.replay()
+        other.step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(ps, qs))
+    assert [count_of(opt, p) for p in ps] == [6, 5, 4, 6]
