@@ -489,7 +489,12 @@ class AdamW(torch.optim.Optimizer):
         return loss
 
     def _check_sizes(self, i, state, p):
-        """Whether saved moments are those of a parameter like p."""
+        """Whether saved moments are this optimizer's, of a parameter like p."""
+        steps = state.get("step")
+        if (state and not {"exp_avg", "exp_avg_sq"} <= state.keys()
+                or any(v.dim() != 1 for v in state.values() if isinstance(v, torch.Tensor))
+                or isinstance(steps, torch.Tensor) and steps.is_floating_point()):
+            raise ValueError(f"the state of parameter {i} is another optimizer's")
         if state.get("shape", list(p.shape)) != list(p.shape):
             raise ValueError(f"the state of parameter {i} is of {state['shape']}, its parameter "
                              f"{list(p.shape)}")

@@ -309,3 +309,21 @@ def test_captured_steps_count_for_each():
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(ps, qs))
     assert [count_of(opt, p) for p in ps] == [6, 5, 4, 6]
+
+
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["AdamW", "Adam", "SGD", "Adagrad"])
+@pytest.mark.parametrize("capturable", [False, True])
+def test_another_optimizers_state_is_refused(device, kind, capturable):  # noqa: F811
+    """Where it is loaded, not in the next step; shapes of one dimension, too."""
+    for which in ([1], [0], [0, 1, 2, 3]):
+        ps = [parameters(device)[k] for k in which]
+        give(ps, 1)
+        of = getattr(torch.optim, kind)(ps, lr=1e-2, **({"momentum": 0.9} if kind == "SGD" else {}))
+        of.step()
+        opt = optim.AdamW(ps, capturable=capturable)
+        with pytest.raises(ValueError):
+            opt.load_state_dict(of.state_dict())
+        assert not opt.state
+        opt.step()
