@@ -406,19 +406,21 @@ struct Range {
 // The ranges mostly come in order, as they were allocated, and sort at once.
 int32_t check_overlap(const gqs_tensor *tensors, int64_t count, int64_t p_bytes, int bits)
 {
-    Range few[3 * kTensors], *all = few;
-    if (count > kTensors && !(all = new (std::nothrow) Range[3 * count]))
+    const int arrays = bits == 8 ? 5 : 3;
+    Range few[5 * kTensors], *all = few;
+    if (count > kTensors && !(all = new (std::nothrow) Range[arrays * count]))
         return fail(GQ_ERR_UNSUPPORTED, "%lld tensors", (long long)count);
     int64_t used = 0;
     const auto add = [&](const void *p, int64_t bytes) {
         all[used++] = {(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes};
     };
-    for (int which = 0; which < 3; ++which)
+    for (int which = 0; which < arrays; ++which)
         for (int64_t i = 0; i < count; ++i) {
             const gqs_tensor &t = tensors[i];
+            const void *const at[5] = {t.p, t.m, t.v, t.m_exps, t.v_exps};
             const int64_t state = bits == 8 ? fp8_pitch(t.n) : 4 * t.n;
             if (t.n > 0)
-                add(which == 0 ? t.p : which == 1 ? t.m : t.v, which == 0 ? p_bytes * t.n : state);
+                add(at[which], which == 0 ? p_bytes * t.n : which < 3 ? state : blocks_of(t.n));
         }
     const auto before = [](const Range &a, const Range &b) { return a.begin < b.begin; };
     if (!std::is_sorted(all, all + used, before))
