@@ -636,8 +636,9 @@ class _Linear(torch.autograd.Function):
                 _matrix(x2, "x")  # refuses what the copy would
                 kept = None
             ctx.d = x2.shape[1]
-            y, w8 = _forward_product(x, weight, bias, fp8, need[0])
-            ctx.save_for_backward(weight if need[0] and not fp8 else None, *_parts(kept),
+            need_dx = grad and need[0]
+            y, w8 = _forward_product(x, weight, bias, fp8, need_dx)
+            ctx.save_for_backward(weight if need_dx and not fp8 else None, *_parts(kept),
                                   *_fp8_parts(w8))
             return y
 

@@ -143,3 +143,20 @@ def test_a_captured_pass_keeps_what_it_reads():
         assert torch.equal(y, want)
         del more
     assert not torch.equal(run(block, x), want)
+
+
+def test_a_product_without_gradients_makes_no_transposed_copy(monkeypatch):
+    """Whether or not its inputs could have some."""
+    from allreduce_compatible_gradient_amd import fp8
+    install(monkeypatch)
+    made, make = [], fp8.gqs_fp8_weight
+    monkeypatch.setattr(fp8, "gqs_fp8_weight",
+                        lambda w, *, transposed=True: made.append(transposed)
+                        or make(w, transposed=transposed))
+    x, w = leaf("cpu", 4, 40, seed=1), leaf("cpu", 30, 40, seed=2)
+    with torch.no_grad():
+        train.linear(x, w, fp8=True)
+    train.linear(x.detach(), w, fp8=True).sum().backward()
+    assert made == [False, False]
+    train.linear(x, w, fp8=True).sum().backward()
+    assert made == [False, False, True] and x.grad is not None
