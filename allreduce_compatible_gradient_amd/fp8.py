@@ -7,8 +7,9 @@ square of 128 x 128 for weights (``Fp8Weight``, which serve the forward
 product and, transposed, the one for the gradient of its input).  The matrix
 cores apply the powers of two, so that y = x w^T + b runs at their 8-bit rate.
 Rounding is to nearest or, given a seed, at random without bias; the gradient
-of the input is linear in the gradient of the output, whose random rounding
-leaves its expectation exact.
+of the input is linear in the copy of the gradient of the output, whose
+rounding at random leaves its expectation as it is (not so the sums' own
+roundings: see ``gqs_fp8_product``).
 
 ``gqs_*`` are the C entry points on CUDA (HIP) tensors, with the conventions
 of ``train``'s: [rows, d] with unit column stride, new contiguous outputs,
@@ -245,9 +246,10 @@ def gqs_fp8_product_workspace_bytes(m: int, cols: int, depth: int, dtype=torch.b
 def gqs_fp8_product(x: Fp8, w: Fp8Weight, bias=None, *, transposed: bool = False,
                     dtype=torch.bfloat16, workspace=None, stream=None) -> torch.Tensor:
     """x w^T + bias, or with `transposed` x w + bias, from the copies; the
-    result and its sums in `dtype` and fp32 (fp32 results are exact products
-    summed in fp32; for bf16 ones the matrix cores add the products of 8-bit
-    values in groups, about 2^-13 of a group's largest being lost)."""
+    result and its sums in `dtype` and fp32 (fp32 results, and bf16 ones of
+    few rows, are exact products summed in fp32; for bf16 ones of many rows
+    the matrix cores add the products of 8-bit values in groups of eight, each
+    of which can lose up to 7 2^-13 of its largest)."""
     dt = _dtype(dtype, "dtype")
     if not isinstance(x, Fp8) or not isinstance(x.codes, torch.Tensor) or not x.codes.is_cuda:
         raise ValueError("x must be an Fp8 on a device")

@@ -85,9 +85,11 @@ int32_t gqs_fp8_restore(const void *codes, const void *exps, int64_t rows, int64
  * the weight [cols][depth] and w_codes its codes; transposed 1: w' is the
  * transpose of the weight [depth][cols] and w_codes its codes_t.  w_exps are
  * the weight's exps either way.  bias [cols] in bias_dtype, or NULL.
- * y in dtype.  fp32 results are sums in fp32 of exact products; for bf16
- * ones the matrix cores add eight-bit products in groups, which leaves an
- * error of up to about 2^-13 of the largest product of a group.  The
+ * y in dtype.  fp32 results, and bf16 ones of up to 16 rows, are sums in fp32
+ * of exact products, as those of up to 128 rows are where no tile of more is
+ * faster.  For other bf16 ones the matrix cores add eight-bit products in
+ * groups of eight, of which each of the seven others can lose 2^-13 of the
+ * largest: up to 7 2^-13 of it in a group.  The
  * workspace size also depends on m; 0 bytes may come as NULL.              */
 int64_t gqs_fp8_product_workspace_bytes(int64_t m, int64_t cols, int64_t depth, int32_t dtype);
 int32_t gqs_fp8_product(const void *x_codes, const void *x_exps, int64_t m, const void *w_codes,
