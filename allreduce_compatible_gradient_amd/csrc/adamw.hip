@@ -165,7 +165,7 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const Tensors a, Coefs by_va
     for (int32_t i = 8 * threadIdx.x; i < end; i += 8 * kThreads) {
         float pv[8], gv[8], m[8], v[8];
         float keep1 = r.beta1, keep2 = r.beta2; // of m and v as they are in registers
-        float least = 0.0f;                     // what the root takes v with
+        uint32_t least = 0;                     // bits of what the root takes at least
         load8(p, i, n, pv);
         load8(g, i, n, gv);
         if constexpr (BITS == 8) {
@@ -177,10 +177,10 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const Tensors a, Coefs by_va
             const uint32_t ev = ((const uint8_t *)t.v_exps)[at / 128];
             e4m3_values(wm, 1.0f, m);
             keep1 *= step_of(em);
-            // Half the lowest step of v's block as it came: a v below that step
-            // is mostly 0 there, while its m is now and then a whole lowest
-            // step, whose quotient would have no bound.
-            least = bits_f32((max(ev, 20u) - 19u) << 23);
+            // The lowest step of v's block as it came: a v below it is mostly 0
+            // there, while its m is now and then a whole lowest step, whose
+            // quotient would have no bound.
+            least = (max(ev, 18u) - 18u) << 23;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 v[k] = e5m3_small(wv, k);
@@ -202,10 +202,12 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const Tensors a, Coefs by_va
             m[k] = fmaf(keep1, m[k], r.other1 * gs);
             v[k] = fmaf(keep2, v[k], r.other2 * (gs * gs));
             // The 8-bit moments' roundings leave no time for a division and a
-            // root to the last bit: a unit in the last place each.
+            // root to the last bit: a unit in the last place each.  The bits of
+            // numbers from 0 on are in their order, a NaN's above all.
+            const float under = bits_f32(max(__float_as_uint(v[k]), least));
             const float change =
                 BITS == 8 ? m[k] * __builtin_amdgcn_rcpf(
-                                       fmaf(__builtin_amdgcn_sqrtf(v[k] + least), c.root, r.eps))
+                                       fmaf(__builtin_amdgcn_sqrtf(under), c.root, r.eps))
                           : m[k] / fmaf(sqrtf(v[k]), c.root, r.eps);
             pv[k] = fmaf(-c.size, change, pv[k] * c.decay);
         }

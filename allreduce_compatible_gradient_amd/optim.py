@@ -284,8 +284,8 @@ class AdamW(torch.optim.Optimizer):
     bits=8 keeps both moments in 8 bits, 2 + 1/64 bytes a parameter in place of
     8.  Of a block of 128 elements those whose gradients are below about 2^-17
     of the largest's then take steps that shrink with them, as with a larger
-    eps; those near to it take noisy ones, the largest about twice as long as
-    with 32-bit moments.  random rounds bf16 parameters at random (8-bit moments always are), so
+    eps; those near to it take noisy ones, the largest about 1.4 times as long
+    as with 32-bit moments.  random rounds bf16 parameters at random (8-bit moments always are), so
     that small updates count.  max_norm clips the gradients' norm over all
     parameters (``last_norm`` is that of the last step, on the device).
     Nothing waits for the device.

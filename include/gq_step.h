@@ -133,13 +133,13 @@ typedef struct gqs_adamw_args {
  *   p = p (1 - lr weight_decay)
  *       - lr m / (1 - beta1^step) / (sqrt(v / (1 - beta2^step)) + eps),
  * in fp32; the update takes the moments before their rounding.  With 8-bit
- * moments the first root is that of v + 2^(E - 19), or of v + 2^-126 where E <
- * -107, E the exponent of v's block as it came: half the block's lowest step.
- * Elements of gradients below about 2^-17 of their block's largest keep a v of
- * mostly 0 and an m that is 0 or a whole lowest step, whose quotient alone has
- * no bound (300 steps of normal gradients: up to 850 lr where 32-bit moments
- * take 1.3); with it their steps were at most 2.3 lr, and shrink with the
- * gradient, as with a larger eps.  Root and quotient are then good to a unit in
+ * moments the first root is that of v or, where that is more, of 2^(E - 18), E
+ * the exponent of v's block as it came: the block's lowest step.  Elements of
+ * gradients below about 2^-17 of their block's largest keep a v of mostly 0
+ * and an m that is 0 or a whole lowest step, whose quotient alone has no bound
+ * (300 steps of normal gradients: up to 850 lr where 32-bit moments take 1.3);
+ * so their steps were at most 1.8 lr, and shrink with the gradient, as with a
+ * larger eps.  Root and quotient are then good to a unit in
  * their last place.  A bf16 p is
  * rounded once, to nearest, or, with `random`, at random: the 16 bits below
  * its last place get the half of draw 2 added.  lr >= 0, 0 <= beta < 1, eps
