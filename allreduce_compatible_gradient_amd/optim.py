@@ -431,8 +431,10 @@ class AdamW(torch.optim.Optimizer):
     def _part_counts(self, group):
         """Gives those of a count's parameters that have no gradient now a
         count of their own where others have one."""
-        counts = {}
-        for p in group["params"]:
+        params, counts = group["params"], {}
+        if all(p.grad is not None for p in params):
+            return
+        for p in params:
             state = self.state.get(p)
             if state:
                 count = state.get("step", group.get("step"))
