@@ -141,8 +141,8 @@ __device__ __forceinline__ void store_random8(bf16 *p, int n, float (&v)[8], con
 //
 // One pass, bound by memory: 12 + 16 bytes an fp32 element with its 32-bit
 // moments, 6 + 16 a bf16 one, 6 + 4 with 8-bit moments.  33.6M fp32 elements
-// 165 us, 5.7 TB/s; 201M of bf16 862, 5.1; 33.6M of bf16 with 8-bit moments 68
-// us, 4.9, where about 650 vector instructions for eight elements, more than
+// 165 us, 5.7 TB/s; 201M of bf16 862, 5.1; 33.6M of bf16 with 8-bit moments 57
+// us, 5.9, 201M 394, 5.1, where about 650 vector instructions for eight elements, more than
 // half of them the three Philox calls, take nearly as long as the memory.  A
 // block of 128 of the 8-bit moments is in registers when its new power of two
 // is found, so neither is read twice.

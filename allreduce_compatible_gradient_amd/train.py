@@ -666,7 +666,8 @@ def linear(x, weight, bias=None, *, seed=None, fp8: bool = False):
     With fp8 the products for y and for x's gradient are those of e4m3 copies
     with a scale for each block of 128 (``fp8``), made of x, the weight and
     the gradient in each pass; the gradient's is rounded at random where a
-    seed is given."""
+    seed is given.  The weight's copy reads all of it: for few rows (64 by 1024
+    x 4096, say) a pass without gradients takes longer than the library's."""
     return _Linear.apply(x, weight, bias, seed, torch.is_grad_enabled(), bool(fp8))
 
 
@@ -794,8 +795,9 @@ class Mlp8(torch.nn.Module):
 
     fp8=True takes the products of up and down (and those for the gradients
     of their inputs) in e4m3 with a scale for each block of 128, as
-    ``linear(..., fp8=True)`` does.  Each pass makes its copies of the weights;
-    ``hold_fp8`` keeps them for the passes without gradients."""
+    ``linear(..., fp8=True)`` does.  Each pass makes its copies of the weights,
+    which costs more than it gains for few tokens; ``hold_fp8`` keeps them for
+    the passes without gradients."""
 
     fp8, _held, _holding, _handles = False, None, False, ()  # of a block pickled before them
 
