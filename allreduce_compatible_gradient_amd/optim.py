@@ -140,8 +140,9 @@ def gqs_adamw(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, betas=(0.9, 0.9
     lr may be device tensors (int64 and float32, one element), which a
     captured graph reads at every replay.  A `seed` is needed with Moment8; a
     bf16 parameter is rounded at random where one is given, unless `random` is
-    False, and to nearest otherwise.  Calls of one step with one seed share random numbers between
-    tensors of the same number in their lists: give each list its own.
+    False, and to nearest otherwise.  Calls of one step with one seed share
+    random numbers between tensors of the same number in their lists: give
+    each list its own.
 
     To autograd the params are changed in place, as by torch's own operations."""
     params, grads = list(params), list(grads)
@@ -285,10 +286,10 @@ class AdamW(torch.optim.Optimizer):
     8.  Of a block of 128 elements those whose gradients are below about 2^-17
     of the largest's then take steps that shrink with them, as with a larger
     eps; those near to it take noisy ones, the largest about 1.4 times as long
-    as with 32-bit moments.  random rounds bf16 parameters at random (8-bit moments always are), so
-    that small updates count.  max_norm clips the gradients' norm over all
-    parameters (``last_norm`` is that of the last step, on the device).
-    Nothing waits for the device.
+    as with 32-bit moments.  random rounds bf16 parameters at random (8-bit
+    moments always are), so that small updates count.  max_norm clips the
+    gradients' norm over all parameters (``last_norm`` is that of the last
+    step, on the device).  Nothing waits for the device.
 
     The random numbers come from `seed`, the step and the parameter's place: a
     process group's ranks, which step with equal gradients, stay equal while

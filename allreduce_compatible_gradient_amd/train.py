@@ -904,7 +904,8 @@ class Mlp8(torch.nn.Module):
         seed, bits = None, None
         if torch.is_grad_enabled():
             bits = 8
-            self._let_go()
+            if self._holding:
+                self._let_go()
             if self.random:
                 seed = self._pass_seed()
             self.passes += 1
